@@ -24,6 +24,9 @@
  *   (dir, mag) = W3 relu(W2 relu(W1 x + b1) + b2) + b3
  *   u = dir exp(mag exp_mult) step_mult;  p <- p - lr u - lr wd p
  *
+ * The operators behind the step (norms, embedding, distillation loss) produce
+ * the gradients it reads; they are declared at the end.
+ *
  * All arithmetic on the device is fp32.  Every call returns an lopt_status;
  * no C++ exception crosses this boundary.  lopt_last_error() gives a
  * thread-local message for the last failing call on the calling thread.
@@ -418,6 +421,120 @@ lopt_status lopt_get_tensor_stats(const lopt_handle* h, float* out, int32_t n);
  * valid while steps that record them are queued.  Errors: NULL handle, NULL
  * events with n > 0, other n -> INVALID_ARGUMENT. */
 lopt_status lopt_set_timing_events(lopt_handle* h, void* const* events, int32_t n);
+
+/* ---------------------------------------------------------------------------
+ * Operators that produce the gradients a step reads, for the tensor kinds of
+ * the parameter sets the PyLO page times ("Benchmark results": ViT-B/16 and
+ * GPT-2 training): a transformer's norms (1-D tensors), its token embedding
+ * (the largest matrix), and a distillation loss where a backward pass begins.
+ *
+ * They need no handle and keep nothing between calls.  Each call queues its
+ * kernels on `stream` of the current device and returns; it allocates nothing
+ * and waits for nothing, so it may be captured into a HIP graph.  A gradient
+ * of parameters goes to a caller's buffer, which can be the one that lopt_step
+ * reads, and is added to what is there if `accumulate` is not 0.
+ *
+ * Matrices have unit stride within a row and a row stride ld (in elements, at
+ * least the row's length).  Pointers must be aligned to their elements only.
+ * rows may be 0: then nothing is read, and a gradient of parameters is zero
+ * (unchanged if accumulated).  rows and cols must be below 2^31; rows * cols
+ * need not be.  A buffer that is written may not overlap any other of the
+ * call, except where said.  A workspace belongs to the caller and holds
+ * nothing between calls; two calls that may run at the same time need two.
+ * Sums and statistics are fp32 and in a fixed order: the same inputs give the
+ * same bits.  Every output is rounded once.
+ * Errors: LOPT_ERR_INVALID_ARGUMENT (a NULL pointer, a bad size, stride, type
+ * or hyperparameter, overlapping buffers), LOPT_ERR_UNSUPPORTED (a size over
+ * the limit, a misaligned pointer), LOPT_ERR_WORKSPACE, LOPT_ERR_HIP. */
+
+/* Element types. */
+typedef enum lopt_dtype { LOPT_F32 = 0, LOPT_BF16 = 1, LOPT_F16 = 2 } lopt_dtype;
+
+typedef enum lopt_norm_kind { LOPT_NORM_LAYER = 0, LOPT_NORM_RMS = 1 } lopt_norm_kind;
+
+/* Layer norm or RMS norm of every row of x (rows x cols):
+ *   mu = mean(x) (RMS: 0), rstd = (mean((x - mu)^2) + eps)^(-1/2),
+ *   y = (x - mu) rstd weight + bias.
+ * x, y: elements of type dtype.  weight, bias: cols elements of type w_dtype;
+ * NULL: 1 and 0.  mean, rstd: rows floats that lopt_norm_backward takes; NULL:
+ * not kept.  An RMS norm has neither bias nor mean (NULL).  eps: finite, >= 0;
+ * with 0, a row without spread gives NaN.  A NaN or an infinity spoils its own
+ * row only. */
+lopt_status lopt_norm_forward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t ldx,
+                              const void* weight, const void* bias, int32_t w_dtype, float eps, void* y, int64_t ldy,
+                              float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace that lopt_norm_backward needs to compute dweight or
+ * dbias.  Host only. */
+lopt_status lopt_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradients of lopt_norm_forward.  With xh = (x - mu) rstd and a = dy weight:
+ *   dx = rstd (a - xh mean(a xh) - mean(a))   (RMS: without mean(a)), per row,
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy.
+ * dy, x, dx: type dtype.  dweight, dbias: cols elements of type g_dtype.  Any of
+ * dx, dweight and dbias may be NULL: it is not computed.  mean, rstd: as
+ * lopt_norm_forward wrote them.  workspace: 256-byte aligned, of
+ * lopt_norm_backward_workspace() bytes; not needed without dweight and dbias. */
+lopt_status lopt_norm_backward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, const void* dy, int64_t lddy,
+                               const void* x, int64_t ldx, const void* weight, int32_t w_dtype, const float* mean,
+                               const float* rstd, void* dx, int64_t lddx, void* dweight, void* dbias, int32_t g_dtype,
+                               int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
+
+/* Embedding lookup: out[t] = scale * table[ids[t] - row0] for n_ids ids.
+ * table: rows x cols of type t_dtype, the rows [row0, row0 + rows) of the whole
+ * table (row0 = 0: all of it; a rank's rows of a sharded one otherwise, whose
+ * outputs add up over the ranks).  An id that names no row of it (padding, say
+ * -1, or a row of another shard) gives a row of zeros.  ids: id_bytes (4 or 8)
+ * bytes each, signed.  out: n_ids x cols of type o_dtype.  At most 2^27 ids;
+ * row0 within [0, 2^40]; scale finite. */
+lopt_status lopt_embedding_forward(int64_t n_ids, const void* ids, int32_t id_bytes, int64_t rows, int64_t cols, int64_t row0,
+                                   const void* table, int64_t ldt, int32_t t_dtype, float scale, void* out, int64_t ldo,
+                                   int32_t o_dtype, void* stream);
+
+/* Bytes of workspace that lopt_embedding_backward needs.  Host only. */
+lopt_status lopt_embedding_backward_workspace(int64_t n_ids, int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradient of lopt_embedding_forward:
+ *   dtable[v] = scale * sum over t with ids[t] - row0 = v of dout[t],
+ * summed in the order of t (the tokens are sorted by id).  dout: n_ids x cols
+ * of type d_dtype; dtable: rows x cols of type g_dtype.  Rows that no id names
+ * are set to zero, or left untouched if the gradient is accumulated.
+ * workspace: 256-byte aligned, of lopt_embedding_backward_workspace() bytes. */
+lopt_status lopt_embedding_backward(int64_t n_ids, const void* ids, int32_t id_bytes, const void* dout, int64_t ldd,
+                                    int32_t d_dtype, int64_t rows, int64_t cols, int64_t row0, float scale, void* dtable,
+                                    int64_t ldt, int32_t g_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
+#define LOPT_MAX_TOP 1024 /* entries of a teacher's list */
+
+/* Distillation from a teacher's top logits, per row: with the student's logits
+ * z (cols of them), the teacher's list of `top` ids i_k and logits u_k, and
+ * tau = temperature,
+ *   p_k = exp(u_k / tau) / sum_j exp(u_j / tau),  lse = log sum_v exp(z_v / tau),
+ *   loss = tau^2 sum_k p_k (log p_k - z_(i_k) / tau + lse):
+ * tau^2 times the Kullback-Leibler divergence of the student's distribution
+ * from the teacher's, which is renormalised over its list.
+ * logits: rows x cols of type dtype; ids: rows x top, id_bytes (4 or 8) bytes
+ * each, signed; teacher: rows x top of type u_dtype.  An entry whose id lies
+ * outside [0, cols) or whose logit is -inf is absent, whatever else it holds; an id
+ * that is listed twice counts with both entries.  A row without an entry has
+ * loss 0, whatever its logits are.  An entry whose p rounds to 0 adds nothing.
+ * loss, lse: rows floats, NULL: not written.  temperature: finite, > 0.  At
+ * most LOPT_MAX_TOP entries. */
+lopt_status lopt_distill_forward(int64_t rows, int64_t cols, int32_t dtype, const void* logits, int64_t ldz, int32_t top,
+                                 const void* ids, int64_t ldi, int32_t id_bytes, const void* teacher, int64_t ldu,
+                                 int32_t u_dtype, float temperature, float* loss, float* lse, void* stream);
+
+/* Gradient of lopt_distill_forward:
+ *   dlogits_v = dloss tau (exp(z_v / tau - lse) - sum over k with i_k = v of p_k),
+ * 0 for a row without an entry.  dloss: one float a row, dloss_stride apart (0:
+ * one value for all rows).  lse: as lopt_distill_forward wrote it.  dlogits:
+ * type dtype; it may be logits itself (with the same row stride), which it
+ * then replaces. */
+lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, const float* dloss, int64_t dloss_stride,
+                                  const void* logits, int64_t ldz, int32_t top, const void* ids, int64_t ldi,
+                                  int32_t id_bytes, const void* teacher, int64_t ldu, int32_t u_dtype, float temperature,
+                                  const float* lse, void* dlogits, int64_t lddz, void* stream);
 
 /* Message of the last failing call on this thread ("" if none). */
 const char* lopt_last_error(void);

@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "liblopt.so")
 # runs them, assume finite values in their ReLUs (-fno-honor-nans gives a
 # single v_max_f32 per ReLU).  The sources are compiled in parallel.
 SOURCES = [("lopt_kernels.hip", []), ("lopt_apply.hip", ["-fno-honor-nans"]),
-           ("lopt_single.hip", ["-fno-honor-nans"]), ("lopt_api.cpp", [])]
+           ("lopt_single.hip", ["-fno-honor-nans"]), ("lopt_api.cpp", []), ("lopt_norm_forward.hip", []),
+           ("lopt_norm_backward.hip", []), ("lopt_embedding.hip", []), ("lopt_distill.hip", []), ("lopt_ops_api.cpp", [])]
 ARCH = "gfx950"
 
 # Packed-fp32 VALU instructions are disabled for all device code.

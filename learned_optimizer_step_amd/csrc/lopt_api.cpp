@@ -20,45 +20,17 @@
 #include <vector>
 
 #include "../../include/lopt.h"
+#include "lopt_error.h"
 #include "lopt_internal.h"
 
 using namespace lopt;
 
+std::string& lopt::last_error() {
+  thread_local std::string message;
+  return message;
+}
+
 namespace {
-
-thread_local std::string g_last_error;
-
-struct ApiError {
-  lopt_status code;
-  std::string msg;
-};
-
-[[noreturn]] void fail(lopt_status code, const std::string& msg) { throw ApiError{code, msg}; }
-
-void hip_check(hipError_t e, const char* what) {
-  if (e != hipSuccess) fail(LOPT_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
-template <class F>
-lopt_status guarded(F&& f) {
-  try {
-    f();
-    g_last_error.clear();
-    return LOPT_OK;
-  } catch (const ApiError& e) {
-    g_last_error = e.msg;
-    return e.code;
-  } catch (const std::bad_alloc&) {
-    g_last_error = "host allocation failed";
-    return LOPT_ERR_HIP;
-  } catch (const std::exception& e) {
-    g_last_error = e.what();
-    return LOPT_ERR_HIP;
-  } catch (...) {
-    g_last_error = "unknown error";
-    return LOPT_ERR_HIP;
-  }
-}
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -1020,6 +992,6 @@ lopt_status lopt_set_timing_events(lopt_handle* h, void* const* events, int32_t 
   });
 }
 
-const char* lopt_last_error(void) { return g_last_error.c_str(); }
+const char* lopt_last_error(void) { return last_error().c_str(); }
 
 }  // extern "C"

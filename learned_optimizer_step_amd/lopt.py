@@ -40,6 +40,12 @@ LOPT_LAUNCH_SINGLE = 2   # one kernel per step (the five passes behind grid-wide
 LOPT_MAX_TIME = 11
 LOPT_N_FEATURES = 28     # small_fc_lopt's per-element features
 LOPT_VELO_FEATURES = 19  # the VeLO-shaped variant's (features 0..18)
+LOPT_F32 = 0             # element types of the norm, embedding and distillation calls
+LOPT_BF16 = 1
+LOPT_F16 = 2
+LOPT_NORM_LAYER = 0
+LOPT_NORM_RMS = 1
+LOPT_MAX_TOP = 1024      # entries of a teacher's list
 
 
 class LoptError(RuntimeError):
@@ -80,6 +86,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         pass
     lib = ctypes.CDLL(p)
     st = ctypes.c_int
+    i32, i64, f32, ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
     sig = {
         "lopt_default_config": (st, [ctypes.POINTER(lopt_config)]),
         "lopt_mlp_floats": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -108,6 +115,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "lopt_get_launch": (st, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]),
         "lopt_set_tensor_hyper": (st, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]),
         "lopt_get_tensor_stats": (st, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]),
+        "lopt_norm_forward": (st, [i32, i64, i64, i32, ptr, i64, ptr, ptr, i32, f32, ptr, i64, ptr, ptr, ptr]),
+        "lopt_norm_backward_workspace": (st, [i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
+        "lopt_norm_backward": (st, [i32, i64, i64, i32, ptr, i64, ptr, i64, ptr, i32, ptr, ptr, ptr, i64, ptr, ptr, i32,
+                                    i32, ptr, ctypes.c_size_t, ptr]),
+        "lopt_embedding_forward": (st, [i64, ptr, i32, i64, i64, i64, ptr, i64, i32, f32, ptr, i64, i32, ptr]),
+        "lopt_embedding_backward_workspace": (st, [i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
+        "lopt_embedding_backward": (st, [i64, ptr, i32, ptr, i64, i32, i64, i64, i64, f32, ptr, i64, i32, i32, ptr,
+                                         ctypes.c_size_t, ptr]),
+        "lopt_distill_forward": (st, [i64, i64, i32, ptr, i64, i32, ptr, i64, i32, ptr, i64, i32, f32, ptr, ptr, ptr]),
+        "lopt_distill_backward": (st, [i64, i64, i32, ptr, i64, ptr, i64, i32, ptr, i64, i32, ptr, i64, i32, f32, ptr,
+                                       ptr, i64, ptr]),
         "lopt_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -282,6 +300,46 @@ def lopt_set_timing_events(h, events: Sequence[int]) -> None:
     """events: LOPT_N_KERNELS + 1 raw hipEvent_t handles (ints), or [] to stop."""
     arr = (ctypes.c_void_p * max(1, len(events)))(*events)
     _check(load_library().lopt_set_timing_events(h, arr, len(events)))
+
+
+# The norm, embedding and distillation calls take the arguments of
+# include/lopt.h in their order, with device addresses as integers (None: NULL).
+# learned_optimizer_step_amd.layers makes them from torch tensors.
+
+def lopt_norm_forward(*args) -> None:
+    _check(load_library().lopt_norm_forward(*args))
+
+
+def lopt_norm_backward_workspace(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().lopt_norm_backward_workspace(rows, cols, ctypes.byref(out)))
+    return int(out.value)
+
+
+def lopt_norm_backward(*args) -> None:
+    _check(load_library().lopt_norm_backward(*args))
+
+
+def lopt_embedding_forward(*args) -> None:
+    _check(load_library().lopt_embedding_forward(*args))
+
+
+def lopt_embedding_backward_workspace(n_ids: int, rows: int, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load_library().lopt_embedding_backward_workspace(n_ids, rows, cols, ctypes.byref(out)))
+    return int(out.value)
+
+
+def lopt_embedding_backward(*args) -> None:
+    _check(load_library().lopt_embedding_backward(*args))
+
+
+def lopt_distill_forward(*args) -> None:
+    _check(load_library().lopt_distill_forward(*args))
+
+
+def lopt_distill_backward(*args) -> None:
+    _check(load_library().lopt_distill_backward(*args))
 
 
 def config_from(**overrides) -> lopt_config:

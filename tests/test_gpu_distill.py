@@ -1,0 +1,234 @@
+"""The distillation loss on the GPU against its definition in 64 bits."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("no GPU", allow_module_level=True)
+
+from learned_optimizer_step_amd import layers  # noqa: E402
+from learned_optimizer_step_amd import lopt as L  # noqa: E402
+from ops_cases import TINY, TYPES, U, close, distill, rounding  # noqa: E402
+
+# (rows, vocabulary, entries, temperature)
+SHAPES = [(1, 1, 1, 1.0), (1, 2, 2, 2.0), (3, 7, 3, 0.5), (5, 64, 1, 1.0), (4, 513, 20, 2.0), (300, 1000, 8, 2.0),
+          (2, 1001, 300, 1.0), (7, 4097, 33, 4.0), (2, 8191, 65, 0.7), (3, 8192, 1024, 1.0), (2, 50257, 32, 2.0),
+          (1, 130001, 100, 1.0), (600, 300, 5, 3.0)]
+
+
+def make(rows, cols, top, t, ut, idt, seed, absent=0.2):
+    g = torch.Generator().manual_seed(seed)
+    z = 3 * torch.randn(rows, cols, generator=g)
+    u, ids = torch.topk(z + torch.randn(rows, cols, generator=g), top, dim=1)
+    u, z = u.to(ut), z.to(t)
+    gone = torch.rand(rows, top, generator=g) < absent
+    ids[gone] = torch.tensor([-1, -9, cols, cols + 77])[torch.randint(0, 4, (int(gone.sum()),), generator=g)]
+    if rows > 2:
+        ids[1] = -1
+    return z, ids.to(idt), u, torch.randn(rows, generator=g) * 0.3
+
+
+def tols(z, loss, lse, qp, q, dense, size, terms, tau, t):
+    """Each exponent is off by a few U of its size (a product, a sum and the rounding of 1 / tau), the sum of the softmax by
+    its additions (vocabulary / 4096 in a thread, 16, 6 and 8 over it, the wave and the block) and by U per exponential."""
+    add = z.shape[1] // 4096 + 16 + 40
+    e = (8 * size + add) * U
+    # every term of the loss: its three parts' roundings, and p's own, of the size of its exponent
+    return tau * tau * (e + 16 * U * size + 16 * U * size * terms) + TINY[torch.float32], e
+
+
+def check(z, ids, u, dl, tau, what):
+    t = z.dtype
+    loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+    dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)
+    tau32 = torch.tensor(tau, dtype=torch.float32).double().item()
+    want = distill(z, ids, u, tau32)
+    tl, e = tols(z, *want, tau32, t)
+    close(lse, want[1], e, f"{what} lse")
+    close(loss, want[0], tl, f"{what} loss")
+    # the gradient with the lse as the forward pass kept it
+    _, _, qp, q, dense, size, _ = distill(z, ids, u, tau32, lse.cpu())
+    g = (dl.double() * tau32)[:, None]
+    tol = g.abs() * U * (8 * size[:, None] * q + (16 * size[:, None] + ids.shape[1]) * dense)
+    close(dz, qp * g, rounding(qp * g, t) + tol + g.abs() * 2.0 ** -125, f"{what} dz")
+    return loss, lse, dz
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+@pytest.mark.parametrize("rows,cols,top,tau", SHAPES)
+def test_against_the_definition(rows, cols, top, tau, t):
+    for ut, idt, absent in ((torch.float32, torch.int64, 0.2), (t, torch.int32, 0.0)):
+        z, ids, u, dl = make(rows, cols, top, t, ut, idt, rows + cols, absent)
+        check(z, ids, u, dl, tau, f"{rows}x{cols} top {top}")
+
+
+def test_rows_without_entries_and_absent_ones_whatever_they_hold():
+    z, ids, u, dl = make(12, 900, 10, torch.float32, torch.float32, torch.int64, 3, absent=0.3)
+    loss, lse, dz = check(z, ids, u, dl, 2.0, "plain")
+    u2 = u.clone()
+    u2[(ids < 0) | (ids >= 900)] = torch.tensor([math.nan, math.inf, -math.inf, 3e38]).repeat(60)[:int(((ids < 0) | (ids >= 900)).sum())]
+    again = check(z, ids, u2, dl, 2.0, "absent")
+    assert all(torch.equal(a, b) for a, b in zip((loss, lse, dz), again))
+    # entries of -inf are absent, in part or all of a row's
+    u3 = u.clone()
+    u3[3, ::2] = -math.inf
+    u3[4] = -math.inf
+    loss, _, dz = check(z, ids, u3, dl, 2.0, "-inf")
+    assert loss[4] == 0 and not dz[4].any() and loss[1] == 0 and not dz[1].any()
+    # a row without entries has no loss whatever its logits and its share of the gradient are
+    z4 = z.clone()
+    z4[1, 5], z4[4, 7] = math.nan, math.inf
+    loss, lse, dz = (v.cpu() for v in (*layers.distill_forward(z4.cuda(), ids.cuda(), u3.cuda(), 2.0),
+                                       layers.distill_backward(dl.cuda(), z4.cuda(), ids.cuda(), u3.cuda(), lse, 2.0)))
+    assert loss[1] == 0 and loss[4] == 0 and not dz[1].any() and not dz[4].any()
+    assert torch.isnan(lse[1])
+
+
+def test_an_id_that_is_listed_twice():
+    z, ids, u, dl = make(6, 500, 12, torch.float32, torch.float32, torch.int64, 5, absent=0.0)
+    ids[:, 5] = ids[:, 0]
+    ids[:, 11] = ids[:, 0]
+    ids[2] = 7                      # every entry the same
+    _, _, dz = check(z, ids, u, dl, 1.0, "twice")
+    assert torch.equal(dz, check(z, ids, u, dl, 1.0, "again")[2])
+    z, ids, u, dl = make(2, 30000, 1024, torch.bfloat16, torch.float32, torch.int32, 6, absent=0.0)
+    ids[:, 500:] = ids[:, :524]
+    check(z, ids, u, dl, 1.0, "half of the list twice")
+
+
+def test_masked_logits():
+    """A vocabulary masked with -inf, or with the type's lowest value; NaN and +inf spoil their own row."""
+    for t in TYPES:
+        z, ids, u, dl = make(8, 3000, 16, t, torch.float32, torch.int64, 7, absent=0.0)
+        keep = torch.zeros_like(z, dtype=torch.bool).scatter_(1, ids.clamp(min=0), True)
+        for low in (-math.inf, torch.finfo(t).min):
+            m = torch.where(keep | (torch.arange(3000) % 3 == 0), z, torch.tensor(low).to(t))
+            check(m, ids, u, dl, 2.0, f"{t} {low}")
+        m = torch.where(keep & (torch.arange(3000) != ids[0, 0]), z, torch.tensor(-math.inf).to(t))
+        loss, lse = layers.distill_forward(m.cuda(), ids.cuda(), u.cuda(), 1.0)
+        assert loss[0] == math.inf       # the teacher wants what the student excludes
+        assert torch.isfinite(lse).all()
+        dz = layers.distill_backward(dl.cuda(), m.cuda(), ids.cuda(), u.cuda(), lse, 1.0)
+        assert torch.isfinite(dz).all()
+        m = z.clone()
+        m[3, 9], m[5, 2500], m[6] = math.nan, math.inf, -math.inf
+        loss, lse = layers.distill_forward(m.cuda(), ids.cuda(), u.cuda(), 1.0)
+        good = [r not in (3, 5, 6) for r in range(8)]
+        assert torch.isfinite(loss).tolist() == good and torch.isnan(lse[3]) and lse[6] == -math.inf
+        dz = layers.distill_backward(dl.cuda(), m.cuda(), ids.cuda(), u.cuda(), lse, 1.0)
+        assert torch.isfinite(dz).all(1).tolist() == good
+
+
+def test_peaked_and_far_logits():
+    z, ids, u, dl = make(6, 2000, 20, torch.float32, torch.float32, torch.int64, 9, absent=0.0)
+    check(z * 200, ids, u * 200, dl, 1.0, "peaked")
+    check(z + 1e4, ids, u - 1e4, dl, 1.0, "far")
+    check(z, ids, u, dl, 1e-3, "cold")
+    check(z, ids, u, dl, 1e3, "hot")
+
+
+def test_strides_in_place_and_what_lies_around():
+    rows, cols, top, ld = 21, 777, 9, 801
+    for t in TYPES:
+        z, ids, u, dl = make(rows, cols, top, t, torch.float32, torch.int64, 10)
+        loss, lse, dz = check(z, ids, u, dl, 2.0, "plain")
+        big = torch.full((rows + 1, ld), 9.0, dtype=t, device="cuda")
+        big[:rows, 4:4 + cols] = z.cuda()
+        wide_i, wide_u = torch.full((rows, 15), 3).cuda(), torch.zeros(rows, 13).cuda()
+        wide_i[:, 2:2 + top], wide_u[:, 1:1 + top] = ids.cuda(), u.cuda()
+        zs, is_, us = big[:rows, 4:4 + cols], wide_i[:, 2:2 + top], wide_u[:, 1:1 + top]
+        l2, s2 = layers.distill_forward(zs, is_, us, 2.0)
+        # other addresses, other vectors: the sums may be taken in another order
+        assert torch.allclose(loss, l2, rtol=1e-4, atol=1e-5) and torch.allclose(lse, s2, rtol=1e-6)
+        stream, code = torch.cuda.current_stream().cuda_stream, layers._DTYPES[t]
+        g = dl.cuda()
+        at = big.data_ptr() + 4 * big.element_size()
+        L.lopt_distill_backward(rows, cols, code, g.data_ptr(), 1, at, ld, top, is_.data_ptr(), 15, 8, us.data_ptr(), 13, 0, 2.0,
+                                lse.data_ptr(), at, ld, stream)      # over the logits
+        assert torch.equal(big[:rows, 4:4 + cols], dz)
+        big[:rows, 4:4 + cols] = 9.0
+        assert bool((big == 9.0).all())
+        buf = z.cuda()
+        assert layers.distill_backward(g, buf, ids.cuda(), u.cuda(), lse, 2.0, out=buf) is buf and torch.equal(buf, dz)
+
+
+def test_one_weight_for_all_rows_and_autograd():
+    z, ids, u, _ = make(24, 600, 10, torch.float32, torch.float32, torch.int64, 11)
+    z3, i3, u3 = z.view(4, 6, 600).cuda().requires_grad_(True), ids.view(4, 6, 10).cuda(), u.view(4, 6, 10).cuda()
+    loss = layers.distill_loss(z3, i3, u3, 2.0)
+    assert loss.shape == (4, 6)
+    grad, = torch.autograd.grad(loss.mean(), z3)      # one value for all rows, expanded
+    _, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), 2.0)
+    want = layers.distill_backward(torch.full((24,), 1 / 24).cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, 2.0)
+    assert torch.equal(grad.view(24, 600), want)
+    # central differences of the definition in 64 bits
+    d = torch.randn(24, 600, generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+    h = 1e-4
+    diff = (distill(z.double() + h * d, ids, u, 2.0)[0] - distill(z.double() - h * d, ids, u, 2.0)[0]).mean() / (2 * h)
+    got = (grad.view(24, 600).double().cpu() * d).sum()
+    assert abs(got - diff) <= 1e-6 * abs(diff) + 200 * U * (grad.view(24, 600).double().cpu() * d).abs().sum() + 1e-8
+
+
+def test_on_another_stream_and_in_a_graph():
+    z, ids, u, dl = make(50, 5000, 12, torch.bfloat16, torch.float32, torch.int64, 13)
+    z, ids, u, dl = z.cuda(), ids.cuda(), u.cuda(), dl.cuda()
+    loss, lse = layers.distill_forward(z, ids, u, 2.0)
+    dz = layers.distill_backward(dl, z, ids, u, lse, 2.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        l2, s2 = layers.distill_forward(z, ids, u, 2.0)
+        d2 = layers.distill_backward(dl, z, ids, u, s2, 2.0)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(loss, l2) and torch.equal(lse, s2) and torch.equal(dz, d2)
+    zs = z.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        l3, s3 = layers.distill_forward(zs, ids, u, 2.0)
+        d3 = layers.distill_backward(dl, zs, ids, u, s3, 2.0)
+    for k in range(4):
+        zs.copy_(z * (k + 1))
+        le, se = layers.distill_forward(zs, ids, u, 2.0)
+        de = layers.distill_backward(dl, zs, ids, u, se, 2.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(le, l3) and torch.equal(se, s3) and torch.equal(de, d3), k
+
+
+def test_no_rows_and_more_elements_than_32_bits_count():
+    e = torch.empty(0, 30, device="cuda")
+    i, u = torch.empty(0, 4, dtype=torch.int64, device="cuda"), torch.empty(0, 4, device="cuda")
+    loss, lse = layers.distill_forward(e, i, u)
+    assert loss.shape == (0,) and layers.distill_backward(loss, e, i, u, lse).shape == (0, 30)
+    rows, cols = 33000, 65537           # 2^31 + 15 M elements
+    z = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    z[-3:] = torch.randn(3, cols, device="cuda")
+    ids = torch.randint(0, cols, (rows, 6), device="cuda")
+    u = torch.randn(rows, 6, device="cuda")
+    loss, lse = layers.distill_forward(z, ids, u)
+    part = layers.distill_forward(z[-3:].clone(), ids[-3:], u[-3:])
+    assert torch.equal(loss[-3:], part[0]) and torch.equal(lse[-3:], part[1])
+    assert bool(((lse[:-3] - math.log(cols)).abs() <= 60 * U * 12).all())
+    g = torch.ones(rows, device="cuda")
+    want = layers.distill_backward(g[-3:], z[-3:].clone(), ids[-3:], u[-3:], lse[-3:])
+    layers.distill_backward(g, z, ids, u, lse, out=z)
+    assert torch.equal(z[-3:], want)
+
+
+def test_refusals_of_the_tensors():
+    z, i, u = torch.ones(3, 8, device="cuda"), torch.zeros(3, 2, dtype=torch.int64, device="cuda"), torch.ones(3, 2, device="cuda")
+    loss, lse = layers.distill_forward(z, i, u)
+    for call in (lambda: layers.distill_loss(z, i, u[:, :1]), lambda: layers.distill_loss(z, i[:2], u[:2]),
+                 lambda: layers.distill_loss(z, i.float(), u), lambda: layers.distill_loss(z, i.cpu(), u),
+                 lambda: layers.distill_loss(z.double(), i, u), lambda: layers.distill_backward(loss.half(), z, i, u, lse),
+                 lambda: layers.distill_backward(loss, z, i, u, lse[:2]),
+                 lambda: layers.distill_backward(loss, z, i, u, lse, out=z.half())):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: layers.distill_loss(z, i, u, 0.0), lambda: layers.distill_loss(z, i, u, float("nan")),
+                 lambda: layers.distill_loss(z, i.repeat(1, 600), u.repeat(1, 600))):
+        with pytest.raises(L.LoptError):
+            call()
