@@ -1,4 +1,5 @@
-"""Builds liblopt.so (HIP kernels + C ABI) for gfx950 in-tree.
+"""Builds liblopt.so (HIP kernels + C ABI) for gfx950 in-tree, and _layers.so
+(the torch calls of the norms, embedding and distillation loss) over it.
 
     python -m learned_optimizer_step_amd.build
 """
@@ -56,15 +57,50 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
                      *[f"-D{d}" for d in defines],
                      os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
-    with concurrent.futures.ThreadPoolExecutor(len(cmds)) as ex:
-        for f in [ex.submit(_run, cmd, verbose) for cmd in cmds]:
+    with concurrent.futures.ThreadPoolExecutor(len(cmds) + 1) as ex:
+        jobs = [ex.submit(_run, cmd, verbose) for cmd in cmds]
+        if out == LIB:
+            jobs.append(ex.submit(_compile_layers, verbose))
+        for f in jobs:
             f.result()
     out_tmp = out + ".tmp"
     _run([hipcc(), "-shared", "-fPIC", *objs, "-o", out_tmp], verbose)
     os.replace(out_tmp, out)
     if out == LIB:
+        _link_layers(verbose)
+        os.replace(_layers_object() + ".so", LAYERS)
         build_microbench(verbose)
     return out
+
+
+LAYERS = os.path.join(PKG, "_layers.so")
+
+
+def _layers_object() -> str:
+    return os.path.join(PKG, "_build", "layers")
+
+
+def _compile_layers(verbose: bool) -> None:
+    """csrc/layers.cpp for the host, against the installed torch."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    obj = _layers_object() + ".o"
+    inc = [f for d in cpp_extension.include_paths() for f in ("-isystem", d)]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-c", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+          "-DTORCH_EXTENSION_NAME=_layers", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+          "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
+          os.path.join(CSRC, "layers.cpp"), "-o", obj], verbose)
+
+
+def _link_layers(verbose: bool) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    # liblopt.so is found beside _layers.so
+    _run([cxx, "-shared", _layers_object() + ".o", "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_hip",
+          "-L", PKG, "-llopt", "-Wl,-rpath,$ORIGIN", "-o", _layers_object() + ".so"], verbose)
 
 
 MICROBENCH = os.path.join(PKG, "lopt_microbench")

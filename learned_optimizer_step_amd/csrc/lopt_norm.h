@@ -38,6 +38,37 @@ auto with_layout(int64_t n, F&& f) {
   return f(RowLayout<16, 1024, 1024>());
 }
 
+// The thread's elements of a vector of n weights; `fill` where there is none.
+// The type is branched on once, around loads that do not wait for each other.
+template <class L, int V, class W>
+__device__ __forceinline__ void load_weights_as(const void* p, int lane, int n, float fill, float (&w)[L::E]) {
+#pragma unroll
+  for (int k = 0; k < L::E / V; ++k) {
+    const int c = (k * L::TPR + lane) * V;
+    if (c + V <= n) {
+      const Pack<W, V> v = *reinterpret_cast<const Pack<W, V>*>(static_cast<const W*>(p) + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[k * V + i] = to_f32(v.v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[k * V + i] = c + i < n ? to_f32(static_cast<const W*>(p)[c + i]) : fill;
+    }
+  }
+}
+template <class L, int V>
+__device__ __forceinline__ void load_weights(const void* p, int dtype, int lane, int n, float fill, float (&w)[L::E]) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < L::E; ++e) w[e] = fill;
+  } else if (dtype == kF32) {
+    load_weights_as<L, V, float>(p, lane, n, fill, w);
+  } else if (dtype == kBF16) {
+    load_weights_as<L, V, bf16>(p, lane, n, fill, w);
+  } else {
+    load_weights_as<L, V, f16>(p, lane, n, fill, w);
+  }
+}
+
 // Sums over the TPR threads of a row.  Across waves the sums go through LDS;
 // `turn` alternates two buffers, so one barrier a call is enough (a wave that
 // writes a buffer again has passed the barrier of the call between).

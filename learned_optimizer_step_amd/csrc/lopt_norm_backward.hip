@@ -25,15 +25,12 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
   const float inv_n = 1.f / float(n);
 
   float w[E], dw[E], db[RMS ? 1 : E];
+  load_weights<L, V>(a.w, a.wdtype, lane, n, 1.f, w);
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (k * L::TPR + lane) * V + i;
-      w[k * V + i] = (a.w && c < n) ? load_any(a.w, a.wdtype, c) : 1.f;
-      dw[k * V + i] = 0.f;
-      if (!RMS) db[k * V + i] = 0.f;
-    }
+  for (int e = 0; e < E; ++e) {
+    dw[e] = 0.f;
+    if (!RMS) db[e] = 0.f;
+  }
 
   const int64_t stride = int64_t(gridDim.x) * L::ROWS;
   for (int64_t r0 = int64_t(blockIdx.x) * L::ROWS; r0 < a.rows; r0 += stride) {

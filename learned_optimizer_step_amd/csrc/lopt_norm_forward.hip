@@ -38,14 +38,8 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
 
   // the weights stay in registers for all rows of the thread
   float w[L::E], b[L::E];
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (k * L::TPR + lane) * V + i;
-      w[k * V + i] = (a.w && c < n) ? load_any(a.w, a.wdtype, c) : 1.f;
-      b[k * V + i] = (a.b && c < n) ? load_any(a.b, a.wdtype, c) : 0.f;
-    }
+  load_weights<L, V>(a.w, a.wdtype, lane, n, 1.f, w);
+  load_weights<L, V>(a.b, a.wdtype, lane, n, 0.f, b);
 
   const int64_t stride = int64_t(gridDim.x) * L::ROWS;
   // every thread of a block makes the same number of rounds (barriers inside)

@@ -307,39 +307,39 @@ def lopt_set_timing_events(h, events: Sequence[int]) -> None:
 # learned_optimizer_step_amd.layers makes them from torch tensors.
 
 def lopt_norm_forward(*args) -> None:
-    _check(load_library().lopt_norm_forward(*args))
+    _check((_lib or load_library()).lopt_norm_forward(*args))
 
 
 def lopt_norm_backward_workspace(rows: int, cols: int) -> int:
     out = ctypes.c_size_t()
-    _check(load_library().lopt_norm_backward_workspace(rows, cols, ctypes.byref(out)))
-    return int(out.value)
+    _check((_lib or load_library()).lopt_norm_backward_workspace(rows, cols, ctypes.byref(out)))
+    return out.value
 
 
 def lopt_norm_backward(*args) -> None:
-    _check(load_library().lopt_norm_backward(*args))
+    _check((_lib or load_library()).lopt_norm_backward(*args))
 
 
 def lopt_embedding_forward(*args) -> None:
-    _check(load_library().lopt_embedding_forward(*args))
+    _check((_lib or load_library()).lopt_embedding_forward(*args))
 
 
 def lopt_embedding_backward_workspace(n_ids: int, rows: int, cols: int) -> int:
     out = ctypes.c_size_t()
-    _check(load_library().lopt_embedding_backward_workspace(n_ids, rows, cols, ctypes.byref(out)))
-    return int(out.value)
+    _check((_lib or load_library()).lopt_embedding_backward_workspace(n_ids, rows, cols, ctypes.byref(out)))
+    return out.value
 
 
 def lopt_embedding_backward(*args) -> None:
-    _check(load_library().lopt_embedding_backward(*args))
+    _check((_lib or load_library()).lopt_embedding_backward(*args))
 
 
 def lopt_distill_forward(*args) -> None:
-    _check(load_library().lopt_distill_forward(*args))
+    _check((_lib or load_library()).lopt_distill_forward(*args))
 
 
 def lopt_distill_backward(*args) -> None:
-    _check(load_library().lopt_distill_backward(*args))
+    _check((_lib or load_library()).lopt_distill_backward(*args))
 
 
 def config_from(**overrides) -> lopt_config:

@@ -10,6 +10,7 @@ import torch
 
 U = 2.0 ** -24
 TYPES = [torch.float32, torch.bfloat16, torch.float16]
+CODE = {t: k for k, t in enumerate(TYPES)}   # lopt_dtype
 TINY = {torch.float32: 2.0 ** -126, torch.bfloat16: 2.0 ** -126, torch.float16: 2.0 ** -24}
 
 

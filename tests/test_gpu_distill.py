@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import TINY, TYPES, U, close, distill, rounding  # noqa: E402
+from ops_cases import CODE, TINY, TYPES, U, close, distill, rounding  # noqa: E402
 
 # (rows, vocabulary, entries, temperature)
 SHAPES = [(1, 1, 1, 1.0), (1, 2, 2, 2.0), (3, 7, 3, 0.5), (5, 64, 1, 1.0), (4, 513, 20, 2.0), (300, 1000, 8, 2.0),
@@ -143,7 +143,7 @@ def test_strides_in_place_and_what_lies_around():
         l2, s2 = layers.distill_forward(zs, is_, us, 2.0)
         # other addresses, other vectors: the sums may be taken in another order
         assert torch.allclose(loss, l2, rtol=1e-4, atol=1e-5) and torch.allclose(lse, s2, rtol=1e-6)
-        stream, code = torch.cuda.current_stream().cuda_stream, layers._DTYPES[t]
+        stream, code = torch.cuda.current_stream().cuda_stream, CODE[t]
         g = dl.cuda()
         at = big.data_ptr() + 4 * big.element_size()
         L.lopt_distill_backward(rows, cols, code, g.data_ptr(), 1, at, ld, top, is_.data_ptr(), 15, 8, us.data_ptr(), 13, 0, 2.0,

@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import TYPES, U, close, rounding  # noqa: E402
+from ops_cases import CODE, TYPES, U, close, rounding  # noqa: E402
 
 # (tokens, rows, columns): the sort's passes (rows below and from 256, 65536), its tiles of 4096 tokens, chunks that end
 # inside runs, widths around the slabs of 64 vectors
@@ -130,7 +130,7 @@ def test_strides_and_what_lies_around():
         out = torch.full((rows + 1, ld), 3.0, dtype=t, device="cuda")
         nb = L.lopt_embedding_backward_workspace(n, rows, cols)
         ws = torch.full((nb + 256,), 171, dtype=torch.uint8, device="cuda")   # what was in it does not matter
-        code = layers._DTYPES[t]
+        code = CODE[t]
         L.lopt_embedding_backward(n, ids.data_ptr(), 8, d.data_ptr(), ld, code, rows, cols, 0, 1.5,
                                   out.data_ptr() + 2 * out.element_size(), ld, code, 0, ws.data_ptr(), nb,
                                   torch.cuda.current_stream().cuda_stream)

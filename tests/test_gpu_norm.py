@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import (TYPES, U, close, norm_backward, norm_forward, norm_forward_tols, rounding,  # noqa: E402
+from ops_cases import (CODE, TYPES, U, close, norm_backward, norm_forward, norm_forward_tols, rounding,  # noqa: E402
                        row_depth)
 
 # one row to thousands; every row layout with its first and last width, widths that no vector divides, and rows too long
@@ -128,7 +128,7 @@ def test_strided_rows_and_rows_behind_the_last():
         assert all(torch.equal(p, q) for p, q in zip(want, got))
         outs = [torch.full((rows + 2, ld), 7.0, dtype=t, device="cuda") for _ in range(2)]
         stream = torch.cuda.current_stream().cuda_stream
-        code, size = layers._DTYPES[t], outs[0].element_size()
+        code, size = CODE[t], outs[0].element_size()
         L.lopt_norm_forward(0, rows, cols, code, x.data_ptr(), ld, w.data_ptr(), b.data_ptr(), 0, 1e-5,
                             outs[0].data_ptr() + 5 * size, ld, None, None, stream)
         L.lopt_norm_backward(0, rows, cols, code, dy.data_ptr(), ld, x.data_ptr(), ld, w.data_ptr(), 0, mean0.data_ptr(),
@@ -194,6 +194,15 @@ def test_autograd_and_differences(rms):
         # differences: h^2 of the third derivative (about the value's size here), and 2^-52 / h; the gradient: its roundings
         tol = 1e-6 * abs(want) + 100 * U * (grad.double().cpu() * d).abs().sum() + 1e-7 * (1 + dy.double().abs().sum())
         assert abs(got - want) <= tol, (k, got, want)
+
+
+def test_gradients_cannot_be_differentiated():
+    x, dy, w, b = gpu(*make(5, 64, torch.float32, torch.float32, 4))
+    x.requires_grad_(True)
+    grad, = torch.autograd.grad(layers.layer_norm(x, w, b), x, dy, create_graph=True)
+    assert torch.equal(grad, torch.autograd.grad(layers.layer_norm(x, w, b), x, dy)[0])
+    with pytest.raises(RuntimeError, match="cannot be differentiated"):
+        torch.autograd.grad(grad.sum(), x)
 
 
 def test_gradients_that_come_expanded():

@@ -5,7 +5,6 @@ import ctypes
 import pytest
 import torch
 
-from learned_optimizer_step_amd import layers
 from learned_optimizer_step_amd import lopt as L
 
 A = [(k + 1) << 40 for k in range(12)]   # addresses far apart, 256-byte aligned
@@ -124,7 +123,8 @@ def test_in_place_gradient_of_logits_is_not_an_overlap(lib):
     assert "lse is NULL" in str(e.value)
 
 
-def test_layers_have_no_cpu_path():
+def test_layers_have_no_cpu_path(lib):
+    from learned_optimizer_step_amd import layers
     x, ids = torch.ones(3, 8), torch.zeros(3, dtype=torch.int64)
     for call in (lambda: layers.layer_norm(x), lambda: layers.rms_norm(x), lambda: layers.embedding(ids, x),
                  lambda: layers.embedding_backward(x, ids, 4), lambda: layers.distill_loss(x, ids[:, None], x[:, :1]),
