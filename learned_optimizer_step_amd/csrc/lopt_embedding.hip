@@ -14,11 +14,19 @@
 namespace lopt {
 namespace {
 
-constexpr int kTile = 4096;       // tokens a block of the sort takes at a time
-constexpr int kMaxTiles = 256;    // blocks of the sort
+// The sort.  A list of up to kOneBlock tokens is sorted by one block in LDS in
+// one launch (4096 tokens: 9.5 us; as two launches a pass 15 and their gaps;
+// 16384: 31 against 19).
 constexpr int kSortBlock = 1024;
-constexpr int kPerWave = kTile / (kSortBlock / 64);   // tokens of a wave, in 64s
+constexpr int64_t kOneBlock = 8192;
+constexpr int kTile = 1024;       // tokens a block of a longer sort takes at a time (4096: twice the time a pass)
+constexpr int kMaxTiles = 256;    // blocks of the sort
 constexpr int kDigits = 256;      // 8 bits a pass
+
+// The sums: see k_embedding_sum.
+constexpr int kSumVec = 4;        // columns of a lane
+constexpr int kSumAhead = 8;      // tokens loaded at a time, while those before them are added up
+constexpr int kReach = 8;         // tokens that a chunk takes from the next one to end a run
 
 // Row of the table that an id names, `rows` if none.
 __device__ __forceinline__ uint32_t row_of(const void* ids, int id_bytes, int64_t t, int64_t row0, int64_t rows) {
@@ -70,11 +78,13 @@ __global__ __launch_bounds__(256) void k_embedding_forward(EmbeddingForward a) {
 struct Work {
   uint32_t *key[2], *val[2];   // tokens' rows and positions, by turns
   uint32_t* hist;              // [tiles][256] digits of a pass
-  unsigned char* touched;      // per row: some token names it
+  unsigned char* touched;      // long lists: rows that some token names
+  uint32_t* crossing;          // number of runs that cross a chunk's border, then the chunks they begin in
   float* part;                 // [chunks][2][cols]: sums of runs that cross a chunk's first / last token
   int64_t tiles, rounds, chunks;
   int32_t chunk;               // tokens of a chunk
   int32_t passes;
+  int32_t sorted;              // which key and val hold the sorted tokens
   size_t bytes;
 };
 
@@ -85,10 +95,15 @@ Work layout(unsigned char* ws, int64_t n, int64_t rows, int64_t cols) {
   const int64_t tiles = (n + kTile - 1) / kTile;
   w.rounds = std::max<int64_t>(1, (tiles + kMaxTiles - 1) / kMaxTiles);
   w.tiles = std::max<int64_t>(1, (tiles + w.rounds - 1) / w.rounds);
-  w.chunk = n <= 16384 ? 8 : 32;
+  // long chunks leave fewer sums of crossing runs, as long as the chip has waves (four to eight per SIMD)
+  const int64_t slabs = (cols + 64 * kSumVec - 1) / (64 * kSumVec);
+  w.chunk = 8;
+  for (const int c : {16, 32, 48})
+    if (n / c * slabs >= 4096) w.chunk = c;
   w.chunks = (n + w.chunk - 1) / w.chunk;
   w.passes = 1;
   while (w.passes < 4 && (uint64_t(rows) >> (8 * w.passes)) != 0) ++w.passes;
+  w.sorted = n <= kOneBlock ? 0 : w.passes & 1;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     unsigned char* p = ws ? ws + at : nullptr;
@@ -100,27 +115,79 @@ Work layout(unsigned char* ws, int64_t n, int64_t rows, int64_t cols) {
     w.val[k] = reinterpret_cast<uint32_t*>(take(size_t(n) * 4));
   }
   w.hist = reinterpret_cast<uint32_t*>(take(size_t(w.tiles) * kDigits * 4));
-  w.touched = take(size_t(rows));
+  w.touched = take(n <= kOneBlock ? 0 : size_t(rows));
+  w.crossing = reinterpret_cast<uint32_t*>(take(size_t(w.chunks + 1) * 4));
   w.part = reinterpret_cast<float*>(take(size_t(w.chunks) * 2 * size_t(cols) * 4));
   w.bytes = at;
   return w;
 }
 
-// Digits of every tile; the first pass reads the ids and clears the row marks.
-__global__ __launch_bounds__(kSortBlock) void k_embedding_digits(EmbeddingBackward a, Work w, int pass) {
+// The sort's launches keep few compute units busy, so blocks behind the sort's
+// clear the gradient meanwhile.  A short list's one launch clears all of it
+// and the named rows are written again; a long list names much of the table,
+// so its first pass marks the rows, and the launches of the later passes clear
+// the others, a share each (65,536 tokens of 32,000 x 2048: 161 us for
+// everything with all rows cleared under the four launches).
+struct Clear {
+  uint16_t* to;             // 2-byte units
+  int64_t row, ld;          // units of a row
+  int64_t first, last;      // this launch's rows
+  const unsigned char* touched;   // NULL: clear every row
+};
+
+// The rows' 16-byte vectors in one sequence, 1024 neighbours a block and turn
+// (a wave a row instead takes twice as long); row and place in it are carried
+// along, as a division for each vector costs more than its store.
+__device__ __forceinline__ void clear_block(const Clear& c, int64_t block, int64_t blocks) {
+  constexpr int U = 4;
+  const Pack<uint16_t, 8> zero{};
+  const int64_t per = (c.row + 7) / 8, step = blocks * kSortBlock, step_r = step / per, step_i = step - step_r * per;
+  const int64_t at = block * kSortBlock + threadIdx.x;
+  int64_t r = c.first + at / per, i = at % per;
+  while (r < c.last) {
+    int64_t rs[U], is[U];
+    bool skip[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      rs[k] = r;
+      is[k] = i;
+      skip[k] = r >= c.last || (c.touched && c.touched[r]);
+      r += step_r;
+      i += step_i;
+      if (i >= per) {
+        i -= per;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (!skip[k]) store_pack<uint16_t, 8>(c.to + rs[k] * c.ld, is[k] * 8, c.row, zero);
+  }
+}
+
+// Digits of every tile; the first pass reads the ids.
+__global__ __launch_bounds__(kSortBlock) void k_embedding_digits(EmbeddingBackward a, Work w, int pass, Clear clear) {
+  if (int64_t(blockIdx.x) >= w.tiles) {
+    clear_block(clear, blockIdx.x - w.tiles, gridDim.x - w.tiles);
+    return;
+  }
   __shared__ uint32_t hist[kDigits];
   for (int d = threadIdx.x; d < kDigits; d += kSortBlock) hist[d] = 0;
+  if (pass == 0) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) w.crossing[0] = 0;
+    if (!a.accumulate)
+      for (int64_t v = (int64_t(blockIdx.x) * kSortBlock + threadIdx.x) * 16; v < a.rows; v += w.tiles * kSortBlock * 16)
+        store_pack<unsigned char, 16>(w.touched, v, a.rows, Pack<unsigned char, 16>{});
+  }
   __syncthreads();
   const int64_t first = int64_t(blockIdx.x) * w.rounds * kTile, last = std::min<int64_t>(a.n_ids, first + w.rounds * kTile);
+#pragma unroll 4
   for (int64_t t = first + threadIdx.x; t < last; t += kSortBlock) {
     const uint32_t key = pass == 0 ? row_of(a.ids, a.id_bytes, t, a.row0, a.rows) : w.key[pass & 1][t];
     atomicAdd(&hist[(key >> (8 * pass)) & 255], 1u);
   }
   __syncthreads();
   for (int d = threadIdx.x; d < kDigits; d += kSortBlock) w.hist[int64_t(blockIdx.x) * kDigits + d] = hist[d];
-  if (pass == 0 && !a.accumulate)
-    for (int64_t v = int64_t(blockIdx.x) * kSortBlock + threadIdx.x; v < a.rows; v += int64_t(gridDim.x) * kSortBlock)
-      w.touched[v] = 0;
 }
 
 // Exclusive scan of one value per digit over the first 256 threads of a block.
@@ -141,9 +208,9 @@ __device__ __forceinline__ uint32_t scan_digits(uint32_t x, uint32_t* wave_total
   return before + inc - x;
 }
 
-// The other lanes of the wave with this lane's digit (valid lanes only).
-__device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid) {
-  uint64_t m = __ballot(valid);
+// The lanes of the wave with this lane's digit.
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit) {
+  uint64_t m = ~uint64_t(0);
 #pragma unroll
   for (int b = 0; b < 8; ++b) {
     const bool bit = (digit >> b) & 1;
@@ -153,39 +220,137 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool valid) {
   return m;
 }
 
-// One stable pass: every token goes behind the tokens of lower digits and the
-// earlier ones of its own.  Within a tile each wave holds 256 consecutive
-// tokens, ranks them among its own (ballots), and the waves' counts are
-// scanned in order.
-__global__ __launch_bounds__(kSortBlock) void k_embedding_place(EmbeddingBackward a, Work w, int pass) {
-  constexpr int WAVES = kSortBlock / 64, N = kPerWave / 64;
-  __shared__ uint32_t count[WAVES][kDigits];
+constexpr int kSortWaves = kSortBlock / 64;
+
+// rank[j]: the wave's tokens before token j of this lane with its digit, by
+// the order of the tokens (64 consecutive ones for each j); count: the wave's
+// tokens of every digit.
+template <int N>
+__device__ __forceinline__ void rank_wave(const uint32_t (&key)[N], int shift, uint32_t* count, uint32_t (&rank)[N]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t digit = (key[j] >> shift) & 255;
+    const uint64_t same = same_digit(digit), lower = same & ((uint64_t(1) << lane) - 1);
+    rank[j] = count[digit] + __popcll(lower);
+    // the wave's reads of its counts come before its writes, and those before the next reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (lower == 0) count[digit] += __popcll(same);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+__device__ __forceinline__ void clear_counts(uint32_t (&count)[kSortWaves][kDigits]) {
+  uint4* c = reinterpret_cast<uint4*>(&count[0][0]);
+  for (int i = threadIdx.x; i < kSortWaves * kDigits / 4; i += kSortBlock) c[i] = uint4{0, 0, 0, 0};
+}
+
+// All of a short list in one block: every pass in LDS.  Behind the list's end
+// the keys are all ones and stay last (the sort is stable).
+template <int N>
+__global__ __launch_bounds__(kSortBlock) void k_embedding_sort(EmbeddingBackward a, Work w, Clear clear) {
+  if (blockIdx.x > 0) {
+    clear_block(clear, blockIdx.x - 1, gridDim.x - 1);
+    return;
+  }
+  __shared__ uint32_t count[kSortWaves][kDigits];
+  __shared__ uint32_t skey[kSortBlock * N], sval[kSortBlock * N];
+  __shared__ uint32_t wave_total[4];
+  const int wave = threadIdx.x >> 6, first = wave * 64 * N + (threadIdx.x & 63);
+  const int n = int(a.n_ids);
+  uint32_t key[N], val[N], rank[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int t = first + j * 64;
+    key[j] = t < n ? row_of(a.ids, a.id_bytes, t, a.row0, a.rows) : ~uint32_t(0);
+    val[j] = uint32_t(t);
+  }
+  if (threadIdx.x == 0) w.crossing[0] = 0;
+  for (int pass = 0; pass < w.passes; ++pass) {
+    clear_counts(count);
+    __syncthreads();
+    rank_wave<N>(key, 8 * pass, count[wave], rank);
+    __syncthreads();
+    uint32_t total = 0;
+    if (threadIdx.x < kDigits)
+#pragma unroll
+      for (int k = 0; k < kSortWaves; ++k) total += count[k][threadIdx.x];
+    uint32_t at = scan_digits(total, wave_total);
+    if (threadIdx.x < kDigits)
+#pragma unroll
+      for (int k = 0; k < kSortWaves; ++k) {
+        const uint32_t c = count[k][threadIdx.x];
+        count[k][threadIdx.x] = at;
+        at += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t to = count[wave][(key[j] >> (8 * pass)) & 255] + rank[j];
+      skey[to] = key[j];
+      sval[to] = val[j];
+    }
+    __syncthreads();
+    if (pass + 1 < w.passes)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        key[j] = skey[first + j * 64];
+        val[j] = sval[first + j * 64];
+      }
+  }
+  for (int t = threadIdx.x; t < n; t += kSortBlock) {
+    w.key[0][t] = skey[t];
+    w.val[0][t] = sval[t];
+  }
+}
+
+// One stable pass over a long list: every token goes behind the tokens of
+// lower digits and the earlier ones of its own.
+__global__ __launch_bounds__(kSortBlock) void k_embedding_place(EmbeddingBackward a, Work w, int pass, Clear clear) {
+  if (int64_t(blockIdx.x) >= w.tiles) {
+    clear_block(clear, blockIdx.x - w.tiles, gridDim.x - w.tiles);
+    return;
+  }
+  constexpr int N = kTile / kSortBlock;
+  __shared__ uint32_t count[kSortWaves][kDigits];
   __shared__ uint32_t base[kDigits];
   __shared__ uint32_t wave_total[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6;
 
+  // tokens of each digit, and those of the tiles before this block's: four threads a digit
   uint32_t total = 0, before = 0;
-  if (threadIdx.x < kDigits)
-    for (int64_t b = 0; b < w.tiles; ++b) {
-      const uint32_t h = w.hist[b * kDigits + threadIdx.x];
-      if (b < int64_t(blockIdx.x)) before += h;
+  {
+    const int d = threadIdx.x & 255, q = threadIdx.x >> 8;
+#pragma unroll 8
+    for (int64_t b = q; b < w.tiles; b += 4) {
+      const uint32_t h = w.hist[b * kDigits + d];
+      before += b < int64_t(blockIdx.x) ? h : 0;
       total += h;
     }
+    count[q][d] = total;
+    count[q + 4][d] = before;
+    __syncthreads();
+    if (threadIdx.x < kDigits) {
+      total = count[0][d] + count[1][d] + count[2][d] + count[3][d];
+      before = count[4][d] + count[5][d] + count[6][d] + count[7][d];
+    } else {
+      total = 0;
+    }
+  }
   const uint32_t start = scan_digits(total, wave_total);
   if (threadIdx.x < kDigits) base[threadIdx.x] = start + before;
 
   for (int64_t round = 0; round < w.rounds; ++round) {
-    const int64_t tile = (int64_t(blockIdx.x) * w.rounds + round) * kTile;
-    for (int d = threadIdx.x; d < WAVES * kDigits; d += kSortBlock) (&count[0][0])[d] = 0;
-    __syncthreads();
+    const int64_t first = (int64_t(blockIdx.x) * w.rounds + round) * kTile + wave * 64 * N + (threadIdx.x & 63);
     uint32_t key[N], val[N], rank[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int64_t t = tile + wave * kPerWave + j * 64 + lane;
-      const bool valid = t < a.n_ids;
-      key[j] = 0;
+      const int64_t t = first + j * 64;
+      key[j] = ~uint32_t(0);   // behind the list's end: last in its tile
       val[j] = uint32_t(t);
-      if (valid) {
+      if (t < a.n_ids) {
         if (pass == 0) {
           key[j] = row_of(a.ids, a.id_bytes, t, a.row0, a.rows);
           if (!a.accumulate && int64_t(key[j]) < a.rows) w.touched[key[j]] = 1;
@@ -194,24 +359,16 @@ __global__ __launch_bounds__(kSortBlock) void k_embedding_place(EmbeddingBackwar
           val[j] = w.val[pass & 1][t];
         }
       }
-      const uint32_t digit = (key[j] >> (8 * pass)) & 255;
-      const uint64_t same = same_digit(digit, valid), lower = same & ((uint64_t(1) << lane) - 1);
-      rank[j] = 0;
-      if (valid) {
-        rank[j] = count[wave][digit] + __popcll(lower);
-      }
-      // the wave's reads of its counts come before its writes, and those before the next round's reads
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      if (valid && lower == 0) count[wave][digit] += __popcll(same);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
     }
+    __syncthreads();
+    clear_counts(count);
+    __syncthreads();
+    rank_wave<N>(key, 8 * pass, count[wave], rank);
     __syncthreads();
     if (threadIdx.x < kDigits) {
       uint32_t at = base[threadIdx.x];
 #pragma unroll
-      for (int k = 0; k < WAVES; ++k) {
+      for (int k = 0; k < kSortWaves; ++k) {
         const uint32_t c = count[k][threadIdx.x];
         count[k][threadIdx.x] = at;
         at += c;
@@ -220,172 +377,183 @@ __global__ __launch_bounds__(kSortBlock) void k_embedding_place(EmbeddingBackwar
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int64_t t = tile + wave * kPerWave + j * 64 + lane;
-      if (t < a.n_ids) {
+    for (int j = 0; j < N; ++j)
+      if (first + j * 64 < a.n_ids) {
         const uint32_t to = count[wave][(key[j] >> (8 * pass)) & 255] + rank[j];
         w.key[(pass + 1) & 1][to] = key[j];
         w.val[(pass + 1) & 1][to] = val[j];
       }
-    }
-    __syncthreads();
   }
 }
 
-template <class TG>
-__device__ __forceinline__ void store_row(const EmbeddingBackward& a, uint32_t v, int64_t c, const float* x, int n) {
-  TG* to = static_cast<TG*>(a.dtable) + int64_t(v) * a.ldt;
-  constexpr int V = 4;
-  for (int k = 0; k < n; k += V) {
-    Pack<TG, V> p{};
-    if (a.accumulate) p = load_pack<TG, V>(to, c + k, a.cols);
+// x, a vector of sums of a row's columns, into the gradient's row.
+template <class TG, int V, int MODE>
+__device__ __forceinline__ void store_row(const EmbeddingBackward& a, TG* to, const SlabVec<V, MODE>& at, const float (&x)[V]) {
+  Pack<TG, V> p{};
+  if (a.accumulate) p = at.load(static_cast<const TG*>(to));
 #pragma unroll
-    for (int i = 0; i < V; ++i) p.v[i] = from_f32<TG>(to_f32(p.v[i]) + x[k + i] * a.scale);
-    store_pack<TG, V>(to, c + k, a.cols, p);
-  }
+  for (int i = 0; i < V; ++i) p.v[i] = from_f32<TG>(to_f32(p.v[i]) + x[i] * a.scale);
+  at.store(to, p);
 }
 
-// One chunk of sorted tokens over one slab of columns (this lane's from c).
-template <class TD, class TG>
-__device__ __forceinline__ void sum_chunk(const EmbeddingBackward& a, const Work& w, int64_t chunk, int64_t c) {
-  constexpr int V = kVec<TD>, U = 8;
+// Lanes from the first on that hold `key`.
+__device__ __forceinline__ int leading(uint32_t lane_key, uint32_t key) {
+  const uint64_t other = __ballot(lane_key != key);
+  return other ? __builtin_ctzll(other) : 64;
+}
+
+// A lane's 64-bit value, uniform.
+__device__ __forceinline__ uint64_t of_lane(uint64_t x, int lane) {
+  return uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(x >> 32), lane))) << 32 |
+         uint32_t(__builtin_amdgcn_readlane(uint32_t(x), lane));
+}
+
+// One chunk of sorted tokens over the slab of columns from slab0.
+template <class TD, class TG, int MODE>
+__device__ __forceinline__ void sum_chunk(const EmbeddingBackward& a, const Work& w, int64_t chunk, int64_t slab0) {
+  constexpr int V = kSumVec, U = kSumAhead;
   const int lane = threadIdx.x & 63;
-  const uint32_t* skey = w.key[w.passes & 1];
-  const uint32_t* sval = w.val[w.passes & 1];
+  const uint32_t* skey = w.key[w.sorted];
+  const uint32_t* sval = w.val[w.sorted];
   const uint32_t none = uint32_t(a.rows);
-  const int64_t p0 = chunk * w.chunk, p1 = std::min<int64_t>(a.n_ids, p0 + w.chunk);
-  const int n = int(p1 - p0);
-  uint32_t lane_key = none, lane_val = 0;
-  if (lane < n) {
-    lane_key = skey[p0 + lane];
-    lane_val = sval[p0 + lane];
-  }
-  const uint32_t prev = p0 > 0 ? skey[p0 - 1] : none, next = p1 < a.n_ids ? skey[p1] : none;
-  uint32_t cur = __builtin_amdgcn_readlane(lane_key, 0);
-  bool inside = cur != prev;   // the run began in this chunk
+  // the chunk's tokens and kReach + 1 behind it, one a lane
+  const int64_t p0 = chunk * w.chunk, left = a.n_ids - p0;
+  const int own = int(std::min<int64_t>(left, w.chunk));
+  const int64_t mine = p0 + (lane < left ? lane : left - 1);
+  uint32_t lane_key = skey[mine], lane_val = sval[mine];
+  uint32_t prev = skey[p0 > 0 ? p0 - 1 : 0];
+  if (p0 == 0) prev = none;
+  if (lane >= left || lane >= w.chunk + kReach + 1) lane_key = none;
+  if (lane_key == none) lane_val = 0;   // tokens of no row are read as token 0 and left out
+  // tokens that the chunk before takes, and tokens taken from the chunk behind
+  const int head = leading(lane_key, prev);
+  const int first = prev != none && head <= kReach ? head : 0;
+  const uint32_t last = __builtin_amdgcn_readlane(lane_key, own - 1);
+  const int more = own < w.chunk ? 0 : leading(__shfl_down(lane_key, own), last);
+  const int n = more <= kReach ? own + more : own;
+  const bool ends = more <= kReach;   // the last run ends here
+  const uint32_t begin = __builtin_amdgcn_readlane(lane_key, first < own ? first : 0);
+  if (first >= own || begin == none) return;   // all of it belongs to the chunk before, or to no row
+  bool inside = begin != prev;                 // the run began in this chunk
+  // bit i: token i + 1 is of another row than token i
+  const uint64_t change = __ballot(lane_key != uint32_t(__shfl_down(lane_key, 1)));
+  const uint64_t from = uint64_t(lane_val) * uint64_t(a.ldd) * sizeof(TD), to = uint64_t(lane_key) * uint64_t(a.ldt) * sizeof(TG);
+  const SlabVec<V, MODE> at(slab0, lane * V, a.cols);
+  const char* dout = static_cast<const char*>(a.dout);
+  char* dtable = static_cast<char*>(a.dtable);
   float acc[V] = {};
   float* part = w.part + size_t(chunk) * 2 * size_t(a.cols);
-  for (int i0 = 0; i0 < n; i0 += U) {
-    Pack<TD, V> p[U];
+  const auto leave = [&](float* to) {
+    Pack<float, V> p;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p.v[i] = acc[i];
+    at.store(to, p);
+  };
+  Pack<TD, V> p[U], q[U];
+  const auto load = [&](Pack<TD, V>(&x)[U], int i0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) x[j] = at.load(reinterpret_cast<const TD*>(dout + of_lane(from, i0 + j < n ? i0 + j : n - 1)));
+  };
+  load(q, first);
+  for (int i0 = first; i0 < n; i0 += U) {
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      const uint32_t k = __builtin_amdgcn_readlane(lane_key, i0 + j < 64 ? i0 + j : 63);
-      const uint32_t t = __builtin_amdgcn_readlane(lane_val, i0 + j < 64 ? i0 + j : 63);
-      p[j] = Pack<TD, V>{};
-      if (i0 + j < n && k != none && c < a.cols) p[j] = load_pack<TD, V>(static_cast<const TD*>(a.dout) + int64_t(t) * a.ldd, c, a.cols);
+      settle(q[j]);
+      p[j] = q[j];
     }
+    if (i0 + U < n) load(q, i0 + U);
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if (i0 + j >= n) break;
-      const uint32_t k = __builtin_amdgcn_readlane(lane_key, i0 + j);
-      if (k != cur) {
-        if (c < a.cols) {
-          if (inside) store_row<TG>(a, cur, c, acc, V);
-          else
+      const int i = i0 + j;
+      if (i >= n) break;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-              if (c + i < a.cols) part[c + i] = acc[i];
-        }
+      for (int k = 0; k < V; ++k) acc[k] += to_f32(p[j].v[k]);
+      if (i + 1 < n && (change >> i & 1)) {   // the run ends here
+        if (inside) store_row<TG>(a, reinterpret_cast<TG*>(dtable + of_lane(to, i)), at, acc);
+        else leave(part);
         inside = true;
-        cur = k;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = 0.f;
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        if (uint32_t(__builtin_amdgcn_readlane(lane_key, i + 1)) == none) return;
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += to_f32(p[j].v[i]);
     }
   }
-  if (cur == none || c >= a.cols) return;
-  if (inside && cur != next) {
-    store_row<TG>(a, cur, c, acc, V);
+  if (inside && ends) {
+    store_row<TG>(a, reinterpret_cast<TG*>(dtable + of_lane(to, n - 1)), at, acc);
+  } else if (inside) {
+    leave(part + a.cols);
+    if (slab0 == 0 && lane == 0) w.crossing[1 + atomicAdd(w.crossing, 1u)] = uint32_t(chunk);
   } else {
-    if (inside) part += a.cols;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c + i < a.cols) part[c + i] = acc[i];
+    leave(part);
   }
 }
 
 // Sums of the sorted tokens: a wave takes `chunk` of them in order over 64
 // 16-byte vectors of columns, and writes a row where its run of equal keys
-// ends.  A run that crosses the chunk's border leaves its sum in the
-// workspace: slot 0 if it began before the chunk, slot 1 if it began in it.
-// Blocks behind those clear the rows that no token names.
-template <class TD, class TG>
-__global__ __launch_bounds__(256) void k_embedding_sum(EmbeddingBackward a, Work w, int64_t sum_blocks) {
-  constexpr int V = kVec<TD>;
-  const int lane = threadIdx.x & 63;
-  if (int64_t(blockIdx.x) >= sum_blocks) {
-    // rows that no token names, one wave a row
-    const int64_t waves = (int64_t(gridDim.x) - sum_blocks) * 4;
-    for (int64_t v = (int64_t(blockIdx.x) - sum_blocks) * 4 + (threadIdx.x >> 6); v < a.rows; v += waves) {
-      if (w.touched[v]) continue;
-      TG* to = static_cast<TG*>(a.dtable) + v * a.ldt;
-      constexpr int VG = kVec<TG>;
-      const Pack<TG, VG> zero{};
-      for (int64_t c = lane * VG; c < a.cols; c += 64 * VG) store_pack<TG, VG>(to, c, a.cols, zero);
-    }
-    return;
-  }
-  const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V), units = w.chunks * slabs;
-  for (int64_t unit = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); unit < units; unit += sum_blocks * 4)
-    sum_chunk<TD, TG>(a, w, unit / slabs, unit % slabs * (64 * V) + lane * V);
+// ends.  A run that has at most kReach tokens behind the chunk's border is taken
+// to its end, and the next chunk leaves them out; one that goes on further
+// leaves its sum in the workspace: slot 0 if it began before the chunk, slot 1
+// if it began in it.
+// 65,536 tokens of 32,000 x 2048, bf16 to fp32: 95 us.  That is HBM's time for
+// the whole gradient: besides 241 MB of dout read and 102 MB of rows written,
+// the rows cleared before leave the 256 MB memory-side cache meanwhile, 500 MB
+// in all at 5.3 TB/s.  Half the width, which fits that cache, takes 38.
+template <class TD, class TG, int MODE>
+__global__ __launch_bounds__(256) void k_embedding_sum(EmbeddingBackward a, Work w) {
+  constexpr int S = 64 * kSumVec;
+  const int64_t slabs = (a.cols + S - 1) / S, units = w.chunks * slabs;
+  const int64_t step = int64_t(gridDim.x) * 4;
+  for (int64_t unit = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); unit < units; unit += step)
+    sum_chunk<TD, TG, MODE>(a, w, unit / slabs, unit % slabs * S);
 }
 
-// The run of equal keys that begins in `chunk` and goes on behind it, if there is one.
-template <class TG>
-__device__ __forceinline__ void join_run(const EmbeddingBackward& a, const Work& w, float (&quarter)[4][256], int64_t chunk,
-                                         int64_t c0) {
-  const uint32_t* skey = w.key[w.passes & 1];
-  const int64_t p0 = chunk * w.chunk, p1 = p0 + w.chunk;
-  if (p1 >= a.n_ids) return;                       // the last chunk: nothing behind it
-  const uint32_t key = skey[p1 - 1];
-  if (key == uint32_t(a.rows) || skey[p1] != key) return;
-  if (p0 > 0 && skey[p0] == key && skey[p0 - 1] == key) return;   // began before this chunk
-  // chunks behind this one whose first token belongs to the run
+// Runs that cross chunks: one block a run and 256 columns adds up the chunks'
+// sums, four waves a quarter each, the quarters in order.  The list of runs
+// comes in any order, each run's sum does not.
+constexpr int kJoinWaves = 4;
+template <class TG, int MODE>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_embedding_join(EmbeddingBackward a, Work w) {
+  __shared__ float share[kJoinWaves][4][64];
+  const uint32_t* skey = w.key[w.sorted];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t last = chunk;
-  for (int64_t step = 4096; step >= 1; step /= 64) {
-    int cnt;
-    do {
+  const SlabVec<4, MODE> at(int64_t(blockIdx.x) * 256, lane * 4, a.cols);
+  const uint32_t runs = w.crossing[0];
+  for (uint32_t i = blockIdx.y; i < runs; i += gridDim.y) {
+    const int64_t chunk = w.crossing[1 + i];
+    const uint32_t key = skey[(chunk + 1) * w.chunk - 1];
+    // the last chunk with a sum of the run: more than kReach of its tokens; 64 guesses at a time, near ones first
+    int64_t last = chunk;
+    const auto reach = [&](int64_t step) {
       const int64_t j = last + (lane + 1) * step;
-      const uint64_t ok = __ballot(j < w.chunks && skey[j * w.chunk] == key);
-      cnt = ok == ~uint64_t(0) ? 64 : __builtin_ctzll(~ok);
+      const uint64_t ok = __ballot(j * w.chunk + kReach < a.n_ids && skey[j * w.chunk + kReach] == key);
+      const int cnt = ok == ~uint64_t(0) ? 64 : __builtin_ctzll(~ok);
       last += cnt * step;
-    } while (cnt == 64);
-  }
-  const int64_t m = last - chunk + 1, q = (m + 3) / 4;
-  const int64_t b = std::min<int64_t>(m, wave * q), e = std::min<int64_t>(m, b + q);
-  const int64_t c = c0 + lane * 4;
-  float acc[4] = {};
-  if (c < a.cols) {
-#pragma unroll 4
-    for (int64_t j = b; j < e; ++j) {
-      const float* part = w.part + (size_t(chunk + j) * 2 + (j == 0 ? 1 : 0)) * size_t(a.cols);
-      const Pack<float, 4> p = load_pack<float, 4>(part, c, a.cols);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += p.v[i];
+      return cnt == 64;
+    };
+    if (reach(1)) {
+      while (reach(4096)) {}
+      while (reach(64)) {}
+      while (reach(1)) {}
     }
-  }
+    const int64_t m = last - chunk + 1, q = (m + kJoinWaves - 1) / kJoinWaves;
+    const int64_t b = std::min<int64_t>(m, wave * q), e = std::min<int64_t>(m, b + q);
+    float acc[4] = {};
+#pragma unroll 8
+    for (int64_t j = b; j < e; ++j) {
+      const Pack<float, 4> p = at.load(w.part + (size_t(chunk + j) * 2 + (j == 0 ? 1 : 0)) * size_t(a.cols));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) quarter[wave][lane * 4 + i] = acc[i];
-  __syncthreads();
-  if (wave != 0 || c >= a.cols) return;
+      for (int k = 0; k < 4; ++k) acc[k] += p.v[k];
+    }
 #pragma unroll
-  for (int k = 1; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) share[wave][k][lane] = acc[k];
+    __syncthreads();
+    if (wave == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += quarter[k][lane * 4 + i];
-  store_row<TG>(a, key, c, acc, 4);
-}
-
-// Rows whose run crosses chunks: the block of the chunk where the run begins
-// adds up the chunks' sums, four waves a quarter each, the quarters in order.
-template <class TG>
-__global__ __launch_bounds__(256) void k_embedding_join(EmbeddingBackward a, Work w) {
-  __shared__ float quarter[4][256];
-  const int64_t slabs = (a.cols + 255) / 256, units = w.chunks * slabs;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    join_run<TG>(a, w, quarter, u / slabs, u % slabs * 256);
+      for (int s = 1; s < kJoinWaves; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] += share[s][k][lane];
+      store_row<TG>(a, static_cast<TG*>(a.dtable) + int64_t(key) * a.ldt, at, acc);
+    }
     __syncthreads();
   }
 }
@@ -420,25 +588,56 @@ hipError_t launch_embedding_forward(const EmbeddingForward& a, hipStream_t s) {
 hipError_t launch_embedding_backward(const EmbeddingBackward& a, hipStream_t s) {
   if (a.n_ids == 0 && a.accumulate) return hipSuccess;
   const Work w = layout(a.ws, a.n_ids, a.rows, a.cols);
-  for (int pass = 0; pass < w.passes; ++pass) {
-    k_embedding_digits<<<dim3(unsigned(w.tiles)), dim3(kSortBlock), 0, s>>>(a, w, pass);
-    k_embedding_place<<<dim3(unsigned(w.tiles)), dim3(kSortBlock), 0, s>>>(a, w, pass);
+  const bool one = a.n_ids <= kOneBlock;
+  Clear clear{};
+  const int64_t units = a.gdtype == kF32 ? 2 : 1;
+  clear.to = static_cast<uint16_t*>(a.dtable);
+  clear.row = a.cols * units;
+  clear.ld = a.ldt * units;
+  // a long list of one pass (below 256 rows) has no later launch for it, and little to clear
+  const int64_t shares = one ? 1 : w.passes == 1 ? 2 : 2 * (w.passes - 1);
+  if (!one && w.passes > 1) clear.touched = w.touched;
+  auto grid = [&](int64_t share, int64_t sort_blocks) {
+    const bool any = share >= 0 && !a.accumulate;
+    clear.first = any ? a.rows * share / shares : 0;
+    clear.last = any ? a.rows * (share + 1) / shares : 0;
+    const int64_t per = int64_t(kSortBlock) * 8, vectors = (clear.last - clear.first) * ((clear.row + 7) / 8);
+    return dim3(unsigned(sort_blocks + std::min<int64_t>((vectors + per - 1) / per, 1024)));
+  };
+  const dim3 block(kSortBlock);
+  if (one) {
+    const dim3 g = grid(0, 1);
+    if (a.n_ids <= kSortBlock) k_embedding_sort<1><<<g, block, 0, s>>>(a, w, clear);
+    else if (a.n_ids <= 4 * kSortBlock) k_embedding_sort<4><<<g, block, 0, s>>>(a, w, clear);
+    else k_embedding_sort<8><<<g, block, 0, s>>>(a, w, clear);
+  } else {
+    for (int pass = 0; pass < w.passes; ++pass) {
+      const int64_t share = w.passes == 1 ? 0 : 2 * (pass - 1);
+      dim3 g = grid(share, w.tiles);
+      k_embedding_digits<<<g, block, 0, s>>>(a, w, pass, clear);
+      g = grid(share < 0 ? -1 : share + 1, w.tiles);
+      k_embedding_place<<<g, block, 0, s>>>(a, w, pass, clear);
+    }
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.n_ids == 0) return e;
   return with_type(a.gdtype, [&](auto tg) {
     using TG = decltype(tg);
-    const hipError_t e2 = with_type(a.dtype, [&](auto td) {
+    with_type(a.dtype, [&](auto td) {
       using TD = decltype(td);
-      const int64_t slabs = (a.cols + 64 * kVec<TD> - 1) / (64 * kVec<TD>);
-      const int64_t sum_blocks = std::min<int64_t>((w.chunks * slabs + 3) / 4, 1 << 20);
-      const int64_t zero_blocks = a.accumulate ? 0 : std::min<int64_t>((a.rows + 3) / 4, 8192);
-      if (sum_blocks + zero_blocks == 0) return hipSuccess;
-      k_embedding_sum<TD, TG><<<dim3(unsigned(sum_blocks + zero_blocks)), dim3(256), 0, s>>>(a, w, sum_blocks);
-      return hipGetLastError();
+      constexpr int V = kSumVec;
+      const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
+      const dim3 g(unsigned(std::min<int64_t>((w.chunks * slabs + 3) / 4, 1 << 20)));
+      const int mode = row_mode(a.cols, V);
+      if (mode == kTiny) k_embedding_sum<TD, TG, kTiny><<<g, dim3(256), 0, s>>>(a, w);
+      else if (mode == kWhole) k_embedding_sum<TD, TG, kWhole><<<g, dim3(256), 0, s>>>(a, w);
+      else k_embedding_sum<TD, TG, kTail><<<g, dim3(256), 0, s>>>(a, w);
     });
-    if (e2 != hipSuccess || w.chunks < 2) return e2;
-    k_embedding_join<TG><<<dim3(unsigned(std::min<int64_t>(w.chunks * ((a.cols + 255) / 256), 1 << 20))), dim3(256), 0, s>>>(a, w);
+    if (w.chunks >= 2) {
+      const dim3 g(unsigned((a.cols + 255) / 256), unsigned(std::min<int64_t>(w.chunks, 256)));
+      if (a.cols < 4) k_embedding_join<TG, kTiny><<<g, dim3(64 * kJoinWaves), 0, s>>>(a, w);
+      else k_embedding_join<TG, kTail><<<g, dim3(64 * kJoinWaves), 0, s>>>(a, w);
+    }
     return hipGetLastError();
   });
 }

@@ -26,6 +26,20 @@ struct __attribute__((packed, aligned(sizeof(T)))) Pack {
   T v[N];
 };
 
+// Waits here for a load into p.  One counter covers a wave's loads and stores,
+// so a wait behind branches with stores in them waits for all of those too;
+// a batch of loads settled together is waited for once.
+template <class T, int N>
+__device__ __forceinline__ void settle(Pack<T, N>& p) {
+  struct Words {
+    uint32_t w[sizeof(T) * N / 4];
+  };
+  Words u = __builtin_bit_cast(Words, p);
+#pragma unroll
+  for (int i = 0; i < int(sizeof(T) * N / 4); ++i) asm volatile("" : "+v"(u.w[i]));
+  p = __builtin_bit_cast(Pack<T, N>, u);
+}
+
 // Elements of a 16-byte access.
 template <class T>
 constexpr int kVec = 16 / int(sizeof(T));
@@ -53,6 +67,93 @@ __device__ __forceinline__ void store_pack(T* row, int64_t c, int64_t n, const P
       if (c + i < n) row[c + i] = p.v[i];
   }
 }
+
+// A row of n elements cut into vectors of V, one at column c = V, 2 V, ... for
+// each thread, so that loads need no branch (branches around loads make the
+// compiler wait for each one):
+//   MODE kWhole  n is a multiple of V
+//   MODE kTail   the last vector moves back to end with the row; elements that
+//                it shares with the one before it are not its own
+//   MODE kTiny   n < V: element by element
+// Threads behind the row's end load its last vector and own nothing.
+enum : int { kWhole = 0, kTail = 1, kTiny = 2 };
+inline int row_mode(int64_t n, int v) { return n < v ? kTiny : n % v ? kTail : kWhole; }
+
+template <class T, int V, int MODE>
+struct RowVec {
+  int64_t c, at, n;   // the thread's columns begin at c; its vector is read at `at`
+
+  __device__ __forceinline__ RowVec(int64_t c_, int64_t n_) : c(c_), at(MODE == kTiny ? c_ : c_ < n_ - V ? c_ : n_ - V), n(n_) {}
+  // element i of the vector is the thread's own (column at + i)
+  __device__ __forceinline__ bool own(int i) const {
+    if (MODE == kWhole) return c < n;
+    if (MODE == kTail) return c < n && at + i >= c;
+    return c + i < n;
+  }
+  template <class U = T>
+  __device__ __forceinline__ Pack<U, V> load(const U* row) const {
+    Pack<U, V> p;
+    if constexpr (MODE == kTiny) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p.v[i] = c + i < n ? row[c + i] : U(0.f);
+    } else {
+      p = *reinterpret_cast<const Pack<U, V>*>(row + at);
+    }
+    return p;
+  }
+  template <class U = T>
+  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p) const {
+    if (MODE != kTiny && c + V <= n) {
+      *reinterpret_cast<Pack<U, V>*>(row + at) = p;
+    } else if (MODE != kWhole) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (own(i)) row[at + i] = p.v[i];
+    }
+  }
+};
+
+// The same for a slab of columns of a long row, [slab0, slab0 + 64 V): the
+// row's address and slab0 are wave-uniform, so an access is a scalar base and
+// a 32-bit offset.
+template <int V, int MODE>
+struct SlabVec {
+  int64_t base;   // elements from the row's first to where offsets count from
+  int c, at, n;   // as RowVec, from the slab's first column
+  uint32_t off;
+
+  __device__ __forceinline__ SlabVec(int64_t slab0, int c_, int64_t cols) : c(c_), n(cols - slab0 < 65536 ? int(cols - slab0) : 65536) {
+    at = MODE == kTail && c > n - V ? n - V : c;   // n < V in a row's last slab: into the slab before
+    const int back = MODE == kTail && slab0 > 0 ? V : 0;
+    base = slab0 - back;
+    off = MODE == kTiny || c < n || MODE == kTail ? uint32_t(at + back) : 0;
+  }
+  __device__ __forceinline__ bool own(int i) const {
+    if (MODE == kWhole) return c < n;
+    return c + i < n + (c - at) && at + i >= c && c < n;
+  }
+  template <class U>
+  __device__ __forceinline__ Pack<U, V> load(const U* row) const {
+    Pack<U, V> p;
+    if constexpr (MODE == kTiny) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) p.v[i] = c + i < n ? row[c + i] : U(0.f);
+    } else {
+      p = *reinterpret_cast<const Pack<U, V>*>(row + base + off);
+    }
+    return p;
+  }
+  template <class U>
+  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p) const {
+    if (MODE != kTiny && c + V <= n) {
+      *reinterpret_cast<Pack<U, V>*>(row + base + off) = p;
+    } else if (MODE != kWhole) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (own(i)) row[base + off + i] = p.v[i];
+    }
+  }
+};
 
 // An element of a vector whose type is known at run time (0 fp32, 1 bf16, 2 fp16).
 __device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
