@@ -19,130 +19,167 @@
 namespace lopt {
 namespace {
 
+// The memory-side cache holds 256 MB.  The forward pass reads what does not fit
+// it with the non-temporal hint and leaves the last rows' logits there; the
+// backward pass begins with those, and its writes pass the cache by (4096 x
+// 50257 bf16, 412 MB: 68 + 146 us; no hints and the same order in both 117 +
+// 153; hints on all reads 67 + 163; kept bytes of 100 to 250 MB within 2 %).
+constexpr int64_t kKeptBytes = 200'000'000;
+constexpr int64_t kLongRow = 4096;   // columns from which a block has 512 threads, 128 below
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Sum and maximum over a block of W waves, the same bits on every thread.
-template <int W, class Op>
-__device__ __forceinline__ float block_reduce(float x, float* red, Op op) {
-  x = lanes_reduce<64>(x, op);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-  __syncthreads();
-  float s = red[0];
-#pragma unroll
-  for (int k = 1; k < W; ++k) s = op(s, red[k]);
-  return s;
+// Entry k of a row's list: u / tau, -inf if it is absent, and its id.
+struct Entry {
+  float u;
+  int64_t id;
+};
+template <class Args>
+__device__ __forceinline__ Entry load_entry(const Args& a, int64_t r, int k) {
+  Entry e;
+  e.id = a.id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[r * a.ldi + k]
+                         : int64_t(static_cast<const int32_t*>(a.ids)[r * a.ldi + k]);
+  e.u = load_any(a.u, a.udtype, r * a.ldu + k) * a.inv_tau;
+  if (e.id < 0 || e.id >= a.cols) e.u = -INFINITY;
+  return e;
 }
 
-// The teacher's list of one row in LDS: id (-1: absent), probability, and for
-// the loss log p.  Returns whether the row has an entry.
-struct Teacher {
-  int id[kMaxTop];
-  float p[kMaxTop];
+// Elements of a row's part [first, last) before its first 16-byte border, and
+// the number of whole vectors behind it.
+struct Cut {
+  int64_t lead, vecs;
 };
-
-template <int B>
-__device__ __forceinline__ bool load_teacher(Teacher& t, float* red, const void* ids, const void* u, int64_t row, int64_t ldi,
-                                             int64_t ldu, int top, int64_t cols, int id_bytes, int udtype, float inv_tau,
-                                             float& top_u, float& log_sum) {
-  float most = -INFINITY;
-  bool nan = false;
-  for (int k = threadIdx.x; k < top; k += B) {
-    const int64_t id = id_bytes == 8 ? static_cast<const int64_t*>(ids)[row * ldi + k]
-                                     : int64_t(static_cast<const int32_t*>(ids)[row * ldi + k]);
-    const float x = load_any(u, udtype, row * ldu + k) * inv_tau;
-    const bool there = id >= 0 && id < cols && x != -INFINITY;
-    t.id[k] = there ? int(id) : -1;
-    t.p[k] = x;
-    if (there) {
-      most = fmaxf(most, x);
-      nan |= x != x;
-    }
-  }
-  const bool any = __syncthreads_or(most != -INFINITY || nan);
-  if (!any) return false;
-  most = block_reduce<B / 64>(most, red, Max());
-  float sum = 0.f;
-  for (int k = threadIdx.x; k < top; k += B) {
-    const float e = t.id[k] >= 0 ? exp2_hw((t.p[k] - most) * kLog2e) : 0.f;
-    sum += e;
-  }
-  sum = block_reduce<B / 64>(sum, red, Add());
-  top_u = most;
-  log_sum = logf(sum);
-  return true;
+template <class T>
+__device__ __forceinline__ Cut cut_at_16(const T* z, int64_t n) {
+  constexpr int V = kVec<T>;
+  const int64_t to_border = int64_t((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) / int64_t(sizeof(T));
+  const int64_t lead = to_border < n ? to_border : n;
+  return {lead, (n - lead) / V};
 }
 
 // ---------------------------------------------------------------------------
-// Forward: one block a row.
+// Forward: one block a row.  The list's entries and the logits they name are
+// loaded first and stay in registers; the row is read once with a running
+// maximum and sum per thread; two exchanges over the block end it (the maxima
+// of both sides, then three sums).  With m the row's largest logit, u' the
+// list's, e_k = exp((u_k - u') / tau), E their sum and s = sum exp((z - m) / tau):
+//   loss / tau^2 = sum_k e_k ((u_k - u') - (z_(i_k) - m)) / tau / E - log E + log s,
+// small terms all of them, whatever the logits' common offset is.
 template <class T, int B>
 __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
-  constexpr int V = kVec<T>, W = B / 64, U = 4;
-  __shared__ Teacher t;
-  __shared__ float red[W];
+  constexpr int V = kVec<T>, W = B / 64, U = 4, NE = kMaxTop / B;
+  __shared__ float maxima[2][W], sums[3][W];
   const int64_t n = a.cols;
   const float c = a.inv_tau * kLog2e;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* z = static_cast<const T*>(a.z) + r * a.ldz;
+    float u[NE], zk[NE];
+    float top_u = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      u[e] = -INFINITY;
+      zk[e] = 0.f;
+      const int k = e * B + int(threadIdx.x);
+      if (k < a.top) {
+        const Entry t = load_entry(a, r, k);
+        u[e] = t.u;
+        if (t.u != -INFINITY) zk[e] = to_f32(z[t.id]);
+        top_u = fmaxf(top_u, t.u);
+        nan |= t.u != t.u;
+      }
+    }
+    if (nan) top_u = NAN;
+
     // running maximum m of z and sum s of exp((z - m) / tau), per thread
     float m = -INFINITY, s = 0.f;
-    auto take = [&](const Pack<T, V>* p, int count) {
+    const auto take = [&](auto const&... packs) {
       float top = m;
+      ([&] {
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (k < count)
-#pragma unroll
-          for (int i = 0; i < V; ++i) top = fmaxf(top, to_f32(p[k].v[i]));
+        for (int i = 0; i < V; ++i) top = fmaxf(top, to_f32(packs.v[i]));
+      }(), ...);
       const float mc = top == -INFINITY ? 0.f : top * c;   // all -inf so far: every term is exp(-inf) = 0
       s *= exp2_hw((m == -INFINITY ? -INFINITY : m * c - mc));
+      ([&] {
+        float t = 0.f;
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        if (k < count)
-#pragma unroll
-          for (int i = 0; i < V; ++i) s += exp2_hw(fmaf(to_f32(p[k].v[i]), c, -mc));
+        for (int i = 0; i < V; ++i) t += exp2_hw(fmaf(to_f32(packs.v[i]), c, -mc));
+        s += t;
+      }(), ...);
       m = top;
     };
-    int64_t j = threadIdx.x * V;
-    for (; j + int64_t(U - 1) * B * V + V <= n; j += int64_t(U) * B * V) {
-      Pack<T, V> p[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k) p[k] = *reinterpret_cast<const Pack<T, V>*>(z + j + int64_t(k) * B * V);
-      take(p, U);
+    // single elements up to the first 16-byte border and behind the last one: rows of an odd length begin anywhere, and
+    // unaligned vectors take a fifth more time (4096 x 50257 bf16: 112 us for 96)
+    const auto [lead, vecs] = cut_at_16(z, n);
+    const int64_t tail = lead + vecs * V;
+    const Pack<T, V>* zv = reinterpret_cast<const Pack<T, V>*>(z + lead);
+    int64_t j = threadIdx.x;
+    const auto read = [&](auto const& ld) {
+      for (; j + (U - 1) * B < vecs; j += U * B) take(ld(j), ld(j + B), ld(j + 2 * B), ld(j + 3 * B));
+      for (; j < vecs; j += B) take(ld(j));
+    };
+    if ((a.rows - r) * n * int64_t(sizeof(T)) > kKeptBytes) read([&](int64_t i) { return load_stream(zv + i); });
+    else read([&](int64_t i) { return zv[i]; });
+    if (int64_t(threadIdx.x) < lead + n - tail) {
+      const int64_t i = int64_t(threadIdx.x) < lead ? int64_t(threadIdx.x) : tail + threadIdx.x - lead;
+      Pack<T, 1> p;
+      p.v[0] = z[i];
+      const float x = to_f32(p.v[0]), top = fmaxf(m, x), mc = top == -INFINITY ? 0.f : top * c;
+      s = s * exp2_hw((m == -INFINITY ? -INFINITY : m * c - mc)) + exp2_hw(fmaf(x, c, -mc));
+      m = top;
     }
-    for (; j < n; j += int64_t(B) * V) {
-      Pack<T, V> p[U];
-      if (j + V <= n) {
-        p[0] = *reinterpret_cast<const Pack<T, V>*>(z + j);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[0].v[i] = j + i < n ? z[j + i] : from_f32<T>(-INFINITY);
-      }
-      take(p, 1);
-    }
-    const float top = block_reduce<W>(m, red, Max());
-    const float mc = top == -INFINITY ? 0.f : top * c;
-    s *= exp2_hw(m == -INFINITY ? -INFINITY : m * c - mc);
-    s = block_reduce<W>(s, red, Add());
-    const float lse = kLn2 * (mc + log2f(s));
 
-    float top_u, log_sum, loss = 0.f;
-    if (load_teacher<B>(t, red, a.ids, a.u, r, a.ldi, a.ldu, a.top, n, a.id_bytes, a.udtype, a.inv_tau, top_u, log_sum)) {
-      for (int k = threadIdx.x; k < a.top; k += B)
-        if (t.id[k] >= 0) {
-          const float logp = t.p[k] - top_u - log_sum, p = exp2_hw(logp * kLog2e);
-          // p that rounds to 0 has no term, whatever the student's logit
-          if (p != 0.f) loss = fmaf(p, logp - fmaf(to_f32(z[t.id[k]]), a.inv_tau, -lse), loss);
-        }
-      loss = block_reduce<W>(loss, red, Add()) * a.tau * a.tau;
+    const float wave_m = lanes_reduce<64>(m, Max());
+    const float wave_u = lanes_reduce<64>(top_u == top_u ? top_u : INFINITY, Max());   // NaN as +inf: gives NaN below
+    if (lane == 0) {
+      maxima[0][wave] = wave_m;
+      maxima[1][wave] = wave_u;
     }
+    __syncthreads();
+    float mz = maxima[0][0], mu = maxima[1][0];
+#pragma unroll
+    for (int k = 1; k < W; ++k) {
+      mz = fmaxf(mz, maxima[0][k]);
+      mu = fmaxf(mu, maxima[1][k]);
+    }
+    const float mc = mz == -INFINITY ? 0.f : mz * c;
+    s *= exp2_hw(m == -INFINITY ? -INFINITY : m * c - mc);
+    float es = 0.f, eu = 0.f;
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (u[e] != -INFINITY) {
+        const float d = u[e] - mu, p = exp2_hw(d * kLog2e);
+        es += p;
+        // p that rounds to 0 has no term, whatever the student's logit
+        if (p != 0.f) eu = fmaf(p, d - (zk[e] - mz) * a.inv_tau, eu);
+      }
+    s = lanes_sum<64>(s);
+    es = lanes_sum<64>(es);
+    eu = lanes_sum<64>(eu);
+    if (lane == 0) {
+      sums[0][wave] = s;
+      sums[1][wave] = es;
+      sums[2][wave] = eu;
+    }
+    __syncthreads();
     if (threadIdx.x == 0) {
-      if (a.loss) a.loss[r] = loss;
-      if (a.lse) a.lse[r] = lse;
+      s = sums[0][0], es = sums[1][0], eu = sums[2][0];
+#pragma unroll
+      for (int k = 1; k < W; ++k) {
+        s += sums[0][k];
+        es += sums[1][k];
+        eu += sums[2][k];
+      }
+      const float log_s = kLn2 * log2f(s);
+      if (a.lse) a.lse[r] = fmaf(mc, kLn2, log_s);
+      if (a.loss) a.loss[r] = mu == -INFINITY ? 0.f : a.tau * a.tau * (eu / es - kLn2 * log2f(es) + log_s);
     }
-    __syncthreads();   // the list is written again
+    // the next row's exchanges write `maxima` after this barrier's reads of it, and `sums` after its own first barrier
   }
 }
 
@@ -150,67 +187,131 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
 // Backward: a block writes a part of a row, the softmax first and then, over
 // it, the elements that the teacher lists.  dz may be z: a block reads what it
 // needs of its part before it writes there, and no other block reads it.
+// An id that is listed more than once is written by its first entry, which
+// adds up the p of all in their order.
 template <class T, int B>
 __global__ __launch_bounds__(B) void k_distill_backward(DistillBackward a, int parts) {
-  constexpr int V = kVec<T>, W = B / 64, U = 4;
-  __shared__ Teacher t;
-  __shared__ float listed[kMaxTop];
-  __shared__ float red[W];
+  constexpr int V = kVec<T>, W = B / 64, U = 4, NE = kMaxTop / B;
+  __shared__ int4 ids4[kMaxTop / 4];   // -1: absent
+  __shared__ float prob[kMaxTop];
+  __shared__ float maxima[W], sums[W];
+  int* ids = reinterpret_cast<int*>(ids4);
   const int64_t n = a.cols;
   const int64_t width = ((n + parts - 1) / parts + V - 1) / V * V;
   const int64_t units = a.rows * parts;
-  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int64_t r = unit / parts, first = (unit - r * parts) * width, last = std::min<int64_t>(n, first + width);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int64_t turn = blockIdx.x; turn < units; turn += gridDim.x) {
+    const int64_t unit = units - 1 - turn;
+    const int64_t r = unit / parts, first = std::min<int64_t>(n, (unit - r * parts) * width), last = std::min<int64_t>(n, first + width);
     const T* z = static_cast<const T*>(a.z) + r * a.ldz;
     T* dz = static_cast<T*>(a.dz) + r * a.lddz;
-    float top_u, log_sum;
-    const bool some = load_teacher<B>(t, red, a.ids, a.u, r, a.ldi, a.ldu, a.top, n, a.id_bytes, a.udtype, a.inv_tau, top_u, log_sum);
-    if (!some) {
-      for (int64_t j = first + threadIdx.x * V; j < last; j += int64_t(B) * V) store_pack<T, V>(dz, j, last, Pack<T, V>{});
-      __syncthreads();
-      continue;
-    }
     const float lse = a.lse[r], scale = a.dloss[r * a.lddl] * a.tau;
-    auto grad = [&](float x) { return exp2_hw(fmaf(x, a.inv_tau, -lse) * kLog2e); };
-    // the entries in this part: the first of those with one id takes them all
-    unsigned mine = 0;   // this thread's such entries
-    for (int k = threadIdx.x; k < a.top; k += B) {
-      const int id = t.id[k];
-      if (id < first || id >= last) continue;
-      float p = 0.f;
-      int lead = k;
-      for (int j = 0; j < a.top; ++j)
-        if (t.id[j] == id) {
-          if (j < lead) lead = j;
-          p += exp2_hw((t.p[j] - top_u - log_sum) * kLog2e);
+
+    float u[NE], mine[NE];   // mine: the element that the entry writes
+    float top_u = -INFINITY;
+    bool nan = false;
+    unsigned writes = 0;     // this thread's entries that write
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      u[e] = -INFINITY;
+      mine[e] = 0.f;
+      const int k = e * B + int(threadIdx.x);
+      if (k < a.top) {
+        const Entry t = load_entry(a, r, k);
+        u[e] = t.u;
+        ids[k] = t.u != -INFINITY ? int(t.id) : -1;
+        if (t.u != -INFINITY && t.id >= first && t.id < last) {
+          mine[e] = to_f32(z[t.id]);
+          writes |= 1u << e;
         }
-      if (lead != k) continue;
-      listed[k] = scale * (grad(to_f32(z[id])) - p);
-      mine |= 1u << (k / B);
+        top_u = fmaxf(top_u, t.u);
+        nan |= t.u != t.u;
+      } else if (k < (a.top + 3) / 4 * 4) {
+        ids[k] = -1;
+      }
     }
+    if (nan) top_u = INFINITY;   // gives NaN below
+    top_u = lanes_reduce<64>(top_u, Max());
+    if (lane == 0) maxima[wave] = top_u;
     __syncthreads();
-    int64_t j = first + threadIdx.x * V;
-    for (; j + int64_t(U - 1) * B * V + V <= last; j += int64_t(U) * B * V) {
+    top_u = maxima[0];
+#pragma unroll
+    for (int k = 1; k < W; ++k) top_u = fmaxf(top_u, maxima[k]);
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const int k = e * B + int(threadIdx.x);
+      if (k < a.top) {
+        const float p = u[e] == -INFINITY ? 0.f : exp2_hw((u[e] - top_u) * kLog2e);
+        prob[k] = p;
+        sum += p;
+      }
+    }
+    sum = lanes_sum<64>(sum);
+    if (lane == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = sums[0];
+#pragma unroll
+    for (int k = 1; k < W; ++k) sum += sums[k];
+
+    const bool some = top_u != -INFINITY;
+    const auto softmax = [&](float x) { return exp2_hw(fmaf(x, a.inv_tau, -lse) * kLog2e); };
+    const auto grad = [&](float x) { return from_f32<T>(some ? scale * softmax(x) : 0.f); };
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (writes >> e & 1) {
+        const int k = e * B + int(threadIdx.x), id = ids[k];
+        int equal = 0;
+        for (int q = 0; q < (a.top + 3) / 4; ++q) {
+          const int4 o = ids4[q];
+          equal += (o.x == id) + (o.y == id) + (o.z == id) + (o.w == id);
+        }
+        float p = prob[k];
+        if (equal > 1) {   // listed more than once
+          p = 0.f;
+          for (int q = 0; q < a.top; ++q)
+            if (ids[q] == id) {
+              if (q < k) writes &= ~(1u << e);
+              p += prob[q];
+            }
+        }
+        mine[e] = scale * (softmax(mine[e]) - p / sum);
+      }
+    __syncthreads();   // the listed logits of this part are read: dz may be z
+
+    const auto [lead, vecs] = cut_at_16(z + first, last - first);
+    const Pack<T, V>* zv = reinterpret_cast<const Pack<T, V>*>(z + first + lead);
+    Pack<T, V>* dv = reinterpret_cast<Pack<T, V>*>(dz + first + lead);
+    int64_t j = threadIdx.x;
+    for (; j + (U - 1) * B < vecs; j += U * B) {
       Pack<T, V> p[U];
 #pragma unroll
-      for (int k = 0; k < U; ++k) p[k] = *reinterpret_cast<const Pack<T, V>*>(z + j + int64_t(k) * B * V);
+      for (int k = 0; k < U; ++k) p[k] = load_stream(zv + j + k * B);
+#pragma unroll
+      for (int k = 0; k < U; ++k) settle(p[k]);
 #pragma unroll
       for (int k = 0; k < U; ++k) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[k].v[i] = from_f32<T>(scale * grad(to_f32(p[k].v[i])));
-        *reinterpret_cast<Pack<T, V>*>(dz + j + int64_t(k) * B * V) = p[k];
+        for (int i = 0; i < V; ++i) p[k].v[i] = grad(to_f32(p[k].v[i]));
+        store_stream(dv + j + k * B, p[k]);
       }
     }
-    for (; j < last; j += int64_t(B) * V) {
-      Pack<T, V> p = load_pack<T, V>(z, j, last);
+    for (; j < vecs; j += B) {
+      Pack<T, V> p = zv[j];
 #pragma unroll
-      for (int i = 0; i < V; ++i) p.v[i] = from_f32<T>(scale * grad(to_f32(p.v[i])));
-      store_pack<T, V>(dz, j, last, p);
+      for (int i = 0; i < V; ++i) p.v[i] = grad(to_f32(p.v[i]));
+      dv[j] = p;
     }
+    const int64_t tail = lead + vecs * V;
+    if (int64_t(threadIdx.x) < lead + (last - first) - tail) {
+      const int64_t i = first + (int64_t(threadIdx.x) < lead ? int64_t(threadIdx.x) : tail + threadIdx.x - lead);
+      dz[i] = grad(to_f32(z[i]));
+    }
+    __syncthreads();   // the softmax is written; the list is written again after this
+#pragma unroll
+    for (int e = 0; e < NE; ++e)
+      if (writes >> e & 1) dz[ids[e * B + int(threadIdx.x)]] = from_f32<T>(mine[e]);
     __syncthreads();
-    for (int k = threadIdx.x; k < a.top; k += B)
-      if (mine >> (k / B) & 1) dz[t.id[k]] = from_f32<T>(listed[k]);
-    __syncthreads();   // the list is written again
   }
 }
 
@@ -228,7 +329,7 @@ hipError_t launch_distill_forward(const DistillForward& a, hipStream_t s) {
   return with_type(a.dtype, [&](auto t) {
     using T = decltype(t);
     const dim3 grid(unsigned(std::min<int64_t>(a.rows, 1 << 20)));
-    if (a.cols >= 8192) k_distill_forward<T, 512><<<grid, dim3(512), 0, s>>>(a);
+    if (a.cols >= kLongRow) k_distill_forward<T, 512><<<grid, dim3(512), 0, s>>>(a);
     else k_distill_forward<T, 128><<<grid, dim3(128), 0, s>>>(a);
     return hipGetLastError();
   });
@@ -241,7 +342,8 @@ hipError_t launch_distill_backward(const DistillBackward& a, hipStream_t s) {
     // few rows: several blocks a row
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(512 / a.rows, (a.cols + 8191) / 8192));
     const dim3 grid(unsigned(std::min<int64_t>(a.rows * parts, 1 << 20)));
-    k_distill_backward<T, 256><<<grid, dim3(256), 0, s>>>(a, int(parts));
+    if (a.cols >= kLongRow) k_distill_backward<T, 512><<<grid, dim3(512), 0, s>>>(a, int(parts));
+    else k_distill_backward<T, 128><<<grid, dim3(128), 0, s>>>(a, int(parts));
     return hipGetLastError();
   });
 }

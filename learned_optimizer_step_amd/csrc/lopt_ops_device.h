@@ -68,6 +68,20 @@ __device__ __forceinline__ void store_pack(T* row, int64_t c, int64_t n, const P
   }
 }
 
+// A 16-byte vector that is read or written once: with the non-temporal hint it
+// takes no room in the caches from what is read again.
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(2)));
+template <class T, int N>
+__device__ __forceinline__ Pack<T, N> load_stream(const Pack<T, N>* p) {
+  static_assert(sizeof(T) * N == 16, "");
+  return __builtin_bit_cast(Pack<T, N>, __builtin_nontemporal_load(reinterpret_cast<const Words4*>(p)));
+}
+template <class T, int N>
+__device__ __forceinline__ void store_stream(Pack<T, N>* p, const Pack<T, N>& x) {
+  static_assert(sizeof(T) * N == 16, "");
+  __builtin_nontemporal_store(__builtin_bit_cast(Words4, x), reinterpret_cast<Words4*>(p));
+}
+
 // A row of n elements cut into vectors of V, one at column c = V, 2 V, ... for
 // each thread, so that loads need no branch (branches around loads make the
 // compiler wait for each one):
