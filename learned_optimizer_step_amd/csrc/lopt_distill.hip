@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "lopt_ops.h"
 #include "lopt_ops_device.h"
@@ -25,8 +26,6 @@ namespace {
 // 50257 bf16, 412 MB: 68 + 146 us; no hints and the same order in both 117 +
 // 153; hints on all reads 67 + 163; kept bytes of 100 to 250 MB within 2 %).
 constexpr int64_t kKeptBytes = 200'000'000;
-constexpr int64_t kLongRow = 4096;   // columns from which a block has 512 threads, 128 below
-
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -68,9 +67,9 @@ __device__ __forceinline__ Cut cut_at_16(const T* z, int64_t n) {
 // list's, e_k = exp((u_k - u') / tau), E their sum and s = sum exp((z - m) / tau):
 //   loss / tau^2 = sum_k e_k ((u_k - u') - (z_(i_k) - m)) / tau / E - log E + log s,
 // small terms all of them, whatever the logits' common offset is.
-template <class T, int B>
+template <class T, int B, int NE>
 __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
-  constexpr int V = kVec<T>, W = B / 64, U = 4, NE = kMaxTop / B;
+  constexpr int V = kVec<T>, W = B / 64, U = 4;
   __shared__ float maxima[2][W], sums[3][W];
   const int64_t n = a.cols;
   const float c = a.inv_tau * kLog2e;
@@ -189,11 +188,11 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
 // needs of its part before it writes there, and no other block reads it.
 // An id that is listed more than once is written by its first entry, which
 // adds up the p of all in their order.
-template <class T, int B>
+template <class T, int B, int NE>
 __global__ __launch_bounds__(B) void k_distill_backward(DistillBackward a, int parts) {
-  constexpr int V = kVec<T>, W = B / 64, U = 4, NE = kMaxTop / B;
-  __shared__ int4 ids4[kMaxTop / 4];   // -1: absent
-  __shared__ float prob[kMaxTop];
+  constexpr int V = kVec<T>, W = B / 64, U = 4;
+  __shared__ int4 ids4[NE * B / 4];   // -1: absent
+  __shared__ float prob[NE * B];
   __shared__ float maxima[W], sums[W];
   int* ids = reinterpret_cast<int*>(ids4);
   const int64_t n = a.cols;
@@ -324,13 +323,32 @@ hipError_t with_type(int32_t dtype, F&& f) {
 
 }  // namespace
 
+// Calls f(threads, entries a thread) for `units` rows or parts of `cols`
+// logits and lists of `top`.  Small blocks keep more rows in flight where a
+// row is short next to its exchanges (9000 x 3000 bf16, forward + backward:
+// 16 + 30 us with 64 or 128 threads, 18 + 46 with 256, 32 + 76 with 512; 6000 x
+// 12000: 32 + 63, 29 + 61, 26 + 51, 33 + 60); with too few rows for the chip
+// large ones (1 x 50257: 8 us with 128, 4 with 512).
+template <class F>
+void with_block(int64_t units, int64_t cols, int top, F&& f) {
+  const auto entries = [&](auto b) {
+    if (top <= b()) f(b, std::integral_constant<int, 1>());
+    else f(b, std::integral_constant<int, kMaxTop / b()>());
+  };
+  int threads = cols < 2048 ? 64 : cols < 8192 ? 128 : cols < 32768 ? 256 : 512;
+  while (threads < 512 && units * threads < 256 * 512 && cols > threads * 16) threads *= 2;
+  if (threads == 64) entries(std::integral_constant<int, 64>());
+  else if (threads == 128) entries(std::integral_constant<int, 128>());
+  else if (threads == 256) entries(std::integral_constant<int, 256>());
+  else entries(std::integral_constant<int, 512>());
+}
+
 hipError_t launch_distill_forward(const DistillForward& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
   return with_type(a.dtype, [&](auto t) {
     using T = decltype(t);
     const dim3 grid(unsigned(std::min<int64_t>(a.rows, 1 << 20)));
-    if (a.cols >= kLongRow) k_distill_forward<T, 512><<<grid, dim3(512), 0, s>>>(a);
-    else k_distill_forward<T, 128><<<grid, dim3(128), 0, s>>>(a);
+    with_block(a.rows, a.cols, a.top, [&](auto b, auto ne) { k_distill_forward<T, b(), ne()><<<grid, dim3(b()), 0, s>>>(a); });
     return hipGetLastError();
   });
 }
@@ -342,8 +360,7 @@ hipError_t launch_distill_backward(const DistillBackward& a, hipStream_t s) {
     // few rows: several blocks a row
     const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(512 / a.rows, (a.cols + 8191) / 8192));
     const dim3 grid(unsigned(std::min<int64_t>(a.rows * parts, 1 << 20)));
-    if (a.cols >= kLongRow) k_distill_backward<T, 512><<<grid, dim3(512), 0, s>>>(a, int(parts));
-    else k_distill_backward<T, 128><<<grid, dim3(128), 0, s>>>(a, int(parts));
+    with_block(a.rows * parts, a.cols, a.top, [&](auto b, auto ne) { k_distill_backward<T, b(), ne()><<<grid, dim3(b()), 0, s>>>(a, int(parts)); });
     return hipGetLastError();
   });
 }
