@@ -15,7 +15,7 @@
 namespace lopt {
 namespace {
 
-template <class T, class L, bool RMS, bool TAIL>
+template <class T, class L, bool RMS, int MODE>
 __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
   constexpr int V = kVec<T>, NV = L::E / V, E = L::E;
   __shared__ float red[2][L::TPR > 64 ? L::TPR / 64 : 1][2];
@@ -25,7 +25,8 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
   const float inv_n = 1.f / float(n);
 
   float w[E], dw[E], db[RMS ? 1 : E];
-  load_weights<L, V>(a.w, a.wdtype, lane, n, 1.f, w);
+  RowAt<T, L, MODE> at(lane, n);
+  load_weights(at, a.w, a.wdtype, 1.f, w);
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     dw[e] = 0.f;
@@ -42,24 +43,20 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     const float mean = RMS ? 0.f : a.mean[rr], rstd = a.rstd[rr];
     float xh[E], g[E];
     float v[2] = {0.f, 0.f};
+    Pack<T, V> px[NV], pg[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * L::TPR + lane) * V;
-      Pack<T, V> px, pg;
-      if (TAIL) {
-        px = load_pack<T, V>(xr, c, n);
-        pg = load_pack<T, V>(gr, c, n);
-      } else {
-        px = c < n ? *reinterpret_cast<const Pack<T, V>*>(xr + c) : Pack<T, V>{};
-        pg = c < n ? *reinterpret_cast<const Pack<T, V>*>(gr + c) : Pack<T, V>{};
-      }
+      px[k] = at[k].load(xr);
+      pg[k] = at[k].load(gr);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const bool in = row && c + (TAIL ? i : 0) < n;
-        xh[k * V + i] = in ? (to_f32(px.v[i]) - mean) * rstd : 0.f;
-        g[k * V + i] = in ? to_f32(pg.v[i]) : 0.f;
+        const bool own = row && at[k].own(i);
+        xh[k * V + i] = own ? (to_f32(px[k].v[i]) - mean) * rstd : 0.f;
+        g[k * V + i] = own ? to_f32(pg[k].v[i]) : 0.f;
       }
-    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       dw[e] = fmaf(g[e], xh[e], dw[e]);
@@ -75,12 +72,9 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     T* dr = static_cast<T*>(a.dx) + r * a.lddx;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * L::TPR + lane) * V;
-      Pack<T, V> p;
 #pragma unroll
-      for (int i = 0; i < V; ++i) p.v[i] = from_f32<T>(rstd * (g[k * V + i] - fmaf(xh[k * V + i], c1, c2)));
-      if (TAIL) store_pack<T, V>(dr, c, n, p);
-      else if (c < n) *reinterpret_cast<Pack<T, V>*>(dr + c) = p;
+      for (int i = 0; i < V; ++i) px[k].v[i] = from_f32<T>(rstd * (g[k * V + i] - fmaf(xh[k * V + i], c1, c2)));
+      at[k].store(dr, px[k]);
     }
   }
   if (!a.dw && !a.db) return;
@@ -93,15 +87,15 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (k * L::TPR + lane) * V + i;
-        if (c < n) {
+        const int c = at[k].at + i;
+        if (at[k].own(i)) {
           out[c] = dw[k * V + i];
           if (!RMS) out[n + c] = db[k * V + i];
         }
       }
   } else {
     constexpr int LPW = L::TPR < 64 ? L::TPR : 64;   // lanes of a wave with columns of their own
-    __shared__ float sums[RMS ? 1 : 2][E * LPW];
+    __shared__ float sums[RMS ? 1 : 2][GROUPS][E * LPW];
     if constexpr (LPW == 8)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -109,23 +103,24 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
         if (!RMS) db[e] = groups_sum(db[e]);
       }
     const int wave = threadIdx.x >> 6;
-    for (int g = 0; g < GROUPS; ++g) {
-      if (wave == g && (threadIdx.x & 63) < LPW)
+    if ((threadIdx.x & 63) < LPW)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float& s = sums[0][e * LPW + lane];
-          s = g == 0 ? dw[e] : s + dw[e];
-          if (!RMS) {
-            float& t = sums[RMS ? 0 : 1][e * LPW + lane];
-            t = g == 0 ? db[e] : t + db[e];
-          }
-        }
-      __syncthreads();
-    }
+      for (int e = 0; e < E; ++e) {
+        sums[0][wave][e * LPW + lane] = dw[e];
+        if (!RMS) sums[RMS ? 0 : 1][wave][e * LPW + lane] = db[e];
+      }
+    __syncthreads();
+    // a column is the own element of the thread and vector that it falls to; the last vector of kTail has moved back
+    const int moved = MODE == kTail ? (n + V - 1) / V * V - n : 0;
     for (int c = threadIdx.x; c < n; c += L::BLOCK) {
-      const int vec = c / V, at = ((vec / LPW) * V + c % V) * LPW + vec % LPW;
-      out[c] = sums[0][at];
-      if (!RMS) out[n + c] = sums[RMS ? 0 : 1][at];
+      const int vec = c / V, i = c % V + (vec == n / V ? moved : 0), at = ((vec / LPW) * V + i) * LPW + vec % LPW;
+#pragma unroll
+      for (int k = 0; k < (RMS ? 1 : 2); ++k) {
+        float t = sums[k][0][at];
+#pragma unroll
+        for (int g = 1; g < GROUPS; ++g) t += sums[k][g][at];
+        out[k * n + c] = t;
+      }
     }
   }
 }
@@ -226,10 +221,11 @@ __global__ __launch_bounds__(1024) void k_norm_weight_grad(NormBackward a, int64
 int64_t norm_backward_blocks(int64_t rows, int64_t cols) {
   if (rows <= 0) return 0;
   if (cols > kLongestRow) return std::min<int64_t>(rows, 64);
-  return with_layout(cols, [&](auto l) {
+  return with_backward_layout(cols, [&](auto l) {
     using L = decltype(l);
-    const int64_t rounds = 4, need = (rows + L::ROWS * rounds - 1) / (L::ROWS * rounds);
-    return std::min<int64_t>(need, int64_t(1024) * 256 / L::BLOCK);
+    // two rounds of rows a block (fewer sums to join) once every compute unit has a block
+    const int64_t need = (rows + L::ROWS - 1) / L::ROWS, cap = int64_t(1024) * 256 / L::BLOCK;
+    return std::min<int64_t>(std::max<int64_t>(std::min<int64_t>(need, 256), (need + 1) / 2), cap);
   });
 }
 
@@ -247,14 +243,13 @@ hipError_t launch_norm_backward(const NormBackward& a, hipStream_t s) {
         }
         return hipGetLastError();
       }
-      return with_layout(a.cols, [&](auto l) {
+      return with_backward_layout(a.cols, [&](auto l) {
         using L = decltype(l);
         const dim3 grid{unsigned(blocks)}, block{L::BLOCK};
-        const bool tail = a.cols % kVec<T> != 0;
-        if (a.rms && tail) k_norm_backward<T, L, true, true><<<grid, block, 0, s>>>(a);
-        else if (a.rms) k_norm_backward<T, L, true, false><<<grid, block, 0, s>>>(a);
-        else if (tail) k_norm_backward<T, L, false, true><<<grid, block, 0, s>>>(a);
-        else k_norm_backward<T, L, false, false><<<grid, block, 0, s>>>(a);
+        with_mode<T, L>(a.cols, [&](auto mode) {
+          if (a.rms) k_norm_backward<T, L, true, mode()><<<grid, block, 0, s>>>(a);
+          else k_norm_backward<T, L, false, mode()><<<grid, block, 0, s>>>(a);
+        });
         return hipGetLastError();
       });
     });

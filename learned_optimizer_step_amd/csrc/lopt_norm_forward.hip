@@ -27,7 +27,7 @@ __device__ __forceinline__ Moments finish(float mean, float s1, float s2, float 
   return m;
 }
 
-template <class T, class L, bool TAIL>
+template <class T, class L, int MODE>
 __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
   constexpr int V = kVec<T>, NV = L::E / V;
   __shared__ float red[2][L::TPR > 64 ? L::TPR / 64 : 1][2];
@@ -36,10 +36,11 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
   const int n = int(a.cols);
   const float inv_n = 1.f / float(n);
 
+  RowAt<T, L, MODE> at(lane, n);
   // the weights stay in registers for all rows of the thread
   float w[L::E], b[L::E];
-  load_weights<L, V>(a.w, a.wdtype, lane, n, 1.f, w);
-  load_weights<L, V>(a.b, a.wdtype, lane, n, 0.f, b);
+  load_weights(at, a.w, a.wdtype, 1.f, w);
+  load_weights(at, a.b, a.wdtype, 0.f, b);
 
   const int64_t stride = int64_t(gridDim.x) * L::ROWS;
   // every thread of a block makes the same number of rounds (barriers inside)
@@ -49,17 +50,16 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
     const T* xr = static_cast<const T*>(a.x) + (row ? r : 0) * a.ldx;
     float x[L::E];
     float v[2] = {0.f, 0.f};
+    Pack<T, V> p[NV];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (k * L::TPR + lane) * V;
-      const Pack<T, V> p = TAIL ? load_pack<T, V>(xr, c, n)
-                                : (c < n ? *reinterpret_cast<const Pack<T, V>*>(xr + c) : Pack<T, V>{});
+    for (int k = 0; k < NV; ++k) p[k] = at[k].load(xr);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        x[k * V + i] = to_f32(p.v[i]);
-        v[0] += x[k * V + i];
+        x[k * V + i] = to_f32(p[k].v[i]);
+        v[0] += at[k].own(i) ? x[k * V + i] : 0.f;
       }
-    }
     float mean = 0.f;
     if (!a.rms) {
       row_sum(v);
@@ -70,11 +70,11 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = (k * L::TPR + lane) * V + (TAIL ? i : 0);
         float& d = x[k * V + i];
-        d = c < n ? d - mean : 0.f;
-        v[0] += d;
-        v[1] = fmaf(d, d, v[1]);
+        d -= mean;
+        const float o = at[k].own(i) ? d : 0.f;
+        v[0] += o;
+        v[1] = fmaf(o, o, v[1]);
       }
     row_sum(v);
     const Moments m = finish(mean, a.rms ? 0.f : v[0], v[1], inv_n, a.eps);
@@ -82,13 +82,10 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
     T* yr = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int c = (k * L::TPR + lane) * V;
-      Pack<T, V> p;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        p.v[i] = from_f32<T>(fmaf((x[k * V + i] - m.rest) * m.rstd, w[k * V + i], b[k * V + i]));
-      if (TAIL) store_pack<T, V>(yr, c, n, p);
-      else if (c < n) *reinterpret_cast<Pack<T, V>*>(yr + c) = p;
+        p[k].v[i] = from_f32<T>(fmaf((x[k * V + i] - m.rest) * m.rstd, w[k * V + i], b[k * V + i]));
+      at[k].store(yr, p[k]);
     }
     if (lane == 0) {
       if (a.mean) a.mean[r] = m.mean + m.rest;
@@ -160,12 +157,11 @@ hipError_t launch_norm_forward(const NormForward& a, hipStream_t s) {
       k_norm_forward_long<T><<<dim3(unsigned(a.rows < 4096 ? a.rows : 4096)), dim3(1024), 0, s>>>(a);
       return hipGetLastError();
     }
-    return with_layout(a.cols, [&](auto l) {
+    return with_forward_layout(a.cols, [&](auto l) {
       using L = decltype(l);
       const int64_t need = (a.rows + L::ROWS - 1) / L::ROWS, most = int64_t(2048) * 256 / L::BLOCK;
       const dim3 grid(unsigned(need < most ? need : most)), block(L::BLOCK);
-      if (a.cols % kVec<T>) k_norm_forward<T, L, true><<<grid, block, 0, s>>>(a);
-      else k_norm_forward<T, L, false><<<grid, block, 0, s>>>(a);
+      with_mode<T, L>(a.cols, [&](auto mode) { k_norm_forward<T, L, mode()><<<grid, block, 0, s>>>(a); });
       return hipGetLastError();
     });
   });

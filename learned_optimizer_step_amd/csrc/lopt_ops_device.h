@@ -95,9 +95,9 @@ inline int row_mode(int64_t n, int v) { return n < v ? kTiny : n % v ? kTail : k
 
 template <class T, int V, int MODE>
 struct RowVec {
-  int64_t c, at, n;   // the thread's columns begin at c; its vector is read at `at`
+  int c, at, n;   // the thread's columns begin at c; its vector is read at `at`
 
-  __device__ __forceinline__ RowVec(int64_t c_, int64_t n_) : c(c_), at(MODE == kTiny ? c_ : c_ < n_ - V ? c_ : n_ - V), n(n_) {}
+  __device__ __forceinline__ RowVec(int c_, int n_) : c(c_), at(MODE == kTiny ? c_ : c_ < n_ - V ? c_ : n_ - V), n(n_) {}
   // element i of the vector is the thread's own (column at + i)
   __device__ __forceinline__ bool own(int i) const {
     if (MODE == kWhole) return c < n;

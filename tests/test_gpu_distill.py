@@ -16,7 +16,9 @@ from ops_cases import CODE, TINY, TYPES, U, close, distill, rounding  # noqa: E4
 # (rows, vocabulary, entries, temperature)
 SHAPES = [(1, 1, 1, 1.0), (1, 2, 2, 2.0), (3, 7, 3, 0.5), (5, 64, 1, 1.0), (4, 513, 20, 2.0), (300, 1000, 8, 2.0),
           (2, 1001, 300, 1.0), (7, 4097, 33, 4.0), (2, 8191, 65, 0.7), (3, 8192, 1024, 1.0), (2, 50257, 32, 2.0),
-          (1, 130001, 100, 1.0), (600, 300, 5, 3.0)]
+          (1, 130001, 100, 1.0), (600, 300, 5, 3.0),
+          # every block size, with one and with more entries a thread
+          (2100, 900, 70, 1.0), (1100, 2100, 200, 1.0), (1030, 2500, 9, 2.0), (600, 8200, 300, 1.0), (520, 9001, 12, 0.5)]
 
 
 def make(rows, cols, top, t, ut, idt, seed, absent=0.2):
