@@ -19,9 +19,12 @@ namespace {
 // 16384: 31 against 19).
 constexpr int kSortBlock = 1024;
 constexpr int64_t kOneBlock = 8192;
+constexpr int64_t kMarkedRows = 262144;   // rows that one block marks
 constexpr int kTile = 1024;       // tokens a block of a longer sort takes at a time (4096: twice the time a pass)
 constexpr int kMaxTiles = 256;    // blocks of the sort
 constexpr int kDigits = 256;      // 8 bits a pass
+
+constexpr int64_t kFew = 128;     // tokens that k_embedding_few takes (77 of 1000 x 65: 5 us, 13 with a sort)
 
 // The sums: see k_embedding_sum.
 constexpr int kSumVec = 4;        // columns of a lane
@@ -78,12 +81,13 @@ __global__ __launch_bounds__(256) void k_embedding_forward(EmbeddingForward a) {
 struct Work {
   uint32_t *key[2], *val[2];   // tokens' rows and positions, by turns
   uint32_t* hist;              // [tiles][256] digits of a pass
-  unsigned char* touched;      // long lists: rows that some token names
+  unsigned char* touched;      // rows that some token names, if `marks`
   uint32_t* crossing;          // number of runs that cross a chunk's border, then the chunks they begin in
   float* part;                 // [chunks][2][cols]: sums of runs that cross a chunk's first / last token
   int64_t tiles, rounds, chunks;
   int32_t chunk;               // tokens of a chunk
   int32_t passes;
+  int32_t marks;
   int32_t sorted;              // which key and val hold the sorted tokens
   size_t bytes;
 };
@@ -115,7 +119,8 @@ Work layout(unsigned char* ws, int64_t n, int64_t rows, int64_t cols) {
     w.val[k] = reinterpret_cast<uint32_t*>(take(size_t(n) * 4));
   }
   w.hist = reinterpret_cast<uint32_t*>(take(size_t(w.tiles) * kDigits * 4));
-  w.touched = take(n <= kOneBlock ? 0 : size_t(rows));
+  w.marks = n > kOneBlock || rows <= kMarkedRows;   // one block takes long to clear the marks of more
+  w.touched = take(w.marks ? size_t(rows) : 0);
   w.crossing = reinterpret_cast<uint32_t*>(take(size_t(w.chunks + 1) * 4));
   w.part = reinterpret_cast<float*>(take(size_t(w.chunks) * 2 * size_t(cols) * 4));
   w.bytes = at;
@@ -123,27 +128,38 @@ Work layout(unsigned char* ws, int64_t n, int64_t rows, int64_t cols) {
 }
 
 // The sort's launches keep few compute units busy, so blocks behind the sort's
-// clear the gradient meanwhile.  A short list's one launch clears all of it
-// and the named rows are written again; a long list names much of the table,
-// so its first pass marks the rows, and the launches of the later passes clear
-// the others, a share each (65,536 tokens of 32,000 x 2048: 161 us for
-// everything with all rows cleared under the four launches).
+// clear the gradient meanwhile: see launch_embedding_backward.  What is written
+// here is not read again soon, and passes the caches by (65,536 tokens of
+// 32,000 x 2048: 150 us for everything with ordinary accesses, 135 so, 122 with
+// dout read that way too).
 struct Clear {
   uint16_t* to;             // 2-byte units
   int64_t row, ld;          // units of a row
   int64_t first, last;      // this launch's rows
-  const unsigned char* touched;   // NULL: clear every row
+  const unsigned char* touched;   // rows that some token names, which are left; NULL: clear every row
 };
 
-// The rows' 16-byte vectors in one sequence, 1024 neighbours a block and turn
-// (a wave a row instead takes twice as long); row and place in it are carried
-// along, as a division for each vector costs more than its store.
+// The rows' 16-byte vectors in one sequence, THREADS neighbours a block and
+// turn (a wave a row instead takes twice as long); row and place in it are
+// carried along, as a division for each vector costs more than its store.
+template <int THREADS>
 __device__ __forceinline__ void clear_block(const Clear& c, int64_t block, int64_t blocks) {
   constexpr int U = 4;
   const Pack<uint16_t, 8> zero{};
-  const int64_t per = (c.row + 7) / 8, step = blocks * kSortBlock, step_r = step / per, step_i = step - step_r * per;
-  const int64_t at = block * kSortBlock + threadIdx.x;
+  const int64_t per = (c.row + 7) / 8;
+  // within a turn, and from a turn's last to the next one's first
+  const int64_t step = THREADS, step_r = step / per, step_i = step - step_r * per;
+  const int64_t jump = (blocks * U - U + 1) * THREADS, jump_r = jump / per, jump_i = jump - jump_r * per;
+  const int64_t at = block * (THREADS * U) + threadIdx.x;
   int64_t r = c.first + at / per, i = at % per;
+  const auto go = [&](int64_t dr, int64_t di) {
+    r += dr;
+    i += di;
+    if (i >= per) {
+      i -= per;
+      ++r;
+    }
+  };
   while (r < c.last) {
     int64_t rs[U], is[U];
     bool skip[U];
@@ -152,23 +168,23 @@ __device__ __forceinline__ void clear_block(const Clear& c, int64_t block, int64
       rs[k] = r;
       is[k] = i;
       skip[k] = r >= c.last || (c.touched && c.touched[r]);
-      r += step_r;
-      i += step_i;
-      if (i >= per) {
-        i -= per;
-        ++r;
-      }
+      if (k + 1 < U) go(step_r, step_i);
     }
+    go(jump_r, jump_i);
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (!skip[k]) store_pack<uint16_t, 8>(c.to + rs[k] * c.ld, is[k] * 8, c.row, zero);
+    for (int k = 0; k < U; ++k) {
+      uint16_t* row = c.to + rs[k] * c.ld;
+      if (skip[k]) continue;
+      if (is[k] * 8 + 8 <= c.row) store_stream(reinterpret_cast<Pack<uint16_t, 8>*>(row + is[k] * 8), zero);
+      else store_pack<uint16_t, 8>(row, is[k] * 8, c.row, zero);
+    }
   }
 }
 
 // Digits of every tile; the first pass reads the ids.
 __global__ __launch_bounds__(kSortBlock) void k_embedding_digits(EmbeddingBackward a, Work w, int pass, Clear clear) {
   if (int64_t(blockIdx.x) >= w.tiles) {
-    clear_block(clear, blockIdx.x - w.tiles, gridDim.x - w.tiles);
+    clear_block<kSortBlock>(clear, blockIdx.x - w.tiles, gridDim.x - w.tiles);
     return;
   }
   __shared__ uint32_t hist[kDigits];
@@ -252,7 +268,7 @@ __device__ __forceinline__ void clear_counts(uint32_t (&count)[kSortWaves][kDigi
 template <int N>
 __global__ __launch_bounds__(kSortBlock) void k_embedding_sort(EmbeddingBackward a, Work w, Clear clear) {
   if (blockIdx.x > 0) {
-    clear_block(clear, blockIdx.x - 1, gridDim.x - 1);
+    clear_block<kSortBlock>(clear, blockIdx.x - 1, gridDim.x - 1);
     return;
   }
   __shared__ uint32_t count[kSortWaves][kDigits];
@@ -268,6 +284,14 @@ __global__ __launch_bounds__(kSortBlock) void k_embedding_sort(EmbeddingBackward
     val[j] = uint32_t(t);
   }
   if (threadIdx.x == 0) w.crossing[0] = 0;
+  if (w.marks && !a.accumulate) {
+    for (int64_t v = int64_t(threadIdx.x) * 16; v < a.rows; v += kSortBlock * 16)
+      store_pack<unsigned char, 16>(w.touched, v, a.rows, Pack<unsigned char, 16>{});
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (int64_t(key[j]) < a.rows) w.touched[key[j]] = 1;
+  }
   for (int pass = 0; pass < w.passes; ++pass) {
     clear_counts(count);
     __syncthreads();
@@ -310,7 +334,7 @@ __global__ __launch_bounds__(kSortBlock) void k_embedding_sort(EmbeddingBackward
 // lower digits and the earlier ones of its own.
 __global__ __launch_bounds__(kSortBlock) void k_embedding_place(EmbeddingBackward a, Work w, int pass, Clear clear) {
   if (int64_t(blockIdx.x) >= w.tiles) {
-    clear_block(clear, blockIdx.x - w.tiles, gridDim.x - w.tiles);
+    clear_block<kSortBlock>(clear, blockIdx.x - w.tiles, gridDim.x - w.tiles);
     return;
   }
   constexpr int N = kTile / kSortBlock;
@@ -452,7 +476,7 @@ __device__ __forceinline__ void sum_chunk(const EmbeddingBackward& a, const Work
   Pack<TD, V> p[U], q[U];
   const auto load = [&](Pack<TD, V>(&x)[U], int i0) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) x[j] = at.load(reinterpret_cast<const TD*>(dout + of_lane(from, i0 + j < n ? i0 + j : n - 1)));
+    for (int j = 0; j < U; ++j) x[j] = at.load_once(reinterpret_cast<const TD*>(dout + of_lane(from, i0 + j < n ? i0 + j : n - 1)));
   };
   load(q, first);
   for (int i0 = first; i0 < n; i0 += U) {
@@ -499,12 +523,70 @@ __device__ __forceinline__ void sum_chunk(const EmbeddingBackward& a, const Work
 // the rows cleared before leave the 256 MB memory-side cache meanwhile, 500 MB
 // in all at 5.3 TB/s.  Half the width, which fits that cache, takes 38.
 template <class TD, class TG, int MODE>
-__global__ __launch_bounds__(256) void k_embedding_sum(EmbeddingBackward a, Work w) {
+__global__ __launch_bounds__(256) void k_embedding_sum(EmbeddingBackward a, Work w, int64_t sum_blocks, Clear clear) {
+  if (int64_t(blockIdx.x) >= sum_blocks) {
+    clear_block<256>(clear, blockIdx.x - sum_blocks, gridDim.x - sum_blocks);
+    return;
+  }
   constexpr int S = 64 * kSumVec;
   const int64_t slabs = (a.cols + S - 1) / S, units = w.chunks * slabs;
-  const int64_t step = int64_t(gridDim.x) * 4;
+  const int64_t step = sum_blocks * 4;
   for (int64_t unit = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); unit < units; unit += step)
     sum_chunk<TD, TG, MODE>(a, w, unit / slabs, unit % slabs * S);
+}
+
+// A handful of tokens (at most 128) of a small table, in one launch without a
+// sort: each wave holds all ids, two a lane.  The wave of the first token of a
+// row (and a slab of columns) adds up the row's tokens; waves behind those
+// clear the rows that no token names.
+template <class TD, class TG, int MODE>
+__global__ __launch_bounds__(256) void k_embedding_few(EmbeddingBackward a, int64_t sum_waves) {
+  constexpr int V = kSumVec, U = 4, VG = kVec<TG>;
+  const int lane = threadIdx.x & 63, n = int(a.n_ids);
+  const uint32_t none = uint32_t(a.rows);
+  const uint32_t lo = lane < n ? row_of(a.ids, a.id_bytes, lane, a.row0, a.rows) : none;
+  const uint32_t hi = 64 + lane < n ? row_of(a.ids, a.id_bytes, 64 + lane, a.row0, a.rows) : none;
+  const int64_t wave = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (wave >= sum_waves) {
+    if (a.accumulate) return;   // the last block's waves without work
+    const Pack<TG, VG> zero{};
+    for (int64_t r = wave - sum_waves; r < a.rows; r += int64_t(gridDim.x) * 4 - sum_waves) {
+      if (__ballot(lo == uint32_t(r) || hi == uint32_t(r))) continue;
+      TG* row = static_cast<TG*>(a.dtable) + r * a.ldt;
+      for (int64_t c = lane * VG; c < a.cols; c += 64 * VG) store_pack<TG, VG>(row, c, a.cols, zero);
+    }
+    return;
+  }
+  const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
+  const int t = int(wave / slabs);
+  if (t >= n) return;
+  const uint32_t key = t < 64 ? __builtin_amdgcn_readlane(lo, t) : __builtin_amdgcn_readlane(hi, t - 64);
+  uint64_t same_lo = __ballot(lo == key), same_hi = __ballot(hi == key);
+  const int first = same_lo ? __builtin_ctzll(same_lo) : 64 + __builtin_ctzll(same_hi);
+  if (key == none || first != t) return;
+  const SlabVec<V, MODE> at(wave % slabs * (64 * V), lane * V, a.cols);
+  float acc[V] = {};
+  int left = __popcll(same_lo) + __popcll(same_hi);
+  while (left > 0) {
+    Pack<TD, V> p[U];
+    int i = 0;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (j < left) {   // the next token; behind the last one that one again
+        i = same_lo ? __builtin_ctzll(same_lo) : 64 + __builtin_ctzll(same_hi);
+        if (same_lo) same_lo &= same_lo - 1;
+        else same_hi &= same_hi - 1;
+      }
+      p[j] = at.load(static_cast<const TD*>(a.dout) + int64_t(i) * a.ldd);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (j < left)
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] += to_f32(p[j].v[k]);
+    left -= U;
+  }
+  store_row<TG>(a, static_cast<TG*>(a.dtable) + int64_t(key) * a.ldt, at, acc);
 }
 
 // Runs that cross chunks: one block a run and 256 columns adds up the chunks'
@@ -512,13 +594,18 @@ __global__ __launch_bounds__(256) void k_embedding_sum(EmbeddingBackward a, Work
 // comes in any order, each run's sum does not.
 constexpr int kJoinWaves = 4;
 template <class TG, int MODE>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_embedding_join(EmbeddingBackward a, Work w) {
+__global__ __launch_bounds__(64 * kJoinWaves) void k_embedding_join(EmbeddingBackward a, Work w, unsigned run_blocks, Clear clear) {
+  if (blockIdx.y >= run_blocks) {
+    clear_block<64 * kJoinWaves>(clear, int64_t(blockIdx.y - run_blocks) * gridDim.x + blockIdx.x,
+                                 int64_t(gridDim.y - run_blocks) * gridDim.x);
+    return;
+  }
   __shared__ float share[kJoinWaves][4][64];
   const uint32_t* skey = w.key[w.sorted];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const SlabVec<4, MODE> at(int64_t(blockIdx.x) * 256, lane * 4, a.cols);
   const uint32_t runs = w.crossing[0];
-  for (uint32_t i = blockIdx.y; i < runs; i += gridDim.y) {
+  for (uint32_t i = blockIdx.y; i < runs; i += run_blocks) {
     const int64_t chunk = w.crossing[1 + i];
     const uint32_t key = skey[(chunk + 1) * w.chunk - 1];
     // the last chunk with a sum of the run: more than kReach of its tokens; 64 guesses at a time, near ones first
@@ -591,52 +678,85 @@ hipError_t launch_embedding_backward(const EmbeddingBackward& a, hipStream_t s) 
   const bool one = a.n_ids <= kOneBlock;
   Clear clear{};
   const int64_t units = a.gdtype == kF32 ? 2 : 1;
+  const bool large = a.rows * a.cols * units >= (int64_t(8) << 20);   // 16 MB to clear
+  if (a.n_ids > 0 && a.n_ids <= kFew && (a.accumulate || !large)) {
+    return with_type(a.gdtype, [&](auto tg) {
+      return with_type(a.dtype, [&](auto td) {
+        using TG = decltype(tg);
+        using TD = decltype(td);
+        const int64_t sums = a.n_ids * ((a.cols + 64 * kSumVec - 1) / (64 * kSumVec));
+        const int64_t waves = sums + (a.accumulate ? 0 : std::min<int64_t>(a.rows, 8192));
+        const dim3 g(unsigned((waves + 3) / 4));
+        if (a.cols < kSumVec) k_embedding_few<TD, TG, kTiny><<<g, dim3(256), 0, s>>>(a, sums);
+        else k_embedding_few<TD, TG, kTail><<<g, dim3(256), 0, s>>>(a, sums);
+        return hipGetLastError();
+      });
+    });
+  }
   clear.to = static_cast<uint16_t*>(a.dtable);
   clear.row = a.cols * units;
   clear.ld = a.ldt * units;
-  // a long list of one pass (below 256 rows) has no later launch for it, and little to clear
-  const int64_t shares = one ? 1 : w.passes == 1 ? 2 : 2 * (w.passes - 1);
-  if (!one && w.passes > 1) clear.touched = w.touched;
-  auto grid = [&](int64_t share, int64_t sort_blocks) {
-    const bool any = share >= 0 && !a.accumulate;
-    clear.first = any ? a.rows * share / shares : 0;
-    clear.last = any ? a.rows * (share + 1) / shares : 0;
-    const int64_t per = int64_t(kSortBlock) * 8, vectors = (clear.last - clear.first) * ((clear.row + 7) / 8);
-    return dim3(unsigned(sort_blocks + std::min<int64_t>((vectors + per - 1) / per, 1024)));
+  // The next launch's share of the rows to clear, in 20ths of all, and the
+  // blocks of `threads` that clear them.  A short list's sort, sums and join
+  // take about 10, 8 and 4 us, and clear in that proportion (50,257 x 1024: 53
+  // us for everything with all of it in the sort's launch, 48 so); the sort's launch
+  // clears named rows too, which are written again later.  (77 tokens of 1000
+  // x 65: 13 us with all of it there, 18 otherwise.)  A long list names
+  // much of the table: its first pass marks the rows, those of the later ones
+  // clear the others.
+  int64_t done = 0;
+  const auto share = [&](int64_t twentieths, int64_t threads) {
+    clear.first = a.accumulate ? 0 : a.rows * done / 20;
+    done += twentieths;
+    clear.last = a.accumulate ? 0 : a.rows * done / 20;
+    const int64_t vectors = (clear.last - clear.first) * ((clear.row + 7) / 8);
+    return std::min<int64_t>((vectors + threads * 8 - 1) / (threads * 8), 1024 * 1024 / threads);
   };
+  const bool joins = w.chunks >= 2;
+  const bool later = one && w.marks && a.n_ids > 0 && large;
   const dim3 block(kSortBlock);
   if (one) {
-    const dim3 g = grid(0, 1);
+    const dim3 g(unsigned(1 + share(!later ? 20 : joins ? 9 : 11, kSortBlock)));
     if (a.n_ids <= kSortBlock) k_embedding_sort<1><<<g, block, 0, s>>>(a, w, clear);
     else if (a.n_ids <= 4 * kSortBlock) k_embedding_sort<4><<<g, block, 0, s>>>(a, w, clear);
     else k_embedding_sort<8><<<g, block, 0, s>>>(a, w, clear);
   } else {
+    // with one pass (below 256 rows) there is no later launch, and little to clear
+    const int launches = w.passes == 1 ? 2 : 2 * (w.passes - 1);
+    int launch = 0;
+    const auto next = [&](int pass) {
+      if (pass == 0 && w.passes > 1) return share(0, kSortBlock);
+      ++launch;
+      return share(20 * launch / launches - 20 * (launch - 1) / launches, kSortBlock);
+    };
+    if (w.passes > 1) clear.touched = w.touched;
     for (int pass = 0; pass < w.passes; ++pass) {
-      const int64_t share = w.passes == 1 ? 0 : 2 * (pass - 1);
-      dim3 g = grid(share, w.tiles);
+      dim3 g(unsigned(w.tiles + next(pass)));
       k_embedding_digits<<<g, block, 0, s>>>(a, w, pass, clear);
-      g = grid(share < 0 ? -1 : share + 1, w.tiles);
+      g = dim3(unsigned(w.tiles + next(pass)));
       k_embedding_place<<<g, block, 0, s>>>(a, w, pass, clear);
     }
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.n_ids == 0) return e;
+  clear.touched = w.touched;
   return with_type(a.gdtype, [&](auto tg) {
     using TG = decltype(tg);
     with_type(a.dtype, [&](auto td) {
       using TD = decltype(td);
       constexpr int V = kSumVec;
-      const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V);
-      const dim3 g(unsigned(std::min<int64_t>((w.chunks * slabs + 3) / 4, 1 << 20)));
+      const int64_t slabs = (a.cols + 64 * V - 1) / (64 * V), blocks = std::min<int64_t>((w.chunks * slabs + 3) / 4, 1 << 20);
+      const dim3 g(unsigned(blocks + share(!later ? 0 : joins ? 7 : 9, 256)));
       const int mode = row_mode(a.cols, V);
-      if (mode == kTiny) k_embedding_sum<TD, TG, kTiny><<<g, dim3(256), 0, s>>>(a, w);
-      else if (mode == kWhole) k_embedding_sum<TD, TG, kWhole><<<g, dim3(256), 0, s>>>(a, w);
-      else k_embedding_sum<TD, TG, kTail><<<g, dim3(256), 0, s>>>(a, w);
+      if (mode == kTiny) k_embedding_sum<TD, TG, kTiny><<<g, dim3(256), 0, s>>>(a, w, blocks, clear);
+      else if (mode == kWhole) k_embedding_sum<TD, TG, kWhole><<<g, dim3(256), 0, s>>>(a, w, blocks, clear);
+      else k_embedding_sum<TD, TG, kTail><<<g, dim3(256), 0, s>>>(a, w, blocks, clear);
     });
-    if (w.chunks >= 2) {
-      const dim3 g(unsigned((a.cols + 255) / 256), unsigned(std::min<int64_t>(w.chunks, 256)));
-      if (a.cols < 4) k_embedding_join<TG, kTiny><<<g, dim3(64 * kJoinWaves), 0, s>>>(a, w);
-      else k_embedding_join<TG, kTail><<<g, dim3(64 * kJoinWaves), 0, s>>>(a, w);
+    if (joins) {
+      const int64_t x = (a.cols + 255) / 256, runs = std::min<int64_t>(w.chunks, 256), c = share(later ? 4 : 0, 64 * kJoinWaves);
+      const dim3 g(unsigned(x), unsigned(runs + (c + x - 1) / x));
+      if (a.cols < 4) k_embedding_join<TG, kTiny><<<g, dim3(64 * kJoinWaves), 0, s>>>(a, w, unsigned(runs), clear);
+      else k_embedding_join<TG, kTail><<<g, dim3(64 * kJoinWaves), 0, s>>>(a, w, unsigned(runs), clear);
     }
     return hipGetLastError();
   });

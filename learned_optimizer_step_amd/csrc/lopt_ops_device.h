@@ -68,18 +68,21 @@ __device__ __forceinline__ void store_pack(T* row, int64_t c, int64_t n, const P
   }
 }
 
-// A 16-byte vector that is read or written once: with the non-temporal hint it
+// An 8- or 16-byte vector that is read or written once: with the non-temporal hint it
 // takes no room in the caches from what is read again.
-typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(2)));
+template <int BYTES>
+struct StreamWords {
+  typedef uint32_t type __attribute__((ext_vector_type(BYTES / 4), aligned(2)));
+};
 template <class T, int N>
 __device__ __forceinline__ Pack<T, N> load_stream(const Pack<T, N>* p) {
-  static_assert(sizeof(T) * N == 16, "");
-  return __builtin_bit_cast(Pack<T, N>, __builtin_nontemporal_load(reinterpret_cast<const Words4*>(p)));
+  typedef typename StreamWords<sizeof(T) * N>::type Words;
+  return __builtin_bit_cast(Pack<T, N>, __builtin_nontemporal_load(reinterpret_cast<const Words*>(p)));
 }
 template <class T, int N>
 __device__ __forceinline__ void store_stream(Pack<T, N>* p, const Pack<T, N>& x) {
-  static_assert(sizeof(T) * N == 16, "");
-  __builtin_nontemporal_store(__builtin_bit_cast(Words4, x), reinterpret_cast<Words4*>(p));
+  typedef typename StreamWords<sizeof(T) * N>::type Words;
+  __builtin_nontemporal_store(__builtin_bit_cast(Words, x), reinterpret_cast<Words*>(p));
 }
 
 // A row of n elements cut into vectors of V, one at column c = V, 2 V, ... for
@@ -158,9 +161,16 @@ struct SlabVec {
     return p;
   }
   template <class U>
-  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p) const {
+  __device__ __forceinline__ Pack<U, V> load_once(const U* row) const {
+    if constexpr (MODE == kTiny) return load(row);
+    else return load_stream(reinterpret_cast<const Pack<U, V>*>(row + base + off));
+  }
+  // `once`: it is not read again soon
+  template <class U>
+  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p, bool once = false) const {
     if (MODE != kTiny && c + V <= n) {
-      *reinterpret_cast<Pack<U, V>*>(row + base + off) = p;
+      if (once) store_stream(reinterpret_cast<Pack<U, V>*>(row + base + off), p);
+      else *reinterpret_cast<Pack<U, V>*>(row + base + off) = p;
     } else if (MODE != kWhole) {
 #pragma unroll
       for (int i = 0; i < V; ++i)

@@ -17,7 +17,10 @@ from ops_cases import CODE, TYPES, U, close, rounding  # noqa: E402
 # inside runs, widths around the slabs of 64 vectors
 SHAPES = [(1, 1, 1), (1, 7, 5), (3, 2, 64), (77, 1000, 65), (8, 255, 33), (64, 256, 8), (500, 257, 130), (4095, 300, 17),
           (4096, 65535, 20), (4097, 65536, 12), (9000, 70001, 8), (1024, 3, 257), (2000, 50257, 40), (5000, 1, 70),
-          (16384, 500, 12), (16385, 500, 12), (40000, 1000, 36), (333, 40, 513), (333, 40, 1030), (50, 20, 2048)]
+          (16384, 500, 12), (16385, 500, 12), (40000, 1000, 36), (333, 40, 513), (333, 40, 1030), (50, 20, 2048),
+          # a handful of tokens in one launch; tables of 16 MB and more, whose rows are cleared in several launches
+          (64, 30, 3), (65, 9, 70), (128, 50, 515), (129, 50, 515), (5, 50257, 130), (700, 50257, 130), (6000, 33000, 257),
+          (20000, 40000, 131), (9000, 100, 3)]
 
 
 def make_ids(n, rows, seed, kind):
@@ -63,7 +66,8 @@ def test_against_the_definition(n, rows, cols, t):
         want, size, count = dense(dout, ids, rows, torch.tensor(scale, dtype=torch.float32).double())
         # a term passes at most its row's tokens' additions, and the product
         close(dw, want, rounding(want, wt) + (count[:, None] + 2) * U * size, "dw")
-        assert torch.equal(dw, layers.embedding_backward(dout.cuda(), ids.to(idt).cuda(), rows, scale, dtype=wt))
+        filled = torch.full((rows, cols), math.nan, dtype=wt, device="cuda")     # whatever was there
+        assert torch.equal(dw, layers.embedding_backward(dout.cuda(), ids.to(idt).cuda(), rows, scale, out=filled))
 
 
 def test_long_runs_of_one_row():
@@ -96,9 +100,10 @@ def test_a_shard_of_the_table_and_rows_left_alone():
     assert torch.equal(layers.embedding_forward(ids + far, w, 2.0, row0=far), whole)
 
 
+@pytest.mark.parametrize("n", [1, 100, 700, 9000])
 @pytest.mark.parametrize("gt", TYPES, ids=str)
-def test_accumulating(gt):
-    n, rows, cols = 700, 5000, 72
+def test_accumulating(gt, n):
+    rows, cols = 5000, 72
     g = torch.Generator().manual_seed(4)
     ids = make_ids(n, rows, 9, "text").cuda()
     dout = torch.randn(n, cols, generator=g).bfloat16().cuda()
