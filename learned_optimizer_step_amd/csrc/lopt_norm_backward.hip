@@ -2,7 +2,10 @@
 // a = dy w, per row of n columns:
 //   dx = rstd (a - xh mean(a xh) - mean(a))      (RMS: without mean(a))
 //   dw = sum over rows of dy xh,  db = sum over rows of dy
-// Bound by HBM: x and dy are read once, dx is written once.  Each thread adds
+// Bound by HBM: x and dy are read once, dx is written once.  x and dy have no
+// further reader, and are read past the caches (65536 x 768 bf16: 64 to 56 us);
+// so is dx written if the memory-side cache could not hold it for its reader
+// (65536 x 2048 bf16 RMS, 268 MB: 147 to 140 us; 16384 x 2048: 46 to 51, not so).  Each thread adds
 // up dw and db of its columns over the rows of its block in registers; the
 // blocks' sums go to the workspace and a second kernel adds them in the order
 // of the blocks, so the result has the same bits every time.
@@ -34,6 +37,7 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
   }
 
   const int64_t stride = int64_t(gridDim.x) * L::ROWS;
+  const bool pass_by = a.rows * a.cols * int64_t(sizeof(T)) > 200'000'000;
   for (int64_t r0 = int64_t(blockIdx.x) * L::ROWS; r0 < a.rows; r0 += stride) {
     const int64_t r = r0 + threadIdx.x / L::TPR;
     const bool row = L::ROWS == 1 || r < a.rows;
@@ -46,8 +50,8 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     Pack<T, V> px[NV], pg[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      px[k] = at[k].load(xr);
-      pg[k] = at[k].load(gr);
+      px[k] = at[k].load_once(xr);
+      pg[k] = at[k].load_once(gr);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -74,7 +78,7 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int i = 0; i < V; ++i) px[k].v[i] = from_f32<T>(rstd * (g[k * V + i] - fmaf(xh[k * V + i], c1, c2)));
-      at[k].store(dr, px[k]);
+      at[k].store(dr, px[k], pass_by);
     }
   }
   if (!a.dw && !a.db) return;

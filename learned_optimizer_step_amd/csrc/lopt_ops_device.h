@@ -119,9 +119,16 @@ struct RowVec {
     return p;
   }
   template <class U = T>
-  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p) const {
+  __device__ __forceinline__ Pack<U, V> load_once(const U* row) const {
+    if constexpr (MODE == kTiny) return load(row);
+    else return load_stream(reinterpret_cast<const Pack<U, V>*>(row + at));
+  }
+  // `once`: it is not read again soon
+  template <class U = T>
+  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p, bool once = false) const {
     if (MODE != kTiny && c + V <= n) {
-      *reinterpret_cast<Pack<U, V>*>(row + at) = p;
+      if (once) store_stream(reinterpret_cast<Pack<U, V>*>(row + at), p);
+      else *reinterpret_cast<Pack<U, V>*>(row + at) = p;
     } else if (MODE != kWhole) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
