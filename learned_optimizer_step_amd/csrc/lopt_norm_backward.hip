@@ -18,7 +18,7 @@
 namespace lopt {
 namespace {
 
-template <class T, class L, bool RMS, int MODE>
+template <class T, class L, bool RMS, int MODE, bool PASS_BY = false>
 __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
   constexpr int V = kVec<T>, NV = L::E / V, E = L::E;
   __shared__ float red[2][L::TPR > 64 ? L::TPR / 64 : 1][2];
@@ -37,7 +37,6 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
   }
 
   const int64_t stride = int64_t(gridDim.x) * L::ROWS;
-  const bool pass_by = a.rows * a.cols * int64_t(sizeof(T)) > 200'000'000;
   for (int64_t r0 = int64_t(blockIdx.x) * L::ROWS; r0 < a.rows; r0 += stride) {
     const int64_t r = r0 + threadIdx.x / L::TPR;
     const bool row = L::ROWS == 1 || r < a.rows;
@@ -50,8 +49,13 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     Pack<T, V> px[NV], pg[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      px[k] = at[k].load_once(xr);
-      pg[k] = at[k].load_once(gr);
+      if constexpr (MODE == kWhole || PASS_BY) {
+        px[k] = at[k].load_once(xr);
+        pg[k] = at[k].load_once(gr);
+      } else {   // unaligned vectors share cache lines with their neighbours: 5003 x 1025 fp32 20 us, 23 past the caches
+        px[k] = at[k].load(xr);
+        pg[k] = at[k].load(gr);
+      }
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -78,7 +82,7 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_backward(NormBackward a) {
     for (int k = 0; k < NV; ++k) {
 #pragma unroll
       for (int i = 0; i < V; ++i) px[k].v[i] = from_f32<T>(rstd * (g[k * V + i] - fmaf(xh[k * V + i], c1, c2)));
-      at[k].store(dr, px[k], pass_by);
+      at[k].template store<PASS_BY>(dr, px[k]);
     }
   }
   if (!a.dw && !a.db) return;
@@ -250,6 +254,14 @@ hipError_t launch_norm_backward(const NormBackward& a, hipStream_t s) {
       return with_backward_layout(a.cols, [&](auto l) {
         using L = decltype(l);
         const dim3 grid{unsigned(blocks)}, block{L::BLOCK};
+        if constexpr (L::TPR > 8)
+          if (a.rows * a.cols * int64_t(sizeof(T)) > 200'000'000) {
+            with_mode<T, L>(a.cols, [&](auto mode) {
+              if (a.rms) k_norm_backward<T, L, true, mode(), true><<<grid, block, 0, s>>>(a);
+              else k_norm_backward<T, L, false, mode(), true><<<grid, block, 0, s>>>(a);
+            });
+            return hipGetLastError();
+          }
         with_mode<T, L>(a.cols, [&](auto mode) {
           if (a.rms) k_norm_backward<T, L, true, mode()><<<grid, block, 0, s>>>(a);
           else k_norm_backward<T, L, false, mode()><<<grid, block, 0, s>>>(a);

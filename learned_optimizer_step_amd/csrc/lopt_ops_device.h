@@ -123,11 +123,12 @@ struct RowVec {
     if constexpr (MODE == kTiny) return load(row);
     else return load_stream(reinterpret_cast<const Pack<U, V>*>(row + at));
   }
-  // `once`: it is not read again soon
-  template <class U = T>
-  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p, bool once = false) const {
+  // ONCE: it is not read again soon (known at compile time: of two stores that
+  // differ by the hint alone the compiler makes one without it)
+  template <bool ONCE = false, class U = T>
+  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p) const {
     if (MODE != kTiny && c + V <= n) {
-      if (once) store_stream(reinterpret_cast<Pack<U, V>*>(row + at), p);
+      if constexpr (ONCE) store_stream(reinterpret_cast<Pack<U, V>*>(row + at), p);
       else *reinterpret_cast<Pack<U, V>*>(row + at) = p;
     } else if (MODE != kWhole) {
 #pragma unroll
@@ -172,12 +173,10 @@ struct SlabVec {
     if constexpr (MODE == kTiny) return load(row);
     else return load_stream(reinterpret_cast<const Pack<U, V>*>(row + base + off));
   }
-  // `once`: it is not read again soon
   template <class U>
-  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p, bool once = false) const {
+  __device__ __forceinline__ void store(U* row, const Pack<U, V>& p) const {
     if (MODE != kTiny && c + V <= n) {
-      if (once) store_stream(reinterpret_cast<Pack<U, V>*>(row + base + off), p);
-      else *reinterpret_cast<Pack<U, V>*>(row + base + off) = p;
+      *reinterpret_cast<Pack<U, V>*>(row + base + off) = p;
     } else if (MODE != kWhole) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
