@@ -14,7 +14,9 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <algorithm>
 #include <optional>
+#include <stdexcept>
 #include <string>
 #include <tuple>
 
@@ -29,13 +31,13 @@ using torch::autograd::variable_list;
 using Maybe = std::optional<Tensor>;
 
 // A call that liblopt refused: lopt.LoptError in Python.
-struct Refused {
+struct Refused : std::runtime_error {
   int status;
-  std::string message;
+  Refused(int s, const char* message) : std::runtime_error(message), status(s) {}
 };
 
 void check(lopt_status s) {
-  if (s != LOPT_OK) throw Refused{int(s), lopt_last_error()};
+  if (s != LOPT_OK) throw Refused(int(s), lopt_last_error());
 }
 
 [[noreturn]] void bad(const std::string& message) { throw pybind11::value_error(message); }
@@ -356,7 +358,7 @@ PYBIND11_MODULE(_layers, m) {
       if (p) std::rethrow_exception(p);
     } catch (const Refused& e) {
       const py::object type = py::module_::import("learned_optimizer_step_amd.lopt").attr("LoptError");
-      PyErr_SetObject(type.ptr(), type(e.status, e.message).ptr());
+      PyErr_SetObject(type.ptr(), type(e.status, e.what()).ptr());
     }
   });
   m.def("norm_forward", [](const Tensor& x, const Maybe& w, const Maybe& b, double eps, bool rms) {

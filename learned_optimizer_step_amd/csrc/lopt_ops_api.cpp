@@ -4,9 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <cstring>
 #include <string>
-#include <vector>
 
 #include "../../include/lopt.h"
 #include "lopt_error.h"
@@ -40,13 +38,15 @@ struct Buffer {
 };
 
 struct Buffers {
-  std::vector<Buffer> list;
+  static constexpr size_t kMost = 12;   // no call has more
+  Buffer list[kMost];
+  size_t count = 0;
 
   void add(const char* name, const void* p, int64_t bytes, int64_t align, bool written) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     if (!p) fail(LOPT_ERR_INVALID_ARGUMENT, std::string(name) + " is NULL");
     if (a % uintptr_t(align)) fail(LOPT_ERR_UNSUPPORTED, std::string(name) + " is not aligned to its elements");
-    list.push_back({name, a, a + uintptr_t(bytes), written});
+    list[count++] = {name, a, a + uintptr_t(bytes), written};
   }
   // rows x cols elements of size `size`, rows `ld` elements apart
   void matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size, bool written) {
@@ -58,8 +58,8 @@ struct Buffers {
     add(name, p, ((rows - 1) * (rows > 1 ? ld : 0) + cols) * size, size, written);
   }
   void no_overlap() const {
-    for (size_t i = 0; i < list.size(); ++i)
-      for (size_t j = i + 1; j < list.size(); ++j) {
+    for (size_t i = 0; i < count; ++i)
+      for (size_t j = i + 1; j < count; ++j) {
         const Buffer &x = list[i], &y = list[j];
         if ((x.written || y.written) && x.a < y.b && y.a < x.b)
           fail(LOPT_ERR_INVALID_ARGUMENT, std::string(x.name) + " and " + y.name + " overlap");

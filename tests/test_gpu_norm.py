@@ -239,6 +239,26 @@ def test_on_another_stream_and_in_a_graph():
         assert all(torch.equal(p, q) for p, q in zip(eager + eager_grads, (y, mean, rstd, dx, gw, gb))), k
 
 
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("t,rows,cols", [(torch.float32, 50001, 1029), (torch.bfloat16, 13000, 8200)])
+def test_gradients_too_large_for_the_caches(t, rows, cols, rms):
+    """Over 200 MB the gradient is written another way; the last rows against the same rows alone."""
+    x, dy = torch.randn(rows, cols, device="cuda").to(t), torch.randn(rows, cols, device="cuda").to(t)
+    w = torch.randn(cols, device="cuda")
+    _, mean, rstd = layers.norm_forward(x, w, None, rms=rms)
+    dx, dw, db = layers.norm_backward(dy, x, w, mean, rstd, rms=rms)
+    for part in (slice(0, 90), slice(rows - 90, rows)):
+        m = None if rms else mean[part].clone()
+        want = layers.norm_backward(dy[part].clone(), x[part].clone(), w, m, rstd[part].clone(), rms=rms)[0]
+        assert torch.equal(dx[part], want)
+    xh = (x.double() - (0 if rms else mean.double()[:, None])) * rstd.double()[:, None]
+    terms = dy.double() * xh
+    # at most rows / 512 + 100 additions of a term
+    assert bool(((dw.double() - terms.sum(0)).abs() <= (rows // 512 + 100) * U * terms.abs().sum(0)).all())
+    if not rms:
+        assert bool(((db.double() - dy.double().sum(0)).abs() <= (rows // 512 + 100) * U * dy.double().abs().sum(0)).all())
+
+
 def test_more_elements_than_32_bits_count():
     """2^31 + elements (8.6 GB in, 8.6 GB out in bf16): the last rows against the same rows alone."""
     cols, rows = 2048, (1 << 20) + 3

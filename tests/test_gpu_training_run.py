@@ -152,6 +152,36 @@ def test_a_whole_step_in_one_graph():
     graphed.opt.close()
 
 
+def test_two_streams_at_once():
+    """The same operators on two streams that overlap, each with its own data: as one after the other."""
+    def work(seed, stream=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        n, vocab, dim = 9000 + seed, 3000, 256
+        ids = torch.randint(-1, vocab, (n,), generator=g, device="cuda")
+        x = torch.randn(n, dim, generator=g, device="cuda").bfloat16()
+        w = torch.randn(dim, generator=g, device="cuda")
+        z = torch.randn(700, 5000, generator=g, device="cuda").bfloat16()
+        tid = torch.randint(-1, 5000, (700, 40), generator=g, device="cuda")
+        tu = torch.randn(700, 40, generator=g, device="cuda")
+        torch.cuda.current_stream().synchronize()   # the inputs are there; the other stream may still run
+        with torch.cuda.stream(stream):
+            for _ in range(4):
+                y, mean, rstd = layers.norm_forward(x, w, w)
+                dx, dw, db = layers.norm_backward(x, x, w, mean, rstd)
+                dt = layers.embedding_backward(dx, ids, vocab, 2.0)
+                loss, lse = layers.distill_forward(z, tid, tu, 2.0)
+                dz = layers.distill_backward(loss, z, tid, tu, lse, 2.0)
+        return y, dx, dw, db, dt, loss, lse, dz
+
+    want = [work(1), work(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [work(1, streams[0]), work(2, streams[1])]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_distill_definition_of_the_tests():
     """The 64-bit definition that the distillation tests use, against torch's own operators."""
     ids, tid, tu = data(3)
