@@ -154,6 +154,8 @@ def test_a_whole_step_in_one_graph():
 
 def test_two_streams_at_once():
     """The same operators on two streams that overlap, each with its own data: as one after the other."""
+    keep = []   # the inputs belong to the default stream: they must outlive the other's work
+
     def work(seed, stream=None):
         g = torch.Generator(device="cuda").manual_seed(seed)
         n, vocab, dim = 9000 + seed, 3000, 256
@@ -163,6 +165,7 @@ def test_two_streams_at_once():
         z = torch.randn(700, 5000, generator=g, device="cuda").bfloat16()
         tid = torch.randint(-1, 5000, (700, 40), generator=g, device="cuda")
         tu = torch.randn(700, 40, generator=g, device="cuda")
+        keep.append((ids, x, w, z, tid, tu))
         torch.cuda.current_stream().synchronize()   # the inputs are there; the other stream may still run
         with torch.cuda.stream(stream):
             for _ in range(4):
@@ -179,7 +182,7 @@ def test_two_streams_at_once():
     got = [work(1, streams[0]), work(2, streams[1])]
     torch.cuda.synchronize()
     for a, b in zip(want, got):
-        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        assert [torch.equal(p, q) for p, q in zip(a, b)] == [True] * 8
 
 
 def test_distill_definition_of_the_tests():
