@@ -139,20 +139,37 @@ struct Clear {
   const unsigned char* touched;   // rows that some token names, which are left; NULL: clear every row
 };
 
-// The rows' 16-byte vectors in one sequence, THREADS neighbours a block and
-// turn (a wave a row instead takes twice as long); row and place in it are
-// carried along, as a division for each vector costs more than its store.
+__device__ __forceinline__ void clear_vector(const Clear& c, int64_t r, int64_t i) {
+  const Pack<uint16_t, 8> zero{};
+  uint16_t* row = c.to + r * c.ld;
+  if (i + 8 <= c.row) store_stream(reinterpret_cast<Pack<uint16_t, 8>*>(row + i), zero);
+  else store_pack<uint16_t, 8>(row, i, c.row, zero);
+}
+
+// The rows' 16-byte vectors in one sequence.  Every row: a vector a thread in
+// many short blocks, as a grid that stays and strides writes slower (206 MB:
+// 34 us, 41 with 1024 blocks).  Unmarked rows: a grid that strides and looks
+// up four marks at a time (65,536 tokens of 32,000 x 2048: 120 us for
+// everything, 130 with short blocks); row and place in it are carried along.
 template <int THREADS>
 __device__ __forceinline__ void clear_block(const Clear& c, int64_t block, int64_t blocks) {
+  const uint32_t per = uint32_t((c.row + 7) / 8), last = uint32_t(c.last);
+  if (!c.touched) {
+    const int64_t end = (c.last - c.first) * per;
+    for (int64_t at = block * THREADS + threadIdx.x; at < end; at += blocks * THREADS) {
+      const int64_t turn = at / per;
+      clear_vector(c, c.first + turn, (at - turn * per) * 8);
+    }
+    return;
+  }
   constexpr int U = 4;
-  const Pack<uint16_t, 8> zero{};
-  const int64_t per = (c.row + 7) / 8;
   // within a turn, and from a turn's last to the next one's first
-  const int64_t step = THREADS, step_r = step / per, step_i = step - step_r * per;
-  const int64_t jump = (blocks * U - U + 1) * THREADS, jump_r = jump / per, jump_i = jump - jump_r * per;
+  const uint32_t step_r = THREADS / per, step_i = THREADS - step_r * per;
+  const int64_t jump = (blocks * U - U + 1) * THREADS;
+  const uint32_t jump_r = uint32_t(jump / per), jump_i = uint32_t(jump - int64_t(jump_r) * per);
   const int64_t at = block * (THREADS * U) + threadIdx.x;
-  int64_t r = c.first + at / per, i = at % per;
-  const auto go = [&](int64_t dr, int64_t di) {
+  uint32_t r = uint32_t(c.first + at / per), i = uint32_t(at % per);
+  const auto go = [&](uint32_t dr, uint32_t di) {
     r += dr;
     i += di;
     if (i >= per) {
@@ -160,24 +177,20 @@ __device__ __forceinline__ void clear_block(const Clear& c, int64_t block, int64
       ++r;
     }
   };
-  while (r < c.last) {
-    int64_t rs[U], is[U];
+  while (r < last) {
+    uint32_t rs[U], is[U];
     bool skip[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
       rs[k] = r;
       is[k] = i;
-      skip[k] = r >= c.last || (c.touched && c.touched[r]);
+      skip[k] = r >= last || c.touched[r];
       if (k + 1 < U) go(step_r, step_i);
     }
     go(jump_r, jump_i);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      uint16_t* row = c.to + rs[k] * c.ld;
-      if (skip[k]) continue;
-      if (is[k] * 8 + 8 <= c.row) store_stream(reinterpret_cast<Pack<uint16_t, 8>*>(row + is[k] * 8), zero);
-      else store_pack<uint16_t, 8>(row, is[k] * 8, c.row, zero);
-    }
+    for (int k = 0; k < U; ++k)
+      if (!skip[k]) clear_vector(c, rs[k], int64_t(is[k]) * 8);
   }
 }
 
@@ -710,6 +723,7 @@ hipError_t launch_embedding_backward(const EmbeddingBackward& a, hipStream_t s) 
     done += twentieths;
     clear.last = a.accumulate ? 0 : a.rows * done / 20;
     const int64_t vectors = (clear.last - clear.first) * ((clear.row + 7) / 8);
+    if (!clear.touched) return std::min<int64_t>((vectors + threads - 1) / threads, 1 << 20);
     return std::min<int64_t>((vectors + threads * 8 - 1) / (threads * 8), 1024 * 1024 / threads);
   };
   const bool joins = w.chunks >= 2;
