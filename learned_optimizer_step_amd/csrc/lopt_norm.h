@@ -23,9 +23,9 @@ struct RowLayout {
 // Calls f(RowLayout) for the layout that holds rows of n columns (n <=
 // kLongestRow).  Above 2048 columns the passes differ: the forward pass has
 // registers to spare, so 16 elements a thread and more rows in flight (3000 x
-// 6000 bf16: 15.6 us with 512 threads a row, 19.7 with 1024; 20000 x 3001: 52
-// with 256, 62 with 512), the backward pass, with its sums, has not (32 us
-// with 1024, 39 with 512; 80 with 512, 87 with 256).
+// 6000 bf16: a fifth less time with 512 threads a row than with 1024; 20000 x
+// 3001: 15 % less with 256 than with 512); the backward pass, with its sums,
+// has not (a fifth less with 1024 than with 512; 8 % less with 512 than 256).
 template <class F>
 auto with_short_layout(int64_t n, F&& f) {
   if (n <= 64) return f(RowLayout<8, 8, 256>());     // eight rows in a wave
@@ -102,13 +102,13 @@ __device__ __forceinline__ void load_weights(const At& at, const void* p, int dt
 // Sums over the TPR threads of a row.  Across waves the sums go through LDS;
 // `turn` alternates two buffers, so one barrier a call is enough (a wave that
 // writes a buffer again has passed the barrier of the call between).
-template <int TPR, int N>
+template <int TPR, int N, class S = float>
 struct RowSum {
   static constexpr int W = TPR > 64 ? TPR / 64 : 1;
-  float (*red)[W][N];
+  S (*red)[W][N];
   int turn = 0;
 
-  __device__ __forceinline__ void operator()(float (&v)[N]) {
+  __device__ __forceinline__ void operator()(S (&v)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = lanes_sum<(TPR < 64 ? TPR : 64)>(v[i]);
     if constexpr (W > 1) {
@@ -119,10 +119,14 @@ struct RowSum {
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        float s = red[turn][0][i];
+        S t[W];
 #pragma unroll
-        for (int k = 1; k < W; ++k) s += red[turn][k][i];
-        v[i] = s;
+        for (int k = 0; k < W; ++k) t[k] = red[turn][k][i];
+#pragma unroll
+        for (int o = 1; o < W; o *= 2)
+#pragma unroll
+          for (int k = 0; k < W; k += 2 * o) t[k] += t[k + o];
+        v[i] = t[0];
       }
       turn ^= 1;
     }

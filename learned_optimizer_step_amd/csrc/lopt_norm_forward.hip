@@ -9,29 +9,40 @@
 namespace lopt {
 namespace {
 
-// One rounding of x's mean costs |mu| 2^-24, which is much of the spread of a
-// row far from zero: the second sum also adds up x - mu, and its mean goes
-// into mu, the spread and the output.
+// The mean comes from a sum in 64 bits: fp32's would be off by 2^-24 of the
+// values' size, which is much of the spread of a row far from zero, and much of
+// a mean that cancels (65536 x 200 fp32: 27 us, 20 with fp32 sums; bf16, whose
+// threads add in fp32 without roundings, within a few %).  What fp32 cannot hold of it goes into the spread and
+// the output.
 struct Moments {
   float mean, rest, rstd;   // mu = mean + rest
 };
 
-__device__ __forceinline__ Moments finish(float mean, float s1, float s2, float inv_n, float eps) {
+__device__ __forceinline__ Moments mean_of(double sum, int64_t n) {
   Moments m;
-  m.mean = mean;
-  m.rest = s1 * inv_n;
+  const double mu = sum / double(n);
+  m.mean = float(mu);
+  m.rest = float(mu - double(m.mean));
+  m.rstd = 0.f;
+  return m;
+}
+
+// s2: the sum of (x - mean)^2
+__device__ __forceinline__ void spread(Moments& m, float s2, float inv_n, float eps) {
   const float var = fmaxf(s2 * inv_n - m.rest * m.rest, 0.f);
   m.rstd = 1.f / sqrtf(var + eps);
   // fmaxf drops a NaN: a row that holds one has no norm
   if (s2 != s2) m.rstd = s2;
-  return m;
 }
 
 template <class T, class L, int MODE>
 __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
   constexpr int V = kVec<T>, NV = L::E / V;
-  __shared__ float red[2][L::TPR > 64 ? L::TPR / 64 : 1][2];
-  RowSum<L::TPR, 2> row_sum{red};
+  constexpr int W = L::TPR > 64 ? L::TPR / 64 : 1;
+  __shared__ double red1[2][W][1];
+  __shared__ float red2[2][W][1];
+  RowSum<L::TPR, 1, double> row_sum1{red1};
+  RowSum<L::TPR, 1> row_sum2{red2};
   const int lane = threadIdx.x % L::TPR;
   const int n = int(a.cols);
   const float inv_n = 1.f / float(n);
@@ -49,35 +60,38 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
     const bool row = L::ROWS == 1 || r < a.rows;
     const T* xr = static_cast<const T*>(a.x) + (row ? r : 0) * a.ldx;
     float x[L::E];
-    float v[2] = {0.f, 0.f};
     Pack<T, V> p[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) p[k] = at[k].load(xr);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[k * V + i] = to_f32(p[k].v[i]);
-        v[0] += at[k].own(i) ? x[k * V + i] : 0.f;
-      }
-    float mean = 0.f;
+      for (int i = 0; i < V; ++i) x[k * V + i] = to_f32(p[k].v[i]);
+    Moments m{};
     if (!a.rms) {
-      row_sum(v);
-      mean = v[0] * inv_n;
+      // 16-bit values: a thread's few add up in fp32 without a rounding, unless their sizes differ by more than 2^8
+      using Sum = std::conditional_t<sizeof(T) == 4, double, float>;
+      Sum part[2] = {0, 0};
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) part[i & 1] += Sum(at[k].own(i) ? x[k * V + i] : 0.f);
+      double sum[1] = {double(part[0]) + double(part[1])};
+      row_sum1(sum);
+      m = mean_of(sum[0], n);
     }
-    v[0] = v[1] = 0.f;
+    float s2[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float& d = x[k * V + i];
-        d -= mean;
+        d -= m.mean;
         const float o = at[k].own(i) ? d : 0.f;
-        v[0] += o;
-        v[1] = fmaf(o, o, v[1]);
+        s2[0] = fmaf(o, o, s2[0]);
       }
-    row_sum(v);
-    const Moments m = finish(mean, a.rms ? 0.f : v[0], v[1], inv_n, a.eps);
+    row_sum2(s2);
+    spread(m, s2[0], inv_n, a.eps);
     if (!row) continue;
     T* yr = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
@@ -88,7 +102,7 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
       at[k].store(yr, p[k]);
     }
     if (lane == 0) {
-      if (a.mean) a.mean[r] = m.mean + m.rest;
+      if (a.mean) a.mean[r] = m.mean;
       if (a.rstd) a.rstd[r] = m.rstd;
     }
   }
@@ -99,35 +113,37 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
 template <class T>
 __global__ __launch_bounds__(1024) void k_norm_forward_long(NormForward a) {
   constexpr int V = kVec<T>;
-  __shared__ float red[2][16][2];
-  RowSum<1024, 2> row_sum{red};
+  __shared__ double red1[2][16][1];
+  __shared__ float red2[2][16][1];
+  RowSum<1024, 1, double> row_sum1{red1};
+  RowSum<1024, 1> row_sum2{red2};
   const int64_t n = a.cols;
   const float inv_n = 1.f / float(n);
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* xr = static_cast<const T*>(a.x) + r * a.ldx;
-    float mean = 0.f, v[2] = {0.f, 0.f};
+    Moments m{};
     if (!a.rms) {
+      double sum[1] = {0.0};
       for (int64_t c = threadIdx.x * V; c < n; c += 1024 * V) {
         const Pack<T, V> p = load_pack<T, V>(xr, c, n);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i & 1] += to_f32(p.v[i]);
+        for (int i = 0; i < V; ++i) sum[0] += double(to_f32(p.v[i]));
       }
-      row_sum(v);
-      mean = (v[0] + v[1]) * inv_n;
+      row_sum1(sum);
+      m = mean_of(sum[0], n);
     }
-    v[0] = v[1] = 0.f;
+    float s2[1] = {0.f};
     for (int64_t c = threadIdx.x * V; c < n; c += 1024 * V) {
       const Pack<T, V> p = load_pack<T, V>(xr, c, n);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (c + i < n) {
-          const float d = to_f32(p.v[i]) - mean;
-          v[0] += d;
-          v[1] = fmaf(d, d, v[1]);
+          const float d = to_f32(p.v[i]) - m.mean;
+          s2[0] = fmaf(d, d, s2[0]);
         }
     }
-    row_sum(v);
-    const Moments m = finish(mean, a.rms ? 0.f : v[0], v[1], inv_n, a.eps);
+    row_sum2(s2);
+    spread(m, s2[0], inv_n, a.eps);
     T* yr = static_cast<T*>(a.y) + r * a.ldy;
     for (int64_t c = threadIdx.x * V; c < n; c += 1024 * V) {
       Pack<T, V> p = load_pack<T, V>(xr, c, n);
@@ -136,12 +152,12 @@ __global__ __launch_bounds__(1024) void k_norm_forward_long(NormForward a) {
         if (c + i < n) {
           const float w = a.w ? load_any(a.w, a.wdtype, c + i) : 1.f;
           const float b = a.b ? load_any(a.b, a.wdtype, c + i) : 0.f;
-          p.v[i] = from_f32<T>(fmaf((to_f32(p.v[i]) - mean - m.rest) * m.rstd, w, b));
+          p.v[i] = from_f32<T>(fmaf((to_f32(p.v[i]) - m.mean - m.rest) * m.rstd, w, b));
         }
       store_pack<T, V>(yr, c, n, p);
     }
     if (threadIdx.x == 0) {
-      if (a.mean) a.mean[r] = m.mean + m.rest;
+      if (a.mean) a.mean[r] = m.mean;
       if (a.rstd) a.rstd[r] = m.rstd;
     }
   }

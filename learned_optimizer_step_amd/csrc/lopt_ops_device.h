@@ -242,6 +242,32 @@ __device__ __forceinline__ float lanes_reduce(float x, Op op) {
 template <int W>
 __device__ __forceinline__ float lanes_sum(float x) { return lanes_reduce<W>(x, Add()); }
 
+// The same sum in 64 bits; the exchanges move the two halves of a value.
+struct Halves {
+  float lo, hi;
+};
+template <int W>
+__device__ __forceinline__ double lanes_sum(double x) {
+  const auto join = [](float lo, float hi) { return __builtin_bit_cast(double, Halves{lo, hi}); };
+  Halves h = __builtin_bit_cast(Halves, x);
+  x += join(dpp<0xB1>(h.lo), dpp<0xB1>(h.hi));
+  h = __builtin_bit_cast(Halves, x);
+  x += join(dpp<0x4E>(h.lo), dpp<0x4E>(h.hi));
+  h = __builtin_bit_cast(Halves, x);
+  x += join(dpp<0x141>(h.lo), dpp<0x141>(h.hi));
+  if constexpr (W > 8) {
+    h = __builtin_bit_cast(Halves, x);
+    x += join(dpp<0x140>(h.lo), dpp<0x140>(h.hi));
+    h = __builtin_bit_cast(Halves, x);
+    Two lo = swap16(h.lo), hi = swap16(h.hi);
+    x = join(lo.a, hi.a) + join(lo.b, hi.b);
+    h = __builtin_bit_cast(Halves, x);
+    lo = swap32(h.lo), hi = swap32(h.hi);
+    x = join(lo.a, hi.a) + join(lo.b, hi.b);
+  }
+  return x;
+}
+
 // Sum over the lanes of the same place in their group of 8 (the groups of a wave added up).
 __device__ __forceinline__ float groups_sum(float x) {
   x += dpp<0x128>(x);   // row_ror 8: the other group of the 16 lanes
