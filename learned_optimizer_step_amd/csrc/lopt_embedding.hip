@@ -531,10 +531,9 @@ __device__ __forceinline__ void sum_chunk(const EmbeddingBackward& a, const Work
 // to its end, and the next chunk leaves them out; one that goes on further
 // leaves its sum in the workspace: slot 0 if it began before the chunk, slot 1
 // if it began in it.
-// 65,536 tokens of 32,000 x 2048, bf16 to fp32: 95 us.  That is HBM's time for
-// the whole gradient: besides 241 MB of dout read and 102 MB of rows written,
-// the rows cleared before leave the 256 MB memory-side cache meanwhile, 500 MB
-// in all at 5.3 TB/s.  Half the width, which fits that cache, takes 38.
+// 65,536 tokens of 32,000 x 2048, bf16 to fp32: 68 us for 241 MB of dout and
+// 102 MB of rows, 5.0 TB/s (95 through the caches, whose lines were written
+// back meanwhile).
 template <class TD, class TG, int MODE>
 __global__ __launch_bounds__(256) void k_embedding_sum(EmbeddingBackward a, Work w, int64_t sum_blocks, Clear clear) {
   if (int64_t(blockIdx.x) >= sum_blocks) {
