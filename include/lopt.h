@@ -485,8 +485,8 @@ lopt_status lopt_norm_backward(int32_t kind, int64_t rows, int64_t cols, int32_t
  * table (row0 = 0: all of it; a rank's rows of a sharded one otherwise, whose
  * outputs add up over the ranks).  An id that names no row of it (padding, say
  * -1, or a row of another shard) gives a row of zeros.  ids: id_bytes (4 or 8)
- * bytes each, signed.  out: n_ids x cols of type o_dtype.  At most 2^27 ids;
- * row0 within [0, 2^40]; scale finite. */
+ * bytes each, signed.  out: n_ids x cols of type o_dtype.  At most 2^27 ids
+ * and 2^30 columns; row0 within [0, 2^40]; scale finite. */
 lopt_status lopt_embedding_forward(int64_t n_ids, const void* ids, int32_t id_bytes, int64_t rows, int64_t cols, int64_t row0,
                                    const void* table, int64_t ldt, int32_t t_dtype, float scale, void* out, int64_t ldo,
                                    int32_t o_dtype, void* stream);

@@ -42,37 +42,21 @@ __device__ __forceinline__ uint32_t row_of(const void* ids, int id_bytes, int64_
 
 // ---------------------------------------------------------------------------
 // Forward: TPR threads write 8 TPR columns of one token.
-template <class TT, class TO, int TPR>
+template <class TT, class TO, int TPR, int MODE>
 __global__ __launch_bounds__(256) void k_embedding_forward(EmbeddingForward a) {
-  constexpr int E = 8, V = kVec<TT> < E ? kVec<TT> : E;
-  const int lane = threadIdx.x % TPR;
-  const int64_t slabs = (a.cols + E * TPR - 1) / (E * TPR), units = a.n_ids * slabs;
+  constexpr int V = 8;
+  const int64_t slabs = (a.cols + V * TPR - 1) / (V * TPR), units = a.n_ids * slabs;
   for (int64_t u = int64_t(blockIdx.x) * (256 / TPR) + threadIdx.x / TPR; u < units; u += int64_t(gridDim.x) * (256 / TPR)) {
     const int64_t t = slabs == 1 ? u : u / slabs;
-    const int64_t c = (u - t * slabs) * (E * TPR) + lane * E;
     const uint32_t v = row_of(a.ids, a.id_bytes, t, a.row0, a.rows);
     const bool there = int64_t(v) < a.rows;
-    const TT* w = static_cast<const TT*>(a.table) + (there ? int64_t(v) : 0) * a.ldt;
-    Pack<TO, E> o;
+    const RowVec<TT, V, MODE> at(int((u - t * slabs) * (V * TPR)) + int(threadIdx.x % TPR) * V, int(a.cols));
+    Pack<TT, V> p{};
+    if (there) p = at.load(static_cast<const TT*>(a.table) + int64_t(v) * a.ldt);
+    Pack<TO, V> o;
 #pragma unroll
-    for (int k = 0; k < E / V; ++k) {
-      Pack<TT, V> p{};
-      if (there) p = load_pack<TT, V>(w, c + k * V, a.cols);
-#pragma unroll
-      for (int i = 0; i < V; ++i) o.v[k * V + i] = from_f32<TO>(there ? to_f32(p.v[i]) * a.scale : 0.f);
-    }
-    TO* out = static_cast<TO*>(a.out) + t * a.ldo;
-    if constexpr (sizeof(TO) == 4) {
-      Pack<TO, 4> h;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h.v[i] = o.v[4 * k + i];
-        store_pack<TO, 4>(out, c + 4 * k, a.cols, h);
-      }
-    } else {
-      store_pack<TO, E>(out, c, a.cols, o);
-    }
+    for (int i = 0; i < V; ++i) o.v[i] = from_f32<TO>(there ? to_f32(p.v[i]) * a.scale : 0.f);
+    at.store(static_cast<TO*>(a.out) + t * a.ldo, o);
   }
 }
 
@@ -677,8 +661,11 @@ hipError_t launch_embedding_forward(const EmbeddingForward& a, hipStream_t s) {
       const int tpr = a.cols <= 64 ? 8 : 64;
       const int64_t units = a.n_ids * ((a.cols + 8 * tpr - 1) / (8 * tpr)), per = 256 / tpr;
       const dim3 grid(unsigned(std::min<int64_t>((units + per - 1) / per, 1 << 20))), block(256);
-      if (tpr == 8) k_embedding_forward<TT, TO, 8><<<grid, block, 0, s>>>(a);
-      else k_embedding_forward<TT, TO, 64><<<grid, block, 0, s>>>(a);
+      const int mode = row_mode(a.cols, 8);
+      if (mode == kTiny) k_embedding_forward<TT, TO, 8, kTiny><<<grid, block, 0, s>>>(a);
+      else if (tpr == 8) k_embedding_forward<TT, TO, 8, kTail><<<grid, block, 0, s>>>(a);
+      else if (mode == kWhole) k_embedding_forward<TT, TO, 64, kWhole><<<grid, block, 0, s>>>(a);
+      else k_embedding_forward<TT, TO, 64, kTail><<<grid, block, 0, s>>>(a);
       return hipGetLastError();
     });
   });

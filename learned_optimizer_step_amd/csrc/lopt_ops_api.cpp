@@ -93,6 +93,7 @@ size_t norm_bytes(int64_t rows, int64_t cols) {
 
 void check_embedding(int64_t n_ids, int64_t rows, int64_t cols, int64_t row0) {
   check_dims(rows, cols);
+  if (cols > (int64_t(1) << 30)) fail(LOPT_ERR_UNSUPPORTED, "embedding rows of more than 2^30 columns");
   if (n_ids < 0) fail(LOPT_ERR_INVALID_ARGUMENT, "negative number of ids");
   if (n_ids > kMaxIds) fail(LOPT_ERR_UNSUPPORTED, "more than 2^27 ids in one call");
   if (row0 < 0 || row0 > (int64_t(1) << 40)) fail(LOPT_ERR_INVALID_ARGUMENT, "row0 must lie in [0, 2^40]");

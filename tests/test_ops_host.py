@@ -43,6 +43,7 @@ CASES = [
     *[("lopt_embedding_forward", EMB_FWD, c, s) for c, s in [
         (dict(n_ids=-1), BAD), (dict(n_ids=(1 << 27) + 1), UNSUPPORTED), (dict(ids=None), BAD), (dict(id_bytes=2), BAD),
         (dict(rows=-1), BAD), (dict(cols=0), BAD), (dict(rows=1 << 31), UNSUPPORTED), (dict(row0=-1), BAD),
+        (dict(cols=(1 << 30) + 1, ldt=1 << 31, ldo=1 << 31), UNSUPPORTED),
         (dict(row0=(1 << 40) + 1), BAD), (dict(table=None), BAD), (dict(ldt=8), BAD), (dict(t_dtype=4), BAD),
         (dict(o_dtype=4), BAD), (dict(scale=float("inf")), BAD), (dict(out=None), BAD), (dict(out=A[1] + 64), BAD),
         (dict(ldo=15), BAD), (dict(ids=A[0] + 4), UNSUPPORTED)]],
