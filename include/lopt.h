@@ -442,7 +442,8 @@ lopt_status lopt_set_timing_events(lopt_handle* h, void* const* events, int32_t 
  * call, except where said.  A workspace belongs to the caller and holds
  * nothing between calls; two calls that may run at the same time need two.
  * Sums and statistics are fp32 or wider and in a fixed order: the same inputs
- * give the same bits.  Every output is rounded once.
+ * give the same bits (those of a distillation row also depend on where in a
+ * 16-byte piece it begins).  Every output is rounded once.
  * Errors: LOPT_ERR_INVALID_ARGUMENT (a NULL pointer, a bad size, stride, type
  * or hyperparameter, overlapping buffers), LOPT_ERR_UNSUPPORTED (a size over
  * the limit, a misaligned pointer), LOPT_ERR_WORKSPACE, LOPT_ERR_HIP. */

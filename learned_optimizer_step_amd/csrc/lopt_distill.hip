@@ -94,23 +94,29 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
     }
     if (nan) top_u = NAN;
 
-    // running maximum m of z and sum s of exp((z - m) / tau), per thread
-    float m = -INFINITY, s = 0.f;
+    // running maximum m of z and sum s of 2^(z c - mc), per thread, with mc the rounded m c: the sum is rescaled by that
+    // same number, as half a step of m c (2^-19 at 60) is more than the sum's own roundings
+    float m = -INFINITY, s = 0.f, mc = 0.f;
+    const auto rise = [&](float top) {
+      const float old = mc;
+      mc = top == -INFINITY ? 0.f : top * c;   // all -inf so far: every term is 2^-inf = 0
+      asm("" : "+v"(mc));                      // one number for all its uses: no fma takes the product's place
+      s = m == -INFINITY ? 0.f * s : s * exp2_hw(old - mc);
+      m = top;
+    };
     const auto take = [&](auto const&... packs) {
       float top = m;
       ([&] {
 #pragma unroll
         for (int i = 0; i < V; ++i) top = fmaxf(top, to_f32(packs.v[i]));
       }(), ...);
-      const float mc = top == -INFINITY ? 0.f : top * c;   // all -inf so far: every term is exp(-inf) = 0
-      s *= exp2_hw((m == -INFINITY ? -INFINITY : m * c - mc));
+      rise(top);
       ([&] {
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) t += exp2_hw(fmaf(to_f32(packs.v[i]), c, -mc));
         s += t;
       }(), ...);
-      m = top;
     };
     // single elements up to the first 16-byte border and behind the last one: rows of an odd length begin anywhere, and
     // unaligned vectors take a fifth more time (4096 x 50257 bf16: 112 us for 96)
@@ -128,9 +134,9 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
       const int64_t i = int64_t(threadIdx.x) < lead ? int64_t(threadIdx.x) : tail + threadIdx.x - lead;
       Pack<T, 1> p;
       p.v[0] = z[i];
-      const float x = to_f32(p.v[0]), top = fmaxf(m, x), mc = top == -INFINITY ? 0.f : top * c;
-      s = s * exp2_hw((m == -INFINITY ? -INFINITY : m * c - mc)) + exp2_hw(fmaf(x, c, -mc));
-      m = top;
+      const float x = to_f32(p.v[0]);
+      rise(fmaxf(m, x));
+      s += exp2_hw(fmaf(x, c, -mc));
     }
 
     const float wave_m = lanes_reduce<64>(m, Max());
@@ -146,8 +152,7 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
       mz = fmaxf(mz, maxima[0][k]);
       mu = fmaxf(mu, maxima[1][k]);
     }
-    const float mc = mz == -INFINITY ? 0.f : mz * c;
-    s *= exp2_hw(m == -INFINITY ? -INFINITY : m * c - mc);
+    rise(mz);
     float es = 0.f, eu = 0.f;
 #pragma unroll
     for (int e = 0; e < NE; ++e)
@@ -174,9 +179,10 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
         es += sums[1][k];
         eu += sums[2][k];
       }
-      const float log_s = kLn2 * log2f(s);
-      if (a.lse) a.lse[r] = fmaf(mc, kLn2, log_s);
-      if (a.loss) a.loss[r] = mu == -INFINITY ? 0.f : a.tau * a.tau * (eu / es - kLn2 * log2f(es) + log_s);
+      // from the rounded m c to m c itself; one logarithm of s / es, as that of two is lost in their difference
+      const float rest = mz == -INFINITY ? 0.f : fmaf(mz, c, -mc);
+      if (a.lse) a.lse[r] = fmaf(mz, a.inv_tau, kLn2 * (log2f(s) - rest));
+      if (a.loss) a.loss[r] = mu == -INFINITY ? 0.f : a.tau * a.tau * fmaf(kLn2, log2f(s / es) - rest, eu / es);
     }
     // the next row's exchanges write `maxima` after this barrier's reads of it, and `sums` after its own first barrier
   }

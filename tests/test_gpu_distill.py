@@ -211,8 +211,13 @@ def test_no_rows_and_more_elements_than_32_bits_count():
     ids = torch.randint(0, cols, (rows, 6), device="cuda")
     u = torch.randn(rows, 6, device="cuda")
     loss, lse = layers.distill_forward(z, ids, u)
-    part = layers.distill_forward(z[-3:].clone(), ids[-3:], u[-3:])
-    assert torch.equal(loss[-3:], part[0]) and torch.equal(lse[-3:], part[1])
+    # not the bits of a copy of these rows: they begin at other places of a 16-byte piece (65537 elements of 2 bytes a row),
+    # so other threads add other elements, and each of the two is off by up to `tols` by itself
+    last = z[-3:].cpu(), ids[-3:].cpu(), u[-3:].cpu()
+    want = distill(*last, 1.0)
+    tl, te = tols(last[0], *want, 1.0, torch.bfloat16)
+    close(loss[-3:], want[0], tl, "loss of the last rows")
+    close(lse[-3:], want[1], te, "lse of the last rows")
     assert bool(((lse[:-3] - math.log(cols)).abs() <= 60 * U * 12).all())
     g = torch.ones(rows, device="cuda")
     want = layers.distill_backward(g[-3:], z[-3:].clone(), ids[-3:], u[-3:], lse[-3:])
