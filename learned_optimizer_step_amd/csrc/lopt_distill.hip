@@ -11,6 +11,8 @@
 // the softmax in one pass), the backward pass reads z and writes dz.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+
 #include <algorithm>
 #include <type_traits>
 
@@ -95,11 +97,12 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
     if (nan) top_u = NAN;
 
     // running maximum m of z and sum s of 2^(z c - mc), per thread, with mc the rounded m c: the sum is rescaled by that
-    // same number, as half a step of m c (2^-19 at 60) is more than the sum's own roundings
+    // same number, as half a step of m c (2^-19 at 60) is more than the sum's own roundings.  m c may overflow (a mask of
+    // the type's lowest value) where the row's largest does not: held finite, such a thread's terms vanish beside it
     float m = -INFINITY, s = 0.f, mc = 0.f;
     const auto rise = [&](float top) {
       const float old = mc;
-      mc = top == -INFINITY ? 0.f : top * c;   // all -inf so far: every term is 2^-inf = 0
+      mc = top == -INFINITY ? 0.f : fminf(fmaxf(top * c, -FLT_MAX), FLT_MAX);   // all -inf so far: terms are 2^-inf = 0
       asm("" : "+v"(mc));                      // one number for all its uses: no fma takes the product's place
       s = m == -INFINITY ? 0.f * s : s * exp2_hw(old - mc);
       m = top;
@@ -153,6 +156,11 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
       mu = fmaxf(mu, maxima[1][k]);
     }
     rise(mz);
+    const bool far = mz != -INFINITY && !(fabsf(mz * c) <= FLT_MAX);
+    if (far) {   // the row's largest logit cannot be scaled: its sum again, of differences
+      s = 0.f;
+      for (int64_t i = threadIdx.x; i < n; i += B) s += exp2_hw((to_f32(z[i]) - mz) * c);
+    }
     float es = 0.f, eu = 0.f;
 #pragma unroll
     for (int e = 0; e < NE; ++e)
@@ -180,8 +188,12 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
         eu += sums[2][k];
       }
       // from the rounded m c to m c itself; one logarithm of s / es, as that of two is lost in their difference
-      const float rest = mz == -INFINITY ? 0.f : fmaf(mz, c, -mc);
-      if (a.lse) a.lse[r] = fmaf(mz, a.inv_tau, kLn2 * (log2f(s) - rest));
+      const float rest = mz == -INFINITY || far ? 0.f : fmaf(mz, c, -mc);
+      if (a.lse) {
+        // below the least number that one, as the gradient of -inf would be no number
+        const float lse = fmaf(mz, a.inv_tau, kLn2 * (log2f(s) - rest));
+        a.lse[r] = far && lse == -INFINITY ? -FLT_MAX : lse;
+      }
       if (a.loss) a.loss[r] = mu == -INFINITY ? 0.f : a.tau * a.tau * fmaf(kLn2, log2f(s / es) - rest, eu / es);
     }
     // the next row's exchanges write `maxima` after this barrier's reads of it, and `sums` after its own first barrier

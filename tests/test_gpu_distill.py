@@ -239,3 +239,47 @@ def test_refusals_of_the_tensors():
                  lambda: layers.distill_loss(z, i.repeat(1, 600), u.repeat(1, 600))):
         with pytest.raises(L.LoptError):
             call()
+
+
+def shifted(z, ids, u, tau):
+    """The definition with the rows' largest values taken off (in 64 bits, so the bounds do not grow with them): the loss
+    and q - p are the same."""
+    z, u = z.double(), u.double()
+    return distill(z - z.max(1, keepdim=True).values, ids, u - u.max(1, keepdim=True).values, tau)
+
+
+@pytest.mark.parametrize("tau", [0.25, 1.0])
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_threads_that_see_only_the_lowest_value(t, tau):
+    """A vocabulary whose end is masked with the type's lowest value, which overflows when it is scaled: all that most
+    threads see of a row.  In 64 bits it is as good as -inf."""
+    for cols, kept in ((3000, 700), (9000, 8), (50001, 300)):
+        z, ids, u, dl = make(6, cols, 5, t, torch.float32, torch.int64, cols, absent=0.0)
+        ids = torch.where(ids < 0, ids, ids % kept)
+        z[:, kept:] = torch.finfo(t).min
+        loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+        dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)
+        m = z.clone()
+        m[:, kept:] = -math.inf
+        want = distill(m, ids, u, tau)
+        tl, e = tols(m, *want, tau, t)
+        close(lse, want[1], e, f"{cols} lse")
+        close(loss, want[0], tl, f"{cols} loss")
+        _, _, qp, q, dense, size, _ = distill(m, ids, u, tau, lse.cpu())
+        g = (dl.double() * tau)[:, None]
+        tol = g.abs() * U * (8 * size[:, None] * q + (16 * size[:, None] + ids.shape[1]) * dense)
+        close(dz, qp * g, rounding(qp * g, t) + tol + g.abs() * 2.0 ** -125, f"{cols} dz")
+
+
+@pytest.mark.parametrize("tau", [0.25, 1.0])
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_rows_of_nothing_but_the_lowest_value(t, tau):
+    """The student's distribution is uniform; the gradient cannot be exact (lse holds no log of the count there) but is a
+    number, so a mask behind it gives zeros."""
+    z, ids, u, dl = make(4, 2500, 9, t, torch.float32, torch.int64, 2, absent=0.0)
+    z[2:] = torch.finfo(t).min
+    loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+    want = shifted(z, ids, u, tau)
+    close(loss, want[0], tols(z, *want, tau, t)[0], "loss")
+    assert torch.isfinite(lse).all()
+    assert torch.isfinite(layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)).all()
