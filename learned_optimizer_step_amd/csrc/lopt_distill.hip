@@ -33,7 +33,8 @@ constexpr float kLn2 = 0.693147180559945309417f;
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Entry k of a row's list: u / tau, -inf if it is absent, and its id.
+// Entry k of a row's list: its logit, -inf if it is absent, and its id.  The logit is scaled after the list's largest is
+// taken off: a product with 1 / tau first can overflow, and costs half a step of the logits' common offset.
 struct Entry {
   float u;
   int64_t id;
@@ -43,7 +44,7 @@ __device__ __forceinline__ Entry load_entry(const Args& a, int64_t r, int k) {
   Entry e;
   e.id = a.id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[r * a.ldi + k]
                          : int64_t(static_cast<const int32_t*>(a.ids)[r * a.ldi + k]);
-  e.u = load_any(a.u, a.udtype, r * a.ldu + k) * a.inv_tau;
+  e.u = load_any(a.u, a.udtype, r * a.ldu + k);
   if (e.id < 0 || e.id >= a.cols) e.u = -INFINITY;
   return e;
 }
@@ -165,10 +166,10 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
 #pragma unroll
     for (int e = 0; e < NE; ++e)
       if (u[e] != -INFINITY) {
-        const float d = u[e] - mu, p = exp2_hw(d * kLog2e);
+        const float d = u[e] - mu, p = exp2_hw(d * c);
         es += p;
         // p that rounds to 0 has no term, whatever the student's logit
-        if (p != 0.f) eu = fmaf(p, d - (zk[e] - mz) * a.inv_tau, eu);
+        if (p != 0.f) eu = fmaf(p, (d - (zk[e] - mz)) * a.inv_tau, eu);
       }
     s = lanes_sum<64>(s);
     es = lanes_sum<64>(es);
@@ -259,7 +260,7 @@ __global__ __launch_bounds__(B) void k_distill_backward(DistillBackward a, int p
     for (int e = 0; e < NE; ++e) {
       const int k = e * B + int(threadIdx.x);
       if (k < a.top) {
-        const float p = u[e] == -INFINITY ? 0.f : exp2_hw((u[e] - top_u) * kLog2e);
+        const float p = u[e] == -INFINITY ? 0.f : exp2_hw((u[e] - top_u) * (a.inv_tau * kLog2e));
         prob[k] = p;
         sum += p;
       }

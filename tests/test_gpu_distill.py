@@ -283,3 +283,49 @@ def test_rows_of_nothing_but_the_lowest_value(t, tau):
     close(loss, want[0], tols(z, *want, tau, t)[0], "loss")
     assert torch.isfinite(lse).all()
     assert torch.isfinite(layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)).all()
+
+
+@pytest.mark.parametrize("ut", TYPES, ids=str)
+def test_teachers_whose_logits_overflow_when_scaled(ut):
+    """Lists of nothing but the type's lowest or largest value are lists of equal entries; only -inf is absent."""
+    z, ids, u, dl = make(6, 700, 8, torch.float32, ut, torch.int64, 4, absent=0.0)
+    u[0], u[2], u[3, 3:] = torch.finfo(ut).min, torch.finfo(ut).max, torch.finfo(ut).min
+    u[4] = torch.finfo(ut).min
+    u[4, 6:] = -math.inf
+    tau = 0.25
+    loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+    want = shifted(z, ids, u, tau)
+    # entries that the teacher excludes have no part in the sizes
+    size = torch.where(want[5] > 1e6, 1 + 4 * (z.double() / tau).abs().max(1).values, want[5])
+    close(loss, want[0], tols(z, *want[:5], size, want[6], tau, torch.float32)[0], "loss")
+    dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)
+    u64 = u.double() - u.double().max(1, keepdim=True).values
+    _, _, qp, q, dense, size, _ = distill(z, ids, u64, tau, lse.cpu())
+    size = torch.where(size > 1e6, 1 + 4 * (z.double() / tau).abs().max(1).values, size)
+    g = (dl.double() * tau)[:, None]
+    tol = g.abs() * U * (8 * size[:, None] * q + (16 * size[:, None] + 8) * dense)
+    close(dz, qp * g, rounding(qp * g, torch.float32) + tol + g.abs() * 2.0 ** -125, "dz")
+
+
+@pytest.mark.parametrize("tau", [1.0, 3.0, 4.0])
+def test_the_offset_of_all_logits_costs_nothing(tau):
+    """Student and teacher far from zero, in vocabularies of a few elements and of thousands: the loss has the bound of the
+    same logits about zero, 1000 U tau^2 for most of the small ones.  Roundings of the logits scaled by log2 e or 1 / tau,
+    half a step of which is 2^-13 (2048 U) or more here, do not keep it."""
+    for cols, top in ((3, 2), (7, 7), (40, 5), (5000, 30)):
+        z, ids, u, dl = make(64, cols, top, torch.float32, torch.float32, torch.int64, cols, absent=0.0)
+        z, u = z + 1e4, u - 1.3e4
+        loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+        want = shifted(z, ids, u, tau)
+        tl, _ = tols(z, *want, tau, torch.float32)
+        close(loss, want[0], tl, f"{cols} loss")
+        # of lse: the product with the rounded 1 / tau, its own rounding, and the bound about zero
+        exact = torch.logsumexp(z.double() / tau, 1)
+        close(lse, exact, tols(z, *want, tau, torch.float32)[1] + 3 * U * exact.abs(), f"{cols} lse")
+        dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)
+        g = (dl.double() * tau)[:, None]
+        _, _, qp, q, dense, size, _ = distill(z, ids, u.double() - u.double().max(1, keepdim=True).values, tau, lse.cpu())
+        # the student's share has the size of z / tau - lse, two large numbers here; the teacher's has not
+        spread = 1 + (u.max(1).values - u.min(1).values).double() / tau
+        tol = g.abs() * U * (8 * size[:, None] * q + (16 * spread[:, None] + top) * dense)
+        close(dz, qp * g, rounding(qp * g, torch.float32) + tol + g.abs() * 2.0 ** -125, f"{cols} dz")
