@@ -200,28 +200,33 @@ __global__ __launch_bounds__(256) void k_norm_columns_long(NormBackward a) {
     }
 }
 
-// dw and db from the blocks' sums: 32 columns a block, 32 threads a column,
-// each adding up every 32nd block's sum; the 32 results are added in order.
+// dw and db from the blocks' sums: 32 columns a block at a time, 32 threads a
+// column, each adding up every 32nd block's sum; the 32 results are added in
+// order.
+constexpr int64_t kJoinBlocks = 1 << 20;   // a grid has room for 2^32 - 1 threads a dimension
 __global__ __launch_bounds__(1024) void k_norm_weight_grad(NormBackward a, int64_t blocks) {
   __shared__ float s[32][33];
   const int64_t n = a.cols, width = a.rms ? n : 2 * n;
-  const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
   const int g = threadIdx.x / 32;
-  float sum = 0.f;
-  if (c < width) {
+  for (int64_t c0 = int64_t(blockIdx.x) * 32; c0 < width; c0 += int64_t(gridDim.x) * 32) {
+    const int64_t c = c0 + threadIdx.x % 32;
+    float sum = 0.f;
+    if (c < width) {
 #pragma unroll 8
-    for (int64_t b = g; b < blocks; b += 32) sum += a.part[b * width + c];
-  }
-  s[g][threadIdx.x % 32] = sum;
-  __syncthreads();
-  if (g != 0 || c >= width) return;
-  sum = 0.f;
+      for (int64_t b = g; b < blocks; b += 32) sum += a.part[b * width + c];
+    }
+    s[g][threadIdx.x % 32] = sum;
+    __syncthreads();
+    if (g == 0 && c < width) {
+      sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < 32; ++k) sum += s[k][threadIdx.x];
-  void* out = c < n ? a.dw : a.db;
-  const int64_t i = c < n ? c : c - n;
-  if (!out) return;
-  store_any(out, a.gdtype, i, a.accumulate ? load_any(out, a.gdtype, i) + sum : sum);
+      for (int k = 0; k < 32; ++k) sum += s[k][threadIdx.x];
+      void* out = c < n ? a.dw : a.db;
+      const int64_t i = c < n ? c : c - n;
+      if (out) store_any(out, a.gdtype, i, a.accumulate ? load_any(out, a.gdtype, i) + sum : sum);
+    }
+    __syncthreads();   // s is written again
+  }
 }
 
 }  // namespace
@@ -273,7 +278,7 @@ hipError_t launch_norm_backward(const NormBackward& a, hipStream_t s) {
   }
   if (!sums) return hipSuccess;
   const int64_t width = a.rms ? a.cols : 2 * a.cols;
-  k_norm_weight_grad<<<dim3(unsigned((width + 31) / 32)), dim3(1024), 0, s>>>(a, blocks);
+  k_norm_weight_grad<<<dim3(unsigned(std::min<int64_t>((width + 31) / 32, kJoinBlocks))), dim3(1024), 0, s>>>(a, blocks);
   return hipGetLastError();
 }
 

@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import (CODE, TYPES, U, close, norm_backward, norm_forward, norm_forward_tols, rounding,  # noqa: E402
+from ops_cases import (CODE, TINY, TYPES, U, close, norm_backward, norm_forward, norm_forward_tols, rounding,  # noqa: E402
                        row_depth)
 
 # one row to thousands; every row layout with its first and last width, widths that no vector divides, and rows too long
@@ -293,3 +293,24 @@ def test_refusals_of_the_tensors():
             call()
     with pytest.raises(L.LoptError):
         layers.norm_forward(x, w, w, eps=-1.0)
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+def test_weights_of_more_columns_than_one_grid_has_threads_for(rms):
+    """The blocks' sums are joined by 32 threads a column: 2^32 threads and more from 2^26 columns (RMS: 2^27) on."""
+    rows, cols = 2, (1 << (27 if rms else 26)) + 3
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x, dy = (torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    mean = None if rms else torch.tensor([0.25, -0.5], device="cuda")
+    rstd = torch.tensor([1.5, 0.75], device="cuda")
+    dx, dw, db = layers.norm_backward(dy, x, None, mean, rstd, rms=rms, need_x=False)
+    assert dx is None
+    for a in range(0, cols, 1 << 24):
+        part = slice(a, min(cols, a + (1 << 24)))
+        xh = (x[:, part].double() - (0 if rms else mean.double()[:, None])) * rstd.double()[:, None]
+        terms = dy[:, part].double() * xh
+        # two roundings of xh, one of each product's sum and of the join's
+        assert bool(((dw[part].double() - terms.sum(0)).abs() <= 4 * U * terms.abs().sum(0) + TINY[torch.float32]).all()), a
+        if not rms:
+            d = dy[:, part].double()
+            assert bool(((db[part].double() - d.sum(0)).abs() <= U * d.abs().sum(0)).all()), a
