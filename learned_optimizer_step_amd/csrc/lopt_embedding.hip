@@ -25,6 +25,7 @@ constexpr int kMaxTiles = 256;    // blocks of the sort
 constexpr int kDigits = 256;      // 8 bits a pass
 
 constexpr int64_t kFew = 128;     // tokens that k_embedding_few takes (77 of 1000 x 65: 5 us, 13 with a sort)
+constexpr int64_t kFewWaves = 1 << 24;   // its waves, each in a grid of at most 2^32 - 1 threads; more take the sort's path
 
 // The sums: see k_embedding_sum.
 constexpr int kSumVec = 4;        // columns of a lane
@@ -678,16 +679,16 @@ hipError_t launch_embedding_backward(const EmbeddingBackward& a, hipStream_t s) 
   Clear clear{};
   const int64_t units = a.gdtype == kF32 ? 2 : 1;
   const bool large = a.rows * a.cols * units >= (int64_t(8) << 20);   // 16 MB to clear
-  if (a.n_ids > 0 && a.n_ids <= kFew && (a.accumulate || !large)) {
+  const int64_t few_waves = a.n_ids * ((a.cols + 64 * kSumVec - 1) / (64 * kSumVec));
+  if (a.n_ids > 0 && a.n_ids <= kFew && (a.accumulate || !large) && few_waves <= kFewWaves) {
     return with_type(a.gdtype, [&](auto tg) {
       return with_type(a.dtype, [&](auto td) {
         using TG = decltype(tg);
         using TD = decltype(td);
-        const int64_t sums = a.n_ids * ((a.cols + 64 * kSumVec - 1) / (64 * kSumVec));
-        const int64_t waves = sums + (a.accumulate ? 0 : std::min<int64_t>(a.rows, 8192));
+        const int64_t waves = few_waves + (a.accumulate ? 0 : std::min<int64_t>(a.rows, 8192));
         const dim3 g(unsigned((waves + 3) / 4));
-        if (a.cols < kSumVec) k_embedding_few<TD, TG, kTiny><<<g, dim3(256), 0, s>>>(a, sums);
-        else k_embedding_few<TD, TG, kTail><<<g, dim3(256), 0, s>>>(a, sums);
+        if (a.cols < kSumVec) k_embedding_few<TD, TG, kTiny><<<g, dim3(256), 0, s>>>(a, few_waves);
+        else k_embedding_few<TD, TG, kTail><<<g, dim3(256), 0, s>>>(a, few_waves);
         return hipGetLastError();
       });
     });

@@ -244,3 +244,20 @@ def test_refusals_of_the_tensors():
     for call in (lambda: layers.embedding(ids, w, float("nan")), lambda: layers.embedding(ids, w, row0=-1)):
         with pytest.raises(L.LoptError):
             call()
+
+
+def test_a_handful_of_tokens_of_more_columns_than_one_grid_has_threads_for():
+    """2^34 elements (34 GB in bf16): a wave a token and 256 columns would be 2^32 threads."""
+    n, rows, cols = 128, 3, 1 << 27
+    d = torch.empty(n, cols, dtype=torch.bfloat16, device="cuda")
+    for t in range(n):
+        d[t].fill_(float(t % 5 - 2))
+    d[7, -1], d[127, 0] = 9.0, -7.0
+    ids = torch.arange(n, device="cuda") % 4 - 1      # a quarter of the tokens names no row
+    out = torch.full((rows, cols), 3.0, device="cuda")
+    layers.embedding_backward(d, ids, rows, 0.5, out=out, accumulate=True)
+    for r in range(rows):
+        want = 3.0 + 0.5 * sum(t % 5 - 2 for t in range(n) if t % 4 - 1 == r)
+        assert bool((out[r, 1:-1] == want).all()), r
+        assert out[r, 0] == want + 0.5 * (-7.0 - (127 % 5 - 2)) * (127 % 4 - 1 == r), r
+        assert out[r, -1] == want + 0.5 * (9.0 - (7 % 5 - 2)) * (7 % 4 - 1 == r), r
