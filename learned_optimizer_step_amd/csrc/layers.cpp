@@ -102,12 +102,14 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType t, c10::Device device) {
   return at::empty(shape, at::TensorOptions().dtype(t).device(device));
 }
 
-// A caller's contiguous output, or a new one.
+// A caller's contiguous output, which the call will write, or a new one.
 Tensor output(const Maybe& t, at::IntArrayRef shape, c10::Device device, at::ScalarType type, const char* name) {
   if (!t) return empty(shape, type, device);
   if (t->sizes() != shape || !t->is_contiguous() || t->device() != device)
     bad(std::string(name) + " must be a contiguous tensor of shape " + show(shape) + " on " + device.str());
   dtype_code(t->scalar_type(), name);
+  // a change in place, which autograd looks for in what it has saved
+  if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
   return *t;
 }
 

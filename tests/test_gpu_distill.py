@@ -329,3 +329,28 @@ def test_the_offset_of_all_logits_costs_nothing(tau):
         spread = 1 + (u.max(1).values - u.min(1).values).double() / tau
         tol = g.abs() * U * (8 * size[:, None] * q + (16 * spread[:, None] + top) * dense)
         close(dz, qp * g, rounding(qp * g, torch.float32) + tol + g.abs() * 2.0 ** -125, f"{cols} dz")
+
+
+def test_a_gradient_over_the_logits_is_seen_by_autograd():
+    """out=logits is a change in place: a loss that still needs the logits refuses, as after any other."""
+    z, ids, u, dl = make(5, 60, 4, torch.float32, torch.float32, torch.int64, 8, absent=0.0)
+    z, ids, u, dl = z.cuda(), ids.cuda(), u.cuda(), dl.cuda()
+    logits = z.clone().requires_grad_(True) * 1.0
+    loss = layers.distill_loss(logits, ids, u)
+    _, lse = layers.distill_forward(z, ids, u)
+    layers.distill_backward(dl, logits.detach(), ids, u, lse, out=logits.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.sum().backward()
+
+
+def test_every_buffer_that_is_written_counts_as_changed():
+    x, w = torch.randn(6, 40, device="cuda"), torch.ones(40, device="cuda")
+    _, mean, rstd = layers.norm_forward(x, w, w)
+    gw, gb, gt = torch.zeros(40, device="cuda"), torch.zeros(40, device="cuda"), torch.zeros(9, 40, device="cuda")
+    layers.norm_backward(x, x, w, mean, rstd, grad_weight=gw, grad_bias=gb, accumulate=True)
+    layers.embedding_backward(x, torch.arange(6, device="cuda"), 9, out=gt)
+    assert [v._version for v in (gw, gb, gt)] == [1, 1, 1]
+    with torch.inference_mode():     # has no count, and needs none
+        gt = torch.zeros(9, 40, device="cuda")
+    layers.embedding_backward(x, torch.arange(6, device="cuda"), 9, out=gt)
+    assert torch.equal(gt[:6], x)
