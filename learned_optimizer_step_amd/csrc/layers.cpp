@@ -319,9 +319,10 @@ Tensor distill_backward(const Tensor& grad_loss, const Tensor& logits, const Ten
   Tensor dz = output(to, logits.sizes(), l.device, logits.scalar_type(), "out");
   if (dz.scalar_type() != logits.scalar_type()) bad("out must have the type of logits");
   Tensor g = grad_loss.dim() == 1 ? grad_loss : grad_loss.reshape({-1});
-  if (g.stride(0) < 0 || g.stride(0) >= (int64_t(1) << 28)) g = g.contiguous();
+  if (g.numel() > 1 && g.stride(0) >= (int64_t(1) << 28)) g = g.contiguous();
+  const int64_t step = g.numel() > 1 ? g.stride(0) : 0;   // a single element's stride can be anything
   const Tensor s = lse.contiguous();
-  check(lopt_distill_backward(l.z.rows, l.z.cols, l.code, static_cast<const float*>(g.data_ptr()), g.stride(0), l.z.data(), l.z.ld,
+  check(lopt_distill_backward(l.z.rows, l.z.cols, l.code, static_cast<const float*>(g.data_ptr()), step, l.z.data(), l.z.ld,
                               int32_t(std::min<int64_t>(l.i.cols, INT32_MAX)), l.i.data(), l.i.ld, l.nb, l.u.data(), l.u.ld,
                               l.ucode, float(temperature), static_cast<const float*>(s.data_ptr()), dz.data_ptr(), l.z.cols,
                               stream(l.device)));

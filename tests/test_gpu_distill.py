@@ -354,3 +354,12 @@ def test_every_buffer_that_is_written_counts_as_changed():
         gt = torch.zeros(9, 40, device="cuda")
     layers.embedding_backward(x, torch.arange(6, device="cuda"), 9, out=gt)
     assert torch.equal(gt[:6], x)
+
+
+def test_one_row_whose_weight_has_a_large_stride():
+    """The stride of a dimension of one element means nothing, whatever it is."""
+    z, ids, u, dl = make(1, 90, 4, torch.float32, torch.float32, torch.int64, 8, absent=0.0)
+    z, ids, u, dl = z.cuda(), ids.cuda(), u.cuda(), dl.cuda()
+    _, lse = layers.distill_forward(z, ids, u)
+    want = layers.distill_backward(dl, z, ids, u, lse)
+    assert torch.equal(layers.distill_backward(dl.as_strided((1,), (1 << 28,)), z, ids, u, lse), want)
