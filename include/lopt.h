@@ -460,7 +460,7 @@ typedef enum lopt_norm_kind { LOPT_NORM_LAYER = 0, LOPT_NORM_RMS = 1 } lopt_norm
  * NULL: 1 and 0.  mean, rstd: rows floats that lopt_norm_backward takes; NULL:
  * not kept.  An RMS norm has neither bias nor mean (NULL).  eps: finite, >= 0;
  * with 0, a row without spread gives NaN.  A NaN or an infinity spoils its own
- * row only. */
+ * row only; rstd is 0 where the sum of squares is more than a float holds. */
 lopt_status lopt_norm_forward(int32_t kind, int64_t rows, int64_t cols, int32_t dtype, const void* x, int64_t ldx,
                               const void* weight, const void* bias, int32_t w_dtype, float eps, void* y, int64_t ldy,
                               float* mean, float* rstd, void* stream);

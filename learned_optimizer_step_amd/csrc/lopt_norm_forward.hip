@@ -4,6 +4,8 @@
 // registers between the two sums and the output.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+
 #include "lopt_norm.h"
 
 namespace lopt {
@@ -27,12 +29,15 @@ __device__ __forceinline__ Moments mean_of(double sum, int64_t n) {
   return m;
 }
 
-// s2: the sum of (x - mean)^2
-__device__ __forceinline__ void spread(Moments& m, float s2, float inv_n, float eps) {
-  const float var = fmaxf(s2 * inv_n - m.rest * m.rest, 0.f);
+// s2: the sum of (x - mean)^2; inv_n: the rounded 1 / n.  The product of the two is off by its rounding in every element
+// of every row (the mean square of 41 ones is not 1): what it leaves of s2 gives the quotient's last bit (131072 x 128
+// bf16 RMS: 27.1 us, 26.6 without it and 28.6 with a division).
+__device__ __forceinline__ void spread(Moments& m, float s2, float n, float inv_n, float eps) {
+  const float q = s2 * inv_n, mean2 = fmaf(fmaf(-q, n, s2), inv_n, q);
+  const float var = fmaxf(mean2 - m.rest * m.rest, 0.f);
   m.rstd = 1.f / sqrtf(var + eps);
-  // fmaxf drops a NaN: a row that holds one has no norm
-  if (s2 != s2) m.rstd = s2;
+  // fmaxf drops a NaN: a row that holds one has no norm; one whose squares add up to more than fp32 holds has rstd 0
+  if (!(s2 <= FLT_MAX)) m.rstd = s2 == INFINITY ? 0.f : s2;
 }
 
 template <class T, class L, int MODE>
@@ -91,7 +96,7 @@ __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {
         s2[0] = fmaf(o, o, s2[0]);
       }
     row_sum2(s2);
-    spread(m, s2[0], inv_n, a.eps);
+    spread(m, s2[0], float(n), inv_n, a.eps);
     if (!row) continue;
     T* yr = static_cast<T*>(a.y) + r * a.ldy;
 #pragma unroll
@@ -143,7 +148,7 @@ __global__ __launch_bounds__(1024) void k_norm_forward_long(NormForward a) {
         }
     }
     row_sum2(s2);
-    spread(m, s2[0], inv_n, a.eps);
+    spread(m, s2[0], float(n), inv_n, a.eps);
     T* yr = static_cast<T*>(a.y) + r * a.ldy;
     for (int64_t c = threadIdx.x * V; c < n; c += 1024 * V) {
       Pack<T, V> p = load_pack<T, V>(xr, c, n);

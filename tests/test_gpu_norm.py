@@ -11,8 +11,8 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import (CODE, TINY, TYPES, U, close, norm_backward, norm_forward, norm_forward_tols, rounding,  # noqa: E402
-                       row_depth)
+from ops_cases import (CODE, TINY, TYPES, U, close, depth, norm_backward, norm_forward, norm_forward_tols,  # noqa: E402
+                       rounding, row_depth)
 
 # one row to thousands; every row layout with its first and last width, widths that no vector divides, and rows too long
 # for registers
@@ -314,3 +314,37 @@ def test_weights_of_more_columns_than_one_grid_has_threads_for(rms):
         if not rms:
             d = dy[:, part].double()
             assert bool(((db[part].double() - d.sum(0)).abs() <= U * d.abs().sum(0)).all()), a
+
+
+def test_the_mean_is_rounded_once():
+    """fp32 rows whose mean cancels: the sum is taken in 64 bits, so its error is that of the last rounding (an fp32 sum's
+    would be of the size of the values).  A term passes at most `depth` additions in 64 bits."""
+    g = torch.Generator().manual_seed(40)
+    for cols in (7, 60, 200, 768, 1025, 5000, 16385, 40001):
+        x = 100 * torch.randn(40, cols, generator=g)
+        x[:, cols // 2] -= x.double().sum(1).float()
+        _, mean, _ = layers.norm_forward(x.cuda())
+        exact = x.double().mean(1)
+        size = x.double().abs().mean(1)
+        assert bool((exact.abs() < 1e-5 * size).all())
+        close(mean, exact, U * exact.abs() + (depth(cols) + 2) * 2.0 ** -53 * size + TINY[torch.float32], f"{cols} mean")
+
+
+def test_the_mean_square_of_ones_is_one():
+    """The sum of n ones is n and n / n is 1, for every width: the root and its reciprocal too."""
+    for cols in (1, 3, 41, 47, 55, 61, 82, 83, 94, 97, 107, 197, 500, 768, 1000, 1003, 2047, 3001, 6000, 16383, 16385, 40001):
+        for t in TYPES:
+            y, _, rstd = layers.norm_forward(torch.ones(3, cols, dtype=t).cuda(), eps=0.0, rms=True)
+            assert bool((rstd == 1).all()) and bool((y == 1).all()), (cols, t)
+
+
+@pytest.mark.parametrize("cols", [41, 300, 1000, 5000, 20000])
+def test_rows_whose_squares_overflow(cols):
+    """The sum of squares is a float: above it rstd is 0, as that of an infinity, and no other row is touched."""
+    x = torch.ones(3, cols)
+    x[1] *= 3e19
+    x[1, ::2] *= -1
+    for rms in (False, True):
+        y, _, rstd = layers.norm_forward(x.cuda(), None, None, 1e-6, rms=rms)
+        assert rstd[1] == 0 and not y[1].any()
+        assert torch.isfinite(y).all() and (rstd[0::2] > 0).all()
