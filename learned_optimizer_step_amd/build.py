@@ -1,5 +1,5 @@
 """Builds liblopt.so (HIP kernels + C ABI) for gfx950 in-tree, and _layers.so
-(the torch calls of the norms, embedding and distillation loss) over it.
+(the torch calls of the norms, embedding and distillation loss).
 
     python -m learned_optimizer_step_amd.build
 """
@@ -98,9 +98,9 @@ def _link_layers(verbose: bool) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
-    # liblopt.so is found beside _layers.so
+    # not against liblopt.so: its calls are looked up in the one that is loaded
     _run([cxx, "-shared", _layers_object() + ".o", "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_hip",
-          "-L", PKG, "-llopt", "-Wl,-rpath,$ORIGIN", "-o", _layers_object() + ".so"], verbose)
+          "-ldl", "-o", _layers_object() + ".so"], verbose)
 
 
 MICROBENCH = os.path.join(PKG, "lopt_microbench")

@@ -1,7 +1,7 @@
 // The norm, embedding and distillation calls for torch tensors: checks,
 // outputs, workspaces and the automatic differentiation behind
-// learned_optimizer_step_amd/layers.py, built into _layers.so beside liblopt.so
-// (whose C ABI it calls; no kernel is here).
+// learned_optimizer_step_amd/layers.py, built into _layers.so.  It calls the C
+// ABI of the liblopt.so that lopt.load_library() loaded; no kernel is here.
 //
 // It is compiled, unlike the optimizer's ctypes binding, because these calls
 // are many and short and half of them run on autograd's own thread: the same
@@ -14,11 +14,14 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <dlfcn.h>
+
 #include <algorithm>
 #include <optional>
 #include <stdexcept>
 #include <string>
 #include <tuple>
+#include <type_traits>
 
 #include "../../include/lopt.h"
 
@@ -30,6 +33,39 @@ using torch::autograd::Function;
 using torch::autograd::variable_list;
 using Maybe = std::optional<Tensor>;
 
+// The library's calls, looked up in the one that the optimizer's steps run from (LOPT_LIBRARY can name another than the
+// one beside this file).
+struct Library {
+  decltype(&lopt_norm_forward) norm_forward;
+  decltype(&lopt_norm_backward_workspace) norm_backward_workspace;
+  decltype(&lopt_norm_backward) norm_backward;
+  decltype(&lopt_embedding_forward) embedding_forward;
+  decltype(&lopt_embedding_backward_workspace) embedding_backward_workspace;
+  decltype(&lopt_embedding_backward) embedding_backward;
+  decltype(&lopt_distill_forward) distill_forward;
+  decltype(&lopt_distill_backward) distill_backward;
+  decltype(&lopt_last_error) last_error;
+};
+Library lib;
+
+void bind(uintptr_t handle) {
+  Library l;
+  const auto find = [&](auto& call, const char* name) {
+    call = reinterpret_cast<std::decay_t<decltype(call)>>(dlsym(reinterpret_cast<void*>(handle), name));
+    if (!call) throw pybind11::import_error(std::string(name) + " is missing in the liblopt.so that is loaded");
+  };
+  find(l.norm_forward, "lopt_norm_forward");
+  find(l.norm_backward_workspace, "lopt_norm_backward_workspace");
+  find(l.norm_backward, "lopt_norm_backward");
+  find(l.embedding_forward, "lopt_embedding_forward");
+  find(l.embedding_backward_workspace, "lopt_embedding_backward_workspace");
+  find(l.embedding_backward, "lopt_embedding_backward");
+  find(l.distill_forward, "lopt_distill_forward");
+  find(l.distill_backward, "lopt_distill_backward");
+  find(l.last_error, "lopt_last_error");
+  lib = l;
+}
+
 // A call that liblopt refused: lopt.LoptError in Python.
 struct Refused : std::runtime_error {
   int status;
@@ -37,7 +73,7 @@ struct Refused : std::runtime_error {
 };
 
 void check(lopt_status s) {
-  if (s != LOPT_OK) throw Refused(int(s), lopt_last_error());
+  if (s != LOPT_OK) throw Refused(int(s), lib.last_error());
 }
 
 [[noreturn]] void bad(const std::string& message) { throw pybind11::value_error(message); }
@@ -142,7 +178,7 @@ std::tuple<Tensor, Tensor> norm_forward(const Tensor& x, const Maybe& weight, co
   Tensor y = empty(x.sizes(), x.scalar_type(), device);
   Tensor stats = empty({rms ? 1 : 2, m.rows}, at::kFloat, device);
   float* at = static_cast<float*>(stats.data_ptr());
-  check(lopt_norm_forward(rms ? LOPT_NORM_RMS : LOPT_NORM_LAYER, m.rows, m.cols, code, m.data(), m.ld, ptr(w), ptr(b), wcode,
+  check(lib.norm_forward(rms ? LOPT_NORM_RMS : LOPT_NORM_LAYER, m.rows, m.cols, code, m.data(), m.ld, ptr(w), ptr(b), wcode,
                           float(eps), y.data_ptr(), m.cols, rms ? nullptr : at, rms ? at : at + m.rows, stream(device)));
   return {y, stats};
 }
@@ -174,10 +210,10 @@ NormGrads norm_backward(const Tensor& dy, const Tensor& x, const Maybe& weight, 
   Tensor ws;
   size_t bytes = 0;
   if (gw.defined()) {
-    check(lopt_norm_backward_workspace(m.rows, m.cols, &bytes));
+    check(lib.norm_backward_workspace(m.rows, m.cols, &bytes));
     ws = empty({int64_t(bytes)}, at::kByte, device);
   }
-  check(lopt_norm_backward(rms ? LOPT_NORM_RMS : LOPT_NORM_LAYER, m.rows, m.cols, code, g.data(), g.ld, m.data(), m.ld, ptr(w),
+  check(lib.norm_backward(rms ? LOPT_NORM_RMS : LOPT_NORM_LAYER, m.rows, m.cols, code, g.data(), g.ld, m.data(), m.ld, ptr(w),
                            w.defined() ? dtype_code(w.scalar_type(), "weight") : LOPT_F32, mean, rstd, ptr(out.dx), m.cols,
                            ptr(out.dw), ptr(out.db), gw.defined() ? dtype_code(gw.scalar_type(), "grad_weight") : LOPT_F32,
                            accumulate, ptr(ws), bytes, stream(device)));
@@ -226,7 +262,7 @@ Tensor embedding_forward(const Tensor& ids, const Tensor& weight, double scale, 
   c10::SmallVector<int64_t, 5> shape(ids.sizes().begin(), ids.sizes().end());
   shape.push_back(w.cols);
   Tensor out = empty(shape, type, device);
-  check(lopt_embedding_forward(i.numel(), i.data_ptr(), nb, w.rows, w.cols, row0, w.data(), w.ld, code, float(scale),
+  check(lib.embedding_forward(i.numel(), i.data_ptr(), nb, w.rows, w.cols, row0, w.data(), w.ld, code, float(scale),
                                out.data_ptr(), w.cols, ocode, stream(device)));
   return out;
 }
@@ -245,9 +281,9 @@ Tensor embedding_backward(const Tensor& dout, const Tensor& ids, int64_t rows, d
   const c10::DeviceGuard guard(device);
   Tensor dw = output(to, {rows, g.cols}, device, dtype, "out");
   size_t bytes = 0;
-  check(lopt_embedding_backward_workspace(g.rows, rows, g.cols, &bytes));
+  check(lib.embedding_backward_workspace(g.rows, rows, g.cols, &bytes));
   const Tensor ws = empty({int64_t(bytes)}, at::kByte, device);
-  check(lopt_embedding_backward(g.rows, i.data_ptr(), nb, g.data(), g.ld, code, rows, g.cols, row0, float(scale), dw.data_ptr(),
+  check(lib.embedding_backward(g.rows, i.data_ptr(), nb, g.data(), g.ld, code, rows, g.cols, row0, float(scale), dw.data_ptr(),
                                 g.cols, dtype_code(dw.scalar_type(), "dtype"), accumulate, ws.data_ptr(), bytes, stream(device)));
   return dw;
 }
@@ -299,7 +335,7 @@ std::tuple<Tensor, Tensor> distill_forward(const Tensor& logits, const Tensor& i
   const at::IntArrayRef shape = logits.sizes().slice(0, logits.dim() - 1);
   const c10::DeviceGuard guard(l.device);
   Tensor loss = empty(shape, at::kFloat, l.device), lse = empty(shape, at::kFloat, l.device);
-  check(lopt_distill_forward(l.z.rows, l.z.cols, l.code, l.z.data(), l.z.ld, int32_t(std::min<int64_t>(l.i.cols, INT32_MAX)),
+  check(lib.distill_forward(l.z.rows, l.z.cols, l.code, l.z.data(), l.z.ld, int32_t(std::min<int64_t>(l.i.cols, INT32_MAX)),
                              l.i.data(), l.i.ld, l.nb, l.u.data(), l.u.ld, l.ucode, float(temperature),
                              static_cast<float*>(loss.data_ptr()), static_cast<float*>(lse.data_ptr()), stream(l.device)));
   return {loss, lse};
@@ -322,7 +358,7 @@ Tensor distill_backward(const Tensor& grad_loss, const Tensor& logits, const Ten
   if (g.numel() > 1 && g.stride(0) >= (int64_t(1) << 28)) g = g.contiguous();
   const int64_t step = g.numel() > 1 ? g.stride(0) : 0;   // a single element's stride can be anything
   const Tensor s = lse.contiguous();
-  check(lopt_distill_backward(l.z.rows, l.z.cols, l.code, static_cast<const float*>(g.data_ptr()), step, l.z.data(), l.z.ld,
+  check(lib.distill_backward(l.z.rows, l.z.cols, l.code, static_cast<const float*>(g.data_ptr()), step, l.z.data(), l.z.ld,
                               int32_t(std::min<int64_t>(l.i.cols, INT32_MAX)), l.i.data(), l.i.ld, l.nb, l.u.data(), l.u.ld,
                               l.ucode, float(temperature), static_cast<const float*>(s.data_ptr()), dz.data_ptr(), l.z.cols,
                               stream(l.device)));
@@ -356,6 +392,7 @@ std::optional<at::ScalarType> scalar_type(const pybind11::object& dtype) {
 
 PYBIND11_MODULE(_layers, m) {
   namespace py = pybind11;
+  bind(py::module_::import("learned_optimizer_step_amd.lopt").attr("load_library")().attr("_handle").cast<uintptr_t>());
   py::register_local_exception_translator([](std::exception_ptr p) {
     try {
       if (p) std::rethrow_exception(p);

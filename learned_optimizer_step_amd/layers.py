@@ -21,7 +21,7 @@ library ``lopt.LoptError``.
 
 The calls are compiled (csrc/layers.cpp, built into _layers.so by
 ``python -m learned_optimizer_step_amd.build``); importing this module fails
-when they are not built.
+when they are not built.  They run from the library that ``lopt`` has loaded.
 """
 from __future__ import annotations
 
@@ -29,10 +29,7 @@ from typing import Optional
 
 import torch
 
-from . import lopt as L
-
-L.load_library()    # with torch's HIP runtime, before _layers.so binds to it
-from . import _layers as _C  # noqa: E402
+from . import _layers as _C
 
 
 # ---------------------------------------------------------------------------

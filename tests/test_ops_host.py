@@ -140,3 +140,28 @@ def test_layers_have_no_cpu_path(lib):
 def test_the_struct_free_calls_refuse_what_is_no_number(lib):
     with pytest.raises(ctypes.ArgumentError):
         L.lopt_norm_forward(*{**NORM_FWD, "rows": "5"}.values())
+
+
+def test_the_torch_calls_run_from_the_library_that_the_steps_run_from(lib, tmp_path):
+    """LOPT_LIBRARY names another build: the norms, the embedding and the distillation loss are that one's too."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    other = tmp_path / "liblopt_other.so"
+    shutil.copy(L.LIB_PATH, other)
+    code = """if True:
+        from learned_optimizer_step_amd import layers, lopt
+        import torch
+        try:
+            layers.layer_norm(torch.ones(2, 3))
+        except ValueError as e:
+            assert "GPU" in str(e)
+        maps = {l.split()[-1] for l in open("/proc/self/maps") if "liblopt" in l}
+        print(sorted(maps))
+    """
+    env = dict(os.environ, LOPT_LIBRARY=str(other))
+    root = os.path.dirname(os.path.dirname(os.path.abspath(L.__file__)))
+    out = subprocess.run([sys.executable, "-c", code], env=env, cwd=root, capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.strip() == str([str(other)])
