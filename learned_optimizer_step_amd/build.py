@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+from typing import Optional
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -41,7 +42,7 @@ def _run(cmd, verbose):
     noise = ("is not a recognized feature for this target", "argument unused during compilation")
     msgs = [l for l in (res.stdout + res.stderr).splitlines() if not any(x in l for x in noise)]
     if res.returncode != 0:
-        raise RuntimeError("hipcc failed:\n" + "\n".join(msgs))
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n" + "\n".join(msgs))
     if verbose and msgs:
         print("\n".join(msgs))
 
@@ -59,17 +60,15 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
         objs.append(obj)
     with concurrent.futures.ThreadPoolExecutor(len(cmds) + 1) as ex:
         jobs = [ex.submit(_run, cmd, verbose) for cmd in cmds]
-        if out == LIB:
-            jobs.append(ex.submit(_compile_layers, verbose))
+        layers = ex.submit(build_layers, verbose) if out == LIB else None
         for f in jobs:
             f.result()
-    out_tmp = out + ".tmp"
-    _run([hipcc(), "-shared", "-fPIC", *objs, "-o", out_tmp], verbose)
-    os.replace(out_tmp, out)
+        out_tmp = out + ".tmp"
+        _run([hipcc(), "-shared", "-fPIC", *objs, "-o", out_tmp], verbose)
+        os.replace(out_tmp, out)
     if out == LIB:
-        _link_layers(verbose)
-        os.replace(_layers_object() + ".so", LAYERS)
         build_microbench(verbose)
+        layers.result()    # last: liblopt.so needs neither torch nor a host compiler
     return out
 
 
@@ -80,8 +79,12 @@ def _layers_object() -> str:
     return os.path.join(PKG, "_build", "layers")
 
 
-def _compile_layers(verbose: bool) -> None:
-    """csrc/layers.cpp for the host, against the installed torch."""
+def build_layers(verbose: bool = False) -> Optional[str]:
+    """_layers.so from csrc/layers.cpp, for the host, against the installed torch; nothing where there is no torch."""
+    import importlib.util
+    if importlib.util.find_spec("torch") is None:
+        print("torch is not installed: _layers.so is not built (liblopt.so does not need it)", file=sys.stderr)
+        return None
     import sysconfig
     import torch
     from torch.utils import cpp_extension
@@ -92,15 +95,12 @@ def _compile_layers(verbose: bool) -> None:
           "-DTORCH_EXTENSION_NAME=_layers", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
           "-isystem", "/opt/rocm/include", "-isystem", sysconfig.get_paths()["include"],
           os.path.join(CSRC, "layers.cpp"), "-o", obj], verbose)
-
-
-def _link_layers(verbose: bool) -> None:
-    import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
     # not against liblopt.so: its calls are looked up in the one that is loaded
     _run([cxx, "-shared", _layers_object() + ".o", "-L", lib, "-ltorch", "-ltorch_cpu", "-ltorch_python", "-lc10", "-lc10_hip",
           "-ldl", "-o", _layers_object() + ".so"], verbose)
+    os.replace(_layers_object() + ".so", LAYERS)
+    return LAYERS
 
 
 MICROBENCH = os.path.join(PKG, "lopt_microbench")
