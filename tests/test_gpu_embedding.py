@@ -13,8 +13,8 @@ from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
 from ops_cases import CODE, TYPES, U, close, rounding  # noqa: E402
 
-# (tokens, rows, columns): the sort's passes (rows below and from 256, 65536), its tiles of 4096 tokens, chunks that end
-# inside runs, widths around the slabs of 64 vectors
+# (tokens, rows, columns): the sort's passes (rows below and from 256, 65536), its tiles of 1024 tokens and its one-block
+# limit of 8192, chunks that end inside runs, widths around the slabs of 64 vectors
 SHAPES = [(1, 1, 1), (1, 7, 5), (3, 2, 64), (77, 1000, 65), (8, 255, 33), (64, 256, 8), (500, 257, 130), (4095, 300, 17),
           (4096, 65535, 20), (4097, 65536, 12), (9000, 70001, 8), (1024, 3, 257), (2000, 50257, 40), (5000, 1, 70),
           (16384, 500, 12), (16385, 500, 12), (40000, 1000, 36), (333, 40, 513), (333, 40, 1030), (50, 20, 2048),
@@ -261,3 +261,48 @@ def test_a_handful_of_tokens_of_more_columns_than_one_grid_has_threads_for():
         assert bool((out[r, 1:-1] == want).all()), r
         assert out[r, 0] == want + 0.5 * (-7.0 - (127 % 5 - 2)) * (127 % 4 - 1 == r), r
         assert out[r, -1] == want + 0.5 * (9.0 - (7 % 5 - 2)) * (7 % 4 - 1 == r), r
+
+
+def ids_with_runs(n, rows, chunk, seed):
+    """Ids whose sorted runs begin and end 0, 1, 7, 8, 9 and 10 tokens behind borders of chunks, near ones and far ones, in
+    any order; every 20th token names no row."""
+    g = torch.Generator().manual_seed(seed)
+    named, at, counts = n - n // 20, 0, []
+    while at < named and len(counts) < rows - 1:
+        k = len(counts)
+        ahead = 300 if k % 50 == 25 else (0, 1, 1, 2, 3, 1, 6)[k % 7]
+        end = (at // chunk + ahead) * chunk + (0, 1, 7, 8, 9, 10, 8, 9)[k % 8]
+        end = min(named, end if end > at else at + 1 + k % 3)
+        counts.append(end - at)
+        at = end
+    counts.append(named - at)
+    which = torch.randperm(rows, generator=g)[:len(counts)].sort().values
+    ids = torch.cat([which.repeat_interleave(torch.tensor(counts)), torch.full((n - named,), -1)])
+    return ids[torch.randperm(n, generator=g)]
+
+
+@pytest.mark.parametrize("n,rows,cols,chunk", [
+    (8192, 3000, 40, 8), (8193, 3000, 40, 8), (16383, 60000, 5, 8),          # the longest list of one block, and the next
+    (65535, 5000, 30, 8), (65536, 5000, 30, 16), (131072, 9000, 9, 32), (196608, 9000, 64, 48), (196608, 9000, 3, 48),
+    (13120, 700, 1040, 16), (26240, 1000, 1037, 32), (39360, 1500, 1040, 48),   # several slabs
+    (262145, 200, 8, 48), (300001, 40000, 6, 48), (1100003, 300, 4, 48),     # blocks of the sort that take more than one tile
+    (9000, (1 << 24) + 5, 2, 8), (70000, (1 << 24) + 5, 1, 16), (8000, (1 << 24) + 5, 1, 8)])   # four passes
+@pytest.mark.parametrize("dt,gt", [(torch.bfloat16, torch.float32), (torch.float32, torch.float32), (torch.float16, torch.bfloat16)],
+                         ids=str)
+def test_the_geometry_of_long_lists(n, rows, cols, chunk, dt, gt):
+    """Whole numbers, whose sums are exact in fp32 in any order, for every length of a chunk."""
+    slabs = (cols + 255) // 256
+    assert chunk == max([8] + [c for c in (16, 32, 48) if n // c * slabs >= 4096])
+    ids = ids_with_runs(n, rows, chunk, n)
+    g = torch.Generator().manual_seed(cols)
+    d = torch.randint(-8, 9, (n, cols), generator=g).to(dt)
+    there = ids >= 0
+    want = torch.zeros(rows, cols, dtype=torch.float64).index_add_(0, ids[there], d[there].double())
+    assert want.abs().max() < 2 ** 24
+    base = torch.randint(-8, 9, (rows, cols), generator=g).to(gt)
+    ids, d = ids.cuda(), d.cuda()
+    out = torch.full((rows, cols), math.nan, dtype=gt, device="cuda")
+    assert torch.equal(layers.embedding_backward(d, ids, rows, out=out).cpu(), want.float().to(gt))
+    # one rounding of the sum, and rows that no token names as they were
+    added = layers.embedding_backward(d, ids, rows, out=base.cuda(), accumulate=True)
+    assert torch.equal(added.cpu(), (want + base.double()).float().to(gt))
