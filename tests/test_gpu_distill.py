@@ -363,3 +363,41 @@ def test_one_row_whose_weight_has_a_large_stride():
     _, lse = layers.distill_forward(z, ids, u)
     want = layers.distill_backward(dl, z, ids, u, lse)
     assert torch.equal(layers.distill_backward(dl.as_strided((1,), (1 << 28,)), z, ids, u, lse), want)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_rows_that_are_read_past_the_cache(t):
+    """The first rows of more than 200 MB are read another way than the last ones."""
+    cols, rows = 20001, 240_000_000 // (20001 * torch.finfo(t).bits // 8)
+    g = torch.Generator(device="cuda").manual_seed(17)
+    z = (3 * torch.randn(rows, cols, generator=g, device="cuda")).to(t)
+    ids = torch.randint(0, cols, (rows, 12), generator=g, device="cuda")
+    u = torch.randn(rows, 12, generator=g, device="cuda")
+    dl = torch.randn(rows, generator=g, device="cuda")
+    loss, lse = layers.distill_forward(z, ids, u, 2.0)
+    dz = layers.distill_backward(dl, z, ids, u, lse, 2.0)
+    for part in (slice(0, 24), slice(rows // 6 - 12, rows // 6 + 12), slice(rows - 24, rows)):
+        zp, ip, up, lp = (v[part].cpu() for v in (z, ids, u, lse))
+        want = distill(zp, ip, up, 2.0)
+        tl, e = tols(zp, *want, 2.0, t)
+        close(lse[part], want[1], e, f"{part} lse")
+        close(loss[part], want[0], tl, f"{part} loss")
+        _, _, qp, q, dense, size, _ = distill(zp, ip, up, 2.0, lp)
+        s = (dl[part].double().cpu() * 2.0)[:, None]
+        tol = s.abs() * U * (8 * size[:, None] * q + (16 * size[:, None] + 12) * dense)
+        close(dz[part], qp * s, rounding(qp * s, t) + tol + s.abs() * 2.0 ** -125, f"{part} dz")
+
+
+def test_strided_logits_within_the_bounds():
+    """Rows that begin at other places of a 16-byte piece, each within the bounds by itself."""
+    rows, cols, top, ld = 21, 777, 9, 801
+    for t in TYPES:
+        z, ids, u, dl = make(rows, cols, top, t, torch.float32, torch.int64, 10)
+        big = torch.full((rows + 1, ld), 9.0, dtype=t, device="cuda")
+        want = distill(z, ids, u, 2.0)
+        tl, e = tols(z, *want, 2.0, t)
+        for at in (0, 1, 4, 7):
+            big[:rows, at:at + cols] = z.cuda()
+            loss, lse = layers.distill_forward(big[:rows, at:at + cols], ids.cuda(), u.cuda(), 2.0)
+            close(loss, want[0], tl, f"{t} {at} loss")
+            close(lse, want[1], e, f"{t} {at} lse")
