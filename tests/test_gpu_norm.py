@@ -348,3 +348,19 @@ def test_rows_whose_squares_overflow(cols):
         y, _, rstd = layers.norm_forward(x.cuda(), None, None, 1e-6, rms=rms)
         assert rstd[1] == 0 and not y[1].any()
         assert torch.isfinite(y).all() and (rstd[0::2] > 0).all()
+
+
+@pytest.mark.parametrize("given,which", [(g, w) for g in ("x", "xw", "xb", "xwb") for w in ("x", "w", "b", "xw", "xb", "wb", "xwb")
+                                         if set(w) <= set(g)])
+def test_autograd_of_any_of_the_tensors(given, which):
+    """Each gradient reaches its own tensor, whichever are there and whichever want one."""
+    x, dy, w, b = gpu(*make(20, 130, torch.float32, torch.float32, 51))
+    have = {"x": x, "w": w if "w" in given else None, "b": b if "b" in given else None}
+    for k in which:
+        have[k].requires_grad_(True)
+    y = layers.layer_norm(have["x"], have["w"], have["b"])
+    got = torch.autograd.grad(y, [have[k] for k in which], dy)
+    plain = {k: None if v is None else v.detach() for k, v in have.items()}
+    _, mean, rstd = layers.norm_forward(plain["x"], plain["w"], plain["b"])
+    want = dict(zip("xwb", layers.norm_backward(dy, plain["x"], plain["w"], mean, rstd)))
+    assert all(torch.equal(g, want[k]) for g, k in zip(got, which))

@@ -196,3 +196,31 @@ def test_distill_definition_of_the_tests():
     grad, = torch.autograd.grad(loss.sum(), z)
     got = distill(z.detach(), tid, tu, TAU)
     assert torch.allclose(got[0], loss, rtol=1e-12, atol=1e-12) and torch.allclose(got[2] * TAU, grad, rtol=1e-10, atol=1e-13)
+
+
+def test_gradients_through_autograd_in_a_graph():
+    """Forward and backward through autograd captured once, replayed on new tokens; each replay against the same run made
+    eagerly on copies of the parameters."""
+    ps = [p.cuda().requires_grad_(True) for p in parameters()]
+    copies = [p.detach().clone().requires_grad_(True) for p in ps]
+    ids, tid, tu = (v.cuda() for v in data(0))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):      # the products' library is loaded before the capture
+        torch.autograd.grad(run(copies, ids, tid, tu), copies)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = run(ps, ids, tid, tu)
+        grads = torch.autograd.grad(loss, ps)
+        loss = loss.detach()
+    for t in range(1, 5):
+        for to, v in zip((ids, tid, tu), data(t)):
+            to.copy_(v)
+        want_loss = run(copies, ids, tid, tu)
+        want = torch.autograd.grad(want_loss, copies)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want_loss.detach()), t
+        assert [torch.equal(a, b) for a, b in zip(grads, want)] == [True] * 5, t
