@@ -521,7 +521,8 @@ lopt_status lopt_embedding_backward(int64_t n_ids, const void* ids, int32_t id_b
  * that is listed twice counts with both entries.  A row without an entry has
  * loss 0, whatever its logits are.  An entry whose p rounds to 0 adds nothing.
  * lse is rounded to a float, so the gradient's exp(z_v / tau - lse) is off by
- * 2^-24 |lse| of itself; of finite logits, no lse is below the least float.
+ * 2^-24 |lse| of itself, and is held to 1; of finite logits, no lse is below
+ * the least float.
  * loss, lse: rows floats, NULL: not written.  temperature: finite, > 0.  At
  * most LOPT_MAX_TOP entries. */
 lopt_status lopt_distill_forward(int64_t rows, int64_t cols, int32_t dtype, const void* logits, int64_t ldz, int32_t top,

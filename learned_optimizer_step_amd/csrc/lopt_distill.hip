@@ -30,6 +30,7 @@ namespace {
 constexpr int64_t kKeptBytes = 200'000'000;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kFar = 1 << 20;   // scaled logits beyond this are taken for differences: see k_distill_forward
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -98,12 +99,13 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
     if (nan) top_u = NAN;
 
     // running maximum m of z and sum s of 2^(z c - mc), per thread, with mc the rounded m c: the sum is rescaled by that
-    // same number, as half a step of m c (2^-19 at 60) is more than the sum's own roundings.  m c may overflow (a mask of
-    // the type's lowest value) where the row's largest does not: held finite, such a thread's terms vanish beside it
+    // same number, as half a step of m c (2^-19 at 60) is more than the sum's own roundings.  A thread may see nothing but
+    // masks of -1e9 or the type's lowest value, whose m c overflows or has half steps that are exponents of their own: mc
+    // is held within kFar, where half a step is 2^-5 or less (any mc is right for the sum, and such terms vanish)
     float m = -INFINITY, s = 0.f, mc = 0.f;
     const auto rise = [&](float top) {
       const float old = mc;
-      mc = top == -INFINITY ? 0.f : fminf(fmaxf(top * c, -FLT_MAX), FLT_MAX);   // all -inf so far: terms are 2^-inf = 0
+      mc = top == -INFINITY ? 0.f : fminf(fmaxf(top * c, -kFar), kFar);   // all -inf so far: terms are 2^-inf = 0
       asm("" : "+v"(mc));                      // one number for all its uses: no fma takes the product's place
       s = m == -INFINITY ? 0.f * s : s * exp2_hw(old - mc);
       m = top;
@@ -157,8 +159,8 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
       mu = fmaxf(mu, maxima[1][k]);
     }
     rise(mz);
-    const bool far = mz != -INFINITY && !(fabsf(mz * c) <= FLT_MAX);
-    if (far) {   // the row's largest logit cannot be scaled: its sum again, of differences
+    const bool far = mz != -INFINITY && !(fabsf(mz * c) <= kFar);
+    if (far) {   // the row's largest logit is out there itself: its sum again, of differences
       s = 0.f;
       for (int64_t i = threadIdx.x; i < n; i += B) s += exp2_hw((to_f32(z[i]) - mz) * c);
     }
@@ -273,7 +275,8 @@ __global__ __launch_bounds__(B) void k_distill_backward(DistillBackward a, int p
     for (int k = 1; k < W; ++k) sum += sums[k];
 
     const bool some = top_u != -INFINITY;
-    const auto softmax = [&](float x) { return exp2_hw(fmaf(x, a.inv_tau, -lse) * kLog2e); };
+    // a probability is at most 1: half a step of a large lse is an exponent of its own (NaN stays NaN)
+    const auto softmax = [&](float x) { return exp2_hw(__builtin_elementwise_minimum(fmaf(x, a.inv_tau, -lse) * kLog2e, 0.f)); };
     const auto grad = [&](float x) { return from_f32<T>(some ? scale * softmax(x) : 0.f); };
 #pragma unroll
     for (int e = 0; e < NE; ++e)

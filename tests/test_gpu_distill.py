@@ -401,3 +401,42 @@ def test_strided_logits_within_the_bounds():
             loss, lse = layers.distill_forward(big[:rows, at:at + cols], ids.cuda(), u.cuda(), 2.0)
             close(loss, want[0], tl, f"{t} {at} loss")
             close(lse, want[1], e, f"{t} {at} lse")
+
+
+@pytest.mark.parametrize("tau", [0.25, 1.0, 3.0])
+@pytest.mark.parametrize("mask", [-1e6, -1e9, -3e10, -1e20, -1e30])
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16], ids=str)
+def test_masks_of_large_finite_values(t, mask, tau):
+    """As good as -inf, in threads that see nothing else too: half a step of the scaled mask is no exponent."""
+    for cols, kept in ((3000, 700), (50001, 300)):
+        z, ids, u, dl = make(6, cols, 5, t, torch.float32, torch.int64, cols, absent=0.0)
+        ids = torch.where(ids < 0, ids, ids % kept)
+        g = torch.Generator().manual_seed(cols)
+        m, z = z.clone(), z.clone()
+        z[:, kept:] = (mask * (1 + torch.rand(6, cols - kept, generator=g))).to(t)
+        m[:, kept:] = -math.inf
+        loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+        want = distill(m, ids, u, tau)
+        tl, e = tols(m, *want, tau, t)
+        close(lse, want[1], e, f"{cols} lse")
+        close(loss, want[0], tl, f"{cols} loss")
+        dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau)
+        _, _, qp, q, dense, size, _ = distill(m, ids, u, tau, lse.cpu())
+        s = (dl.double() * tau)[:, None]
+        tol = s.abs() * U * (8 * size[:, None] * q + (16 * size[:, None] + 5) * dense)
+        close(dz, qp * s, rounding(qp * s, t) + tol + s.abs() * 2.0 ** -125, f"{cols} dz")
+
+
+@pytest.mark.parametrize("tau", [1e-12, 1e-3, 0.25, 1.0, 3.0])
+@pytest.mark.parametrize("at", [-1e30, -3e10, 1e6, 1e10, 1e12])
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16], ids=str)
+def test_rows_far_from_zero(t, at, tau):
+    """Rows about a large value: the loss is exact; the gradient is off by the rounding of lse, which can be all of it, but
+    no element is larger than the loss's weight times 1 + the teacher's share."""
+    z, ids, u, dl = make(4, 2500, 9, torch.float32, torch.float32, torch.int64, 2, absent=0.0)
+    z = (z + at).to(t)
+    loss, lse = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+    want = shifted(z, ids, u, torch.tensor(tau, dtype=torch.float32).double().item())
+    close(loss, want[0], tols(z, *want, tau, t)[0] + 2 * U * want[0].abs(), "loss")
+    dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau).double().cpu()
+    assert bool((dz.abs() <= (1 + 2.0 ** -7) * dl.double().abs()[:, None] * tau).all())
