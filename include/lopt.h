@@ -523,8 +523,8 @@ lopt_status lopt_embedding_backward(int64_t n_ids, const void* ids, int32_t id_b
  * lse is rounded to a float, so the gradient's exp(z_v / tau - lse) is off by
  * 2^-24 |lse| of itself, and is held to 1; of finite logits, no lse is below
  * the least float.
- * loss, lse: rows floats, NULL: not written.  temperature: finite, > 0.  At
- * most LOPT_MAX_TOP entries. */
+ * loss, lse: rows floats, NULL: not written.  temperature: finite and > 0, and
+ * its square and 1.5 / temperature floats too.  At most LOPT_MAX_TOP entries. */
 lopt_status lopt_distill_forward(int64_t rows, int64_t cols, int32_t dtype, const void* logits, int64_t ldz, int32_t top,
                                  const void* ids, int64_t ldi, int32_t id_bytes, const void* teacher, int64_t ldu,
                                  int32_t u_dtype, float temperature, float* loss, float* lse, void* stream);

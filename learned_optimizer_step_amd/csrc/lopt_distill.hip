@@ -197,7 +197,7 @@ __global__ __launch_bounds__(B) void k_distill_forward(DistillForward a) {
         const float lse = fmaf(mz, a.inv_tau, kLn2 * (log2f(s) - rest));
         a.lse[r] = far && lse == -INFINITY ? -FLT_MAX : lse;
       }
-      if (a.loss) a.loss[r] = mu == -INFINITY ? 0.f : a.tau * a.tau * fmaf(kLn2, log2f(s / es) - rest, eu / es);
+      if (a.loss) a.loss[r] = mu == -INFINITY ? 0.f : a.tau * (a.tau * fmaf(kLn2, log2f(s / es) - rest, eu / es));   // tau^2 alone can vanish
     }
     // the next row's exchanges write `maxima` after this barrier's reads of it, and `sums` after its own first barrier
   }

@@ -83,8 +83,9 @@ void check_ids(int32_t id_bytes) {
 }
 
 void check_temperature(float tau) {
-  if (!std::isfinite(tau) || !(tau > 0.f) || !std::isfinite(1.f / tau))
-    fail(LOPT_ERR_INVALID_ARGUMENT, "temperature must be finite and > 0");
+  // the loss has the factor tau^2, exponents the factor log2(e) / tau
+  if (!std::isfinite(tau) || !(tau > 0.f) || !std::isfinite(1.5f / tau) || !std::isfinite(tau * tau))
+    fail(LOPT_ERR_INVALID_ARGUMENT, "temperature must be finite and > 0, and so must its square and 1.5 / temperature");
 }
 
 size_t norm_bytes(int64_t rows, int64_t cols) {

@@ -440,3 +440,14 @@ def test_rows_far_from_zero(t, at, tau):
     close(loss, want[0], tols(z, *want, tau, t)[0] + 2 * U * want[0].abs(), "loss")
     dz = layers.distill_backward(dl.cuda(), z.cuda(), ids.cuda(), u.cuda(), lse, tau).double().cpu()
     assert bool((dz.abs() <= (1 + 2.0 ** -7) * dl.double().abs()[:, None] * tau).all())
+
+
+def test_the_coldest_temperatures():
+    """Near zero the loss is tau times the largest logit's lead over the taught one, also where tau^2 is no float."""
+    z = torch.tensor([[3.0, 1.0, -2.0], [0.0, 5.0, 4.0]])
+    ids, u = torch.tensor([[1], [2]]), torch.zeros(2, 1)
+    for tau in (1e-6, 1e-20, 1e-25, 1e-30):
+        t32 = torch.tensor(tau, dtype=torch.float32).double().item()
+        loss, _ = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
+        want = t32 * torch.tensor([2.0, 1.0], dtype=torch.float64)
+        close(loss, want, 8 * U * want, f"{tau}")     # 1 / tau, its product with the lead, two factors tau, and log s = 0

@@ -165,3 +165,11 @@ def test_the_torch_calls_run_from_the_library_that_the_steps_run_from(lib, tmp_p
     out = subprocess.run([sys.executable, "-c", code], env=env, cwd=root, capture_output=True, text=True, timeout=300)
     assert out.returncode == 0, out.stderr
     assert out.stdout.strip() == str([str(other)])
+
+
+@pytest.mark.parametrize("call,args", [("lopt_distill_forward", DIS_FWD), ("lopt_distill_backward", DIS_BWD)])
+@pytest.mark.parametrize("temperature", [2e19, 3e38, 4e-39, 3e-39])
+def test_temperatures_whose_factors_are_no_floats(lib, call, args, temperature):
+    with pytest.raises(L.LoptError) as e:
+        getattr(L, call)(*{**args, "temperature": temperature}.values())
+    assert e.value.status == BAD and "temperature" in str(e.value)
