@@ -27,7 +27,8 @@
  * The operators behind the step (norms, embedding, distillation loss) produce
  * the gradients it reads; they are declared at the end.
  *
- * All arithmetic on the device is fp32.  Every call returns an lopt_status;
+ * All arithmetic of a step on the device is fp32 (the operators take bf16 and
+ * fp16 too, and their sums are fp32 or wider).  Every call returns an lopt_status;
  * no C++ exception crosses this boundary.  lopt_last_error() gives a
  * thread-local message for the last failing call on the calling thread.
  * A handle is not thread-safe, and the calls on one handle must be ordered on
@@ -514,7 +515,9 @@ lopt_status lopt_embedding_backward(int64_t n_ids, const void* ids, int32_t id_b
  *   p_k = exp(u_k / tau) / sum_j exp(u_j / tau),  lse = log sum_v exp(z_v / tau),
  *   loss = tau^2 sum_k p_k (log p_k - z_(i_k) / tau + lse):
  * tau^2 times the Kullback-Leibler divergence of the student's distribution
- * from the teacher's, which is renormalised over its list.
+ * from the teacher's, which is renormalised over its list.  With top = 1 and
+ * tau = 1 it is the cross-entropy of the listed token, 0 for a row whose id is
+ * outside the vocabulary (an id to ignore).
  * logits: rows x cols of type dtype; ids: rows x top, id_bytes (4 or 8) bytes
  * each, signed; teacher: rows x top of type u_dtype.  An entry whose id lies
  * outside [0, cols) or whose logit is -inf is absent, whatever else it holds; an id

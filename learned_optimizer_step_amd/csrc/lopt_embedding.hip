@@ -35,7 +35,7 @@ constexpr int kReach = 8;         // tokens that a chunk takes from the next one
 // Row of the table that an id names, `rows` if none.
 __device__ __forceinline__ uint32_t row_of(const void* ids, int id_bytes, int64_t t, int64_t row0, int64_t rows) {
   const int64_t id = id_bytes == 8 ? static_cast<const int64_t*>(ids)[t] : int64_t(static_cast<const int32_t*>(ids)[t]);
-  // row0 is within [0, 2^62], so the difference of any two of them is an int64_t
+  // row0 is within [0, 2^40], so an id at or above it gives a difference that is an int64_t
   if (id < row0) return uint32_t(rows);
   const int64_t v = id - row0;
   return uint32_t(v < rows ? v : rows);

@@ -13,8 +13,8 @@ namespace {
 
 // The mean comes from a sum in 64 bits: fp32's would be off by 2^-24 of the
 // values' size, which is much of the spread of a row far from zero, and much of
-// a mean that cancels (65536 x 200 fp32: 27 us, 20 with fp32 sums; bf16, whose
-// threads add in fp32 without roundings, within a few %).  What fp32 cannot hold of it goes into the spread and
+// a mean that cancels (65536 x 200 fp32: 28 us, 25 with fp32 sums; bf16, whose
+// threads add in fp32 without roundings, within 2 %).  What fp32 cannot hold of it goes into the spread and
 // the output.
 struct Moments {
   float mean, rest, rstd;   // mu = mean + rest

@@ -12,7 +12,7 @@ namespace lopt {
 // Element types as the ABI numbers them (lopt_dtype).
 enum : int32_t { kF32 = 0, kBF16 = 1, kF16 = 2 };
 
-// ---- layer norm and RMS norm (lopt_norm.hip) ----
+// ---- layer norm and RMS norm (lopt_norm_forward.hip, lopt_norm_backward.hip) ----
 struct NormForward {
   const void* x;
   const void* w;   // NULL: 1

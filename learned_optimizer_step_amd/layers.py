@@ -11,7 +11,11 @@ supported).  The ``*_forward`` and ``*_backward`` functions below them make
 one call of the library each (include/lopt.h has the formulas); they take
 buffers for the parameters' gradients and can add to what is there, so a
 training step captured into a HIP graph keeps the gradients where the
-optimizer's step reads them.
+optimizer's step reads them.  The differentiable functions can be captured
+with ``torch.autograd.grad`` too; before a ``backward()`` is captured, let go of
+every eager graph of the same leaves: torch accumulates into a leaf on the
+stream where its first live graph was made, which cannot join a capture when
+it is the default stream.
 
 Everything runs on the GPU, on the tensors' device and its current stream;
 nothing waits.  Tensors may be fp32, bf16 or fp16, of any leading shape; a
@@ -98,7 +102,9 @@ def embedding_backward(grad_out, ids, rows: int, scale: float = 1.0, row0: int =
 def distill_loss(logits, teacher_ids, teacher_logits, temperature: float = 1.0):
     """The distillation loss of every row of logits (float32); see ``distill_forward``.
 
-    Differentiable in the logits; the teacher is a constant."""
+    Differentiable in the logits; the teacher is a constant.  A list of one entry
+    of any finite logit is a target: at temperature 1 the loss is the
+    cross-entropy of that token, 0 for an id outside the vocabulary."""
     return _C.distill(logits, teacher_ids, teacher_logits, temperature)
 
 

@@ -451,3 +451,22 @@ def test_the_coldest_temperatures():
         loss, _ = layers.distill_forward(z.cuda(), ids.cuda(), u.cuda(), tau)
         want = t32 * torch.tensor([2.0, 1.0], dtype=torch.float64)
         close(loss, want, 8 * U * want, f"{tau}")     # 1 / tau, its product with the lead, two factors tau, and log s = 0
+
+
+def test_a_target_is_a_list_of_one_entry():
+    """At temperature 1: the cross-entropy of the target, 0 and no gradient where it is an id to ignore."""
+    rows, cols = 40, 700
+    z, _, _, dl = make(rows, cols, 1, torch.float32, torch.float32, torch.int64, 30)
+    target = torch.randint(0, cols, (rows,), generator=torch.Generator().manual_seed(6))
+    target[::7] = -100
+    leaf = z.cuda().requires_grad_(True)
+    loss = layers.distill_loss(leaf, target.cuda()[:, None], torch.zeros(rows, 1, device="cuda"))
+    grad, = torch.autograd.grad(loss, leaf, dl.cuda())
+    z64 = z.double().requires_grad_(True)
+    want = torch.nn.functional.cross_entropy(z64, target, reduction="none", ignore_index=-100)
+    want_grad, = torch.autograd.grad(want, z64, dl.double())
+    size = 1 + z.double().abs().max(1).values * 2 + 10
+    e = (24 * size + 56) * U       # the lse's bound, and the logit's own parts
+    close(loss, want.detach(), e * (target >= 0), "loss")
+    g = dl.double().abs()[:, None] * (target >= 0)[:, None]
+    close(grad, want_grad, g * (e + 2 * U)[:, None], "gradient")
