@@ -543,6 +543,56 @@ lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, con
                                   int32_t id_bytes, const void* teacher, int64_t ldu, int32_t u_dtype, float temperature,
                                   const float* lse, void* dlogits, int64_t lddz, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * AdamW over a list of tensors, beside the learned optimizer's step: decoupled
+ * weight decay, moments in 32 bits or in 8.  The rules of the operators above
+ * hold (no handle, nothing allocated, nothing waits, may be captured). */
+
+/* One tensor of the list.  param: n values of type p_dtype, contiguous, updated
+ * in place (each rounded once).  grad: n values of type g_dtype, read only; NULL: the tensor
+ * is skipped.  state: its moments, lopt_adamw_state_bytes() bytes, 16-byte aligned, zero
+ * before the first step.  lr, weight_decay: finite. */
+typedef struct lopt_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* state;
+  int64_t n;
+  double lr;
+  double weight_decay;
+  int32_t p_dtype;
+  int32_t g_dtype;
+} lopt_adamw_tensor;
+
+#define LOPT_MOMENT_BLOCK 256 /* elements of a block of moments */
+
+/* Bytes of a tensor's moments, in blocks of LOPT_MOMENT_BLOCK elements (the last one is
+ * filled up with zeros):
+ *   state_bits 32: 256 floats m, 256 floats v;
+ *   state_bits 8:  256 codes of m, 256 codes of v, a byte E_m, a byte E_v, 14 bytes unused.
+ * A code of m is a sign (its highest bit), 4 bits of exponent f and 3 of mantissa k, one of v 5
+ * bits of f and 3 of k.  They stand for
+ *   (f > 0 ? 8 + k : k) 2^(max(f, 1) - F - 3 + E - 100)   with F = 15 for m, 31 for v.
+ * E = 255: the block held a NaN or an infinity, and every number of it is NaN from then on.
+ * Blocks of several tensors may follow each other in one buffer.  Host only; 1 <= n <= 2^38. */
+lopt_status lopt_adamw_state_bytes(int64_t n, int32_t state_bits, size_t* bytes);
+
+/* One step over the n tensors of ts (host memory, copied).  With t = *step + 1,
+ *   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2   (two products and a sum in fp32)
+ *   p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * with the m and v from before they are rounded to 8 bits.  8-bit codes are rounded up or down with a
+ * probability that keeps their mean (for each number 32 bits, a hash of seed, t, the tensor's
+ * place in ts and the element's number; 16 for each moment); a v that is not 0 stays so.  step: two 64-bit numbers in device memory, 8-byte aligned: the
+ * count of steps taken, which the call advances (also when every tensor is skipped, not for an empty list), and one that the
+ * library keeps at 0.  So a captured step counts as it is replayed, but keeps lr and the addresses of its capture.
+ * 0 <= beta1, beta2 < 1; eps finite and >= 0.  Params, states and step may not overlap each other or a gradient. */
+lopt_status lopt_adamw_step(const lopt_adamw_tensor* ts, int32_t n, int32_t state_bits, double beta1, double beta2,
+                            double eps, uint32_t seed, int64_t* step, void* stream);
+
+/* The moments of n elements as numbers of type dtype (8-bit ones are exact in fp32 and bf16, but for bf16's and fp32's least
+ * numbers): m, v: n values each, NULL: not written. */
+lopt_status lopt_adamw_moments(const void* state, int64_t n, int32_t state_bits, int32_t dtype, void* m, void* v,
+                               void* stream);
+
 /* Message of the last failing call on this thread ("" if none). */
 const char* lopt_last_error(void);
 

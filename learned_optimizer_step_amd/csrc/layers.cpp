@@ -1,4 +1,4 @@
-// The norm, embedding and distillation calls for torch tensors: checks,
+// The operators' calls for torch tensors: checks,
 // outputs, workspaces and the automatic differentiation behind
 // learned_optimizer_step_amd/layers.py, built into _layers.so.  It calls the C
 // ABI of the liblopt.so that lopt.load_library() loaded; no kernel is here.
@@ -22,6 +22,7 @@
 #include <string>
 #include <tuple>
 #include <type_traits>
+#include <vector>
 
 #include "../../include/lopt.h"
 
@@ -44,6 +45,9 @@ struct Library {
   decltype(&lopt_embedding_backward) embedding_backward;
   decltype(&lopt_distill_forward) distill_forward;
   decltype(&lopt_distill_backward) distill_backward;
+  decltype(&lopt_adamw_state_bytes) adamw_state_bytes;
+  decltype(&lopt_adamw_step) adamw_step;
+  decltype(&lopt_adamw_moments) adamw_moments;
   decltype(&lopt_last_error) last_error;
 };
 Library lib;
@@ -62,6 +66,9 @@ void bind(uintptr_t handle) {
   find(l.embedding_backward, "lopt_embedding_backward");
   find(l.distill_forward, "lopt_distill_forward");
   find(l.distill_backward, "lopt_distill_backward");
+  find(l.adamw_state_bytes, "lopt_adamw_state_bytes");
+  find(l.adamw_step, "lopt_adamw_step");
+  find(l.adamw_moments, "lopt_adamw_moments");
   find(l.last_error, "lopt_last_error");
   lib = l;
 }
@@ -138,14 +145,18 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType t, c10::Device device) {
   return at::empty(shape, at::TensorOptions().dtype(t).device(device));
 }
 
+// A change in place, which autograd looks for in what it has saved.
+void changed(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // A caller's contiguous output, which the call will write, or a new one.
 Tensor output(const Maybe& t, at::IntArrayRef shape, c10::Device device, at::ScalarType type, const char* name) {
   if (!t) return empty(shape, type, device);
   if (t->sizes() != shape || !t->is_contiguous() || t->device() != device)
     bad(std::string(name) + " must be a contiguous tensor of shape " + show(shape) + " on " + device.str());
   dtype_code(t->scalar_type(), name);
-  // a change in place, which autograd looks for in what it has saved
-  if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+  changed(*t);
   return *t;
 }
 
@@ -382,6 +393,79 @@ class Distill : public Function<Distill> {
   }
 };
 
+// ---------------------------------------------------------------------------
+// AdamW
+
+at::ScalarType moment_type(int64_t bits) { return bits == 8 ? at::kByte : at::kFloat; }
+
+size_t moment_bytes(int64_t n, int64_t bits) {
+  size_t bytes = 0;
+  check(lib.adamw_state_bytes(n, int32_t(bits), &bytes));
+  return bytes;
+}
+
+Tensor adamw_state(const Tensor& param, int64_t bits) {
+  const c10::Device device = gpu(param, "param");
+  const size_t bytes = moment_bytes(param.numel(), bits);
+  return at::zeros({int64_t(bytes / c10::elementSize(moment_type(bits)))}, at::TensorOptions().dtype(moment_type(bits)).device(device));
+}
+
+void check_state(const Tensor& s, int64_t n, int64_t bits, c10::Device device, const std::string& name) {
+  on(device, s, name.c_str());
+  const size_t need = moment_bytes(n, bits);
+  if (s.scalar_type() != moment_type(bits) || !s.is_contiguous() || s.nbytes() < need)
+    bad(name + " must be contiguous, " + c10::toString(moment_type(bits)) + " and of " + std::to_string(need) + " bytes");
+}
+
+void adamw_step(const std::vector<Tensor>& params, const std::vector<Maybe>& grads, const std::vector<Tensor>& states,
+                const Tensor& step, const std::vector<double>& lr, double beta1, double beta2, double eps,
+                const std::vector<double>& weight_decay, int64_t bits, int64_t seed) {
+  const size_t n = params.size();
+  if (grads.size() != n || states.size() != n) bad("params, grads and states must be lists of one length");
+  for (const auto* v : {&lr, &weight_decay})
+    if (v->size() != 1 && v->size() != n) bad("lr and weight_decay must be numbers, or one a parameter");
+  const c10::Device device = gpu(step, "step");
+  if (step.scalar_type() != at::kLong || step.numel() != 2 || !step.is_contiguous()) bad("step must be a contiguous int64 tensor of two elements");
+  std::vector<lopt_adamw_tensor> ts(n);
+  std::vector<Tensor> keep;
+  for (size_t i = 0; i < n; ++i) {
+    const Tensor& p = params[i];
+    const auto name = [&](const char* what) { return std::string(what) + " " + std::to_string(i); };
+    on(device, p, name("parameter").c_str());
+    if (!p.is_contiguous()) bad(name("parameter") + " must be contiguous");
+    check_state(states[i], p.numel(), bits, device, name("state"));
+    ts[i] = {p.data_ptr(), nullptr, states[i].data_ptr(), p.numel(), lr[lr.size() == 1 ? 0 : i],
+             weight_decay[weight_decay.size() == 1 ? 0 : i], dtype_code(p.scalar_type(), "a parameter"), 0};
+    if (!grads[i]) continue;
+    Tensor g = *grads[i];
+    if (g.layout() != at::kStrided) bad(name("gradient") + " must be dense");
+    on(device, g, name("gradient").c_str());
+    if (g.sizes() != p.sizes()) bad(name("gradient") + " must have the shape of its parameter");
+    if (!g.is_contiguous()) keep.push_back(g = g.contiguous());
+    ts[i].grad = g.data_ptr();
+    ts[i].g_dtype = dtype_code(g.scalar_type(), "a gradient");
+  }
+  const c10::DeviceGuard guard(device);
+  check(lib.adamw_step(ts.data(), int32_t(n), int32_t(bits), beta1, beta2, eps, uint32_t(seed),
+                       static_cast<int64_t*>(step.data_ptr()), stream(device)));
+  changed(step);
+  for (size_t i = 0; i < n; ++i)
+    if (grads[i]) {
+      changed(params[i]);
+      changed(states[i]);
+    }
+}
+
+std::tuple<Tensor, Tensor> adamw_moments(const Tensor& state, int64_t n, int64_t bits, at::ScalarType dtype) {
+  const c10::Device device = gpu(state, "state");
+  check_state(state, n, bits, device, "state");
+  const int32_t code = dtype_code(dtype, "dtype");
+  const c10::DeviceGuard guard(device);
+  Tensor m = empty({n}, dtype, device), v = empty({n}, dtype, device);
+  check(lib.adamw_moments(state.data_ptr(), n, int32_t(bits), code, m.data_ptr(), v.data_ptr(), stream(device)));
+  return {m, v};
+}
+
 std::optional<at::ScalarType> scalar_type(const pybind11::object& dtype) {
   if (dtype.is_none()) return std::nullopt;
   if (!THPDtype_Check(dtype.ptr())) throw pybind11::type_error("dtype must be a torch.dtype");
@@ -431,6 +515,11 @@ PYBIND11_MODULE(_layers, m) {
   });
   m.def("embedding", [](const Tensor& ids, const Tensor& w, double scale, int64_t row0, const py::object& dtype) {
     return Embedding::apply(ids, w, scale, row0, scalar_type(dtype));
+  });
+  m.def("adamw_state", &adamw_state);
+  m.def("adamw_step", &adamw_step);
+  m.def("adamw_moments", [](const Tensor& state, int64_t n, int64_t bits, const py::object& dtype) {
+    return adamw_moments(state, n, bits, scalar_type(dtype).value_or(at::kFloat));
   });
   m.def("distill_forward", &distill_forward);
   m.def("distill_backward", &distill_backward);

@@ -1,0 +1,319 @@
+// AdamW over a list of tensors, moments in 32 bits or in 8.  With t = 1, 2, ...
+//   m <- b1 m + (1 - b1) g,  v <- b2 v + (1 - b2) g^2
+//   p <- p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+// Bound by HBM: p, m and v are read and written once, g is read once (fp32: 28
+// bytes an element with 32-bit moments, 16.1 with 8-bit ones).
+//
+// The list travels as a kernel argument, kMaxAdamw tensors a launch: nothing is
+// uploaded, so gradients may lie elsewhere at every step, and a captured launch
+// holds its own list.  A wave takes chunks of kChunk elements of one tensor and
+// finds the tensor in the launch's running sum of chunks; tensors of any sizes
+// fill the same grid.
+//
+// The step counter is on the device, so that a captured step counts as it is
+// replayed: every wave reads it first, and the last block of the last launch to
+// finish (a ticket) advances it.
+//
+// 8-bit moments: a block of 256 numbers shares an exponent e, which puts its
+// largest in the highest binade of the codes.  m has a sign, 4 bits of exponent
+// and 3 of mantissa (2^14 from the largest normal code to the least, and 3 bits
+// below), v no sign and 5 bits of exponent (2^30).  Codes are rounded up or down
+// at random, in proportion to what is left: v changes by a thousandth a step
+// with b2 = 0.999, which rounding to the nearest of 3 bits would lose every
+// time, and the codes could neither rise nor decay.  A number is rounded by
+// adding 16 random bits below the code's last bit.  The 32 random bits of an
+// element are a hash of the seed, t, the tensor's place in the list and the
+// element's number.  A v that is not 0 does not round to 0, as its root divides.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "lopt_ops.h"
+#include "lopt_ops_device.h"
+
+namespace lopt {
+namespace {
+
+constexpr int kPerLane = 4, kBlocks = 4;
+constexpr int kChunk = 64 * kPerLane * kBlocks;   // 4 of the moments' blocks
+static_assert(kMomentBlock == 64 * kPerLane, "a wave holds a block of moments");
+static_assert(sizeof(AdamwLaunch) <= 4096, "kernel arguments");
+
+// a b + c d as two products and a sum, each rounded: what the moments' codes
+// are rounded from can be computed elsewhere to the last bit.
+__device__ __forceinline__ float weighted(float a, float b, float c, float d) {
+#pragma clang fp contract(off)
+  return a * b + c * d;
+}
+__device__ __forceinline__ float square(float x) {
+#pragma clang fp contract(off)
+  return x * x;
+}
+
+// A bijection of 32-bit numbers that scatters neighbours (the finalizer of MurmurHash3).
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
+  x = (x ^ (x >> 13)) * 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+
+struct Highest {   // of non-negative floats by their bits, a NaN above all
+  __device__ __forceinline__ float operator()(float a, float b) const {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    return __uint_as_float(x > y ? x : y);
+  }
+};
+
+// Codes of FIELDS exponents over 3 bits of mantissa.
+template <int FIELDS>
+struct Codes {
+  // Exponent of a block whose largest number is `top`: the next one where top could round up out of the codes.
+  static __device__ __forceinline__ int exponent(float top) {
+    const int e = int((__float_as_uint(top) + 0x100000u) >> 23) - 127;
+    return e < -100 ? -100 : e > 127 ? 127 : e;
+  }
+  // x >= 0, r: 16 random bits
+  static __device__ __forceinline__ uint32_t encode(float x, int e, uint32_t r) {
+    const float y = __builtin_ldexpf(x, -e);
+    const uint32_t normal = ((__float_as_uint(y) + (r << 4)) >> 20) - uint32_t((128 - FIELDS) << 3);
+    const uint32_t small = uint32_t(__builtin_ldexpf(y, FIELDS + 1) + __builtin_ldexpf(float(r), -16));
+    constexpr float least = 1.f / float(1u << (FIELDS - 2));   // of the codes with a hidden bit
+    return std::min(y >= least ? normal : small, uint32_t(FIELDS * 8 - 1));   // a float's own highest binade has none above
+  }
+  static __device__ __forceinline__ float decode(uint32_t code, int e) {
+    const int f = int(code >> 3);
+    const uint32_t man = f ? (code & 7) | 8 : code & 7;
+    return __builtin_ldexpf(float(man), (f ? f : 1) - FIELDS - 2 + e);
+  }
+};
+typedef Codes<16> CodesM;
+typedef Codes<32> CodesV;
+constexpr uint32_t kNotANumber = 255;   // of a block's exponent: a NaN or an infinity is in it
+
+struct Factors {
+  float size;   // 1 / (1 - b1^t)
+  float root;   // (1 - b2^t)^(-1/2)
+  uint32_t key;
+};
+
+// 4 elements of a lane from its place in a tensor of n elements; 0 behind the end.
+template <class T, bool FULL, bool ONCE>
+__device__ __forceinline__ void load4(const T* base, int64_t i, int64_t n, float (&x)[4]) {
+  Pack<T, 4> p;
+  if constexpr (FULL && ONCE) p = load_stream(reinterpret_cast<const Pack<T, 4>*>(base + i));
+  else if constexpr (FULL) p = *reinterpret_cast<const Pack<T, 4>*>(base + i);
+  else p = load_pack<T, 4>(base, i, n);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = to_f32(p.v[k]);
+}
+template <class T, bool FULL, bool ONCE>
+__device__ __forceinline__ void store4(T* base, int64_t i, int64_t n, const float (&x)[4]) {
+  Pack<T, 4> p;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p.v[k] = from_f32<T>(x[k]);
+  if constexpr (FULL && ONCE) store_stream(reinterpret_cast<Pack<T, 4>*>(base + i), p);
+  else if constexpr (FULL) *reinterpret_cast<Pack<T, 4>*>(base + i) = p;
+  else store_pack<T, 4>(base, i, n, p);
+}
+
+// Block `at` (of 256 elements) of a tensor's moments.
+template <int BITS>
+struct Moments;
+
+template <>
+struct Moments<32> {
+  static constexpr int64_t kBytes = 2 * kMomentBlock * 4;
+  float m[4], v[4];
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const unsigned char* s, int lane) {
+    const float* f = reinterpret_cast<const float*>(s);
+    load4<float, true, ONCE>(f, lane * 4, 0, m);
+    load4<float, true, ONCE>(f + kMomentBlock, lane * 4, 0, v);
+  }
+  __device__ __forceinline__ void open() {}
+  template <bool ONCE>
+  __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t, int64_t) const {
+    float* f = reinterpret_cast<float*>(s);
+    store4<float, true, ONCE>(f, lane * 4, 0, m);
+    store4<float, true, ONCE>(f + kMomentBlock, lane * 4, 0, v);
+  }
+};
+
+template <>
+struct Moments<8> {
+  static constexpr int64_t kBytes = 2 * kMomentBlock + 16;
+  uint32_t cm, cv, e;
+  float m[4], v[4];
+  template <bool ONCE>
+  __device__ __forceinline__ void load(const unsigned char* s, int lane) {
+    cm = reinterpret_cast<const uint32_t*>(s)[lane];
+    cv = reinterpret_cast<const uint32_t*>(s + kMomentBlock)[lane];
+    e = *reinterpret_cast<const uint32_t*>(s + 2 * kMomentBlock);
+  }
+  __device__ __forceinline__ void open() {
+    const uint32_t bm = e & 255, bv = e >> 8 & 255;
+    const int em = int(bm) - 100, ev = int(bv) - 100;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t c = cm >> 8 * k & 255;
+      const float x = CodesM::decode(c & 127, em);
+      m[k] = bm == kNotANumber ? NAN : c & 128 ? -x : x;
+      v[k] = bv == kNotANumber ? NAN : CodesV::decode(cv >> 8 * k & 255, ev);
+    }
+  }
+  template <bool ONCE>
+  __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t key, int64_t i) const {
+    float tm = 0.f, tv = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      tm = Highest()(tm, fabsf(m[k]));
+      tv = Highest()(tv, fabsf(v[k]));
+    }
+    tm = lanes_reduce<64>(tm, Highest());
+    tv = lanes_reduce<64>(tv, Highest());
+    const bool bm = !(tm < INFINITY), bv = !(tv < INFINITY);
+    const int em = bm ? 0 : CodesM::exponent(tm), ev = bv ? 0 : CodesV::exponent(tv);
+    uint32_t pm = 0, pv = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t at = uint64_t(i + k);
+      const uint32_t r = mix(key + uint32_t(at) + 0x9E3779B9u * uint32_t(at >> 32));
+      const uint32_t a = CodesM::encode(fabsf(m[k]), em, r & 0xFFFF);
+      uint32_t b = CodesV::encode(v[k], ev, r >> 16);
+      b = v[k] > 0.f && b == 0 ? 1 : b;
+      pm |= (a | (m[k] < 0.f && a ? 128u : 0u)) << 8 * k;
+      pv |= b << 8 * k;
+    }
+    reinterpret_cast<uint32_t*>(s)[lane] = bm ? 0u : pm;
+    reinterpret_cast<uint32_t*>(s + kMomentBlock)[lane] = bv ? 0u : pv;
+    if (lane == 0)
+      *reinterpret_cast<uint32_t*>(s + 2 * kMomentBlock) = (bm ? kNotANumber : uint32_t(em + 100)) | (bv ? kNotANumber : uint32_t(ev + 100)) << 8;
+  }
+};
+
+template <class P, class G, int BITS, bool FULL, bool ONCE>
+__device__ __forceinline__ void chunk_step(const AdamwLaunch& a, const AdamwEntry& t, int64_t start, const Factors& f, uint32_t key, int lane) {
+  P* p = static_cast<P*>(t.p);
+  const G* g = static_cast<const G*>(t.g);
+  unsigned char* s = static_cast<unsigned char*>(t.s) + start / kMomentBlock * Moments<BITS>::kBytes;
+  const float size = t.lr * f.size;
+  float xp[kBlocks][4], xg[kBlocks][4];
+  Moments<BITS> mo[kBlocks];
+  const int64_t i0 = start + lane * 4;
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+    if (FULL || start + b * kMomentBlock < t.n) {
+      load4<P, FULL, ONCE>(p, i0 + b * kMomentBlock, t.n, xp[b]);
+      load4<G, FULL, ONCE>(g, i0 + b * kMomentBlock, t.n, xg[b]);
+      mo[b].template load<ONCE>(s + b * Moments<BITS>::kBytes, lane);
+    }
+#pragma unroll
+  for (int b = 0; b < kBlocks; ++b)
+    if (FULL || start + b * kMomentBlock < t.n) {
+      mo[b].open();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float &m = mo[b].m[k], &v = mo[b].v[k];
+        m = weighted(m, a.b1, xg[b][k], a.c1);
+        v = weighted(v, a.b2, square(xg[b][k]), a.c2);
+        xp[b][k] = xp[b][k] * t.decay - size * m / (sqrtf(v) * f.root + a.eps);
+      }
+      store4<P, FULL, ONCE>(p, i0 + b * kMomentBlock, t.n, xp[b]);
+      mo[b].template store<ONCE>(s + b * Moments<BITS>::kBytes, lane, key, i0 + b * kMomentBlock);
+    }
+}
+
+template <class P, class G, int BITS, bool ONCE>
+__global__ __launch_bounds__(256) void k_adamw(AdamwLaunch a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = int64_t(__hip_atomic_load(a.step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) + 1;
+  Factors f;
+  // 1 - b^t = -expm1(t log b), in 64 bits: b near 1 leaves little of it
+  f.size = float(1.0 / -expm1(double(t) * a.log_b1));
+  f.root = float(1.0 / sqrt(-expm1(double(t) * a.log_b2)));
+  f.key = mix(mix(uint32_t(t)) ^ a.seed);
+  const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6), waves = gridDim.x * 4;
+  for (uint32_t c = __builtin_amdgcn_readfirstlane(wave); c < a.first[a.count]; c += waves) {
+    int lo = 0, hi = a.count;   // the tensor with first[lo] <= c < first[lo + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.first[mid] <= c) lo = mid;
+      else hi = mid;
+    }
+    const AdamwEntry& e = a.e[lo];
+    const int64_t start = int64_t(c - a.first[lo]) * kChunk;
+    const uint32_t key = mix(f.key + a.place[lo]);
+    if (start + kChunk <= e.n) chunk_step<P, G, BITS, true, ONCE>(a, e, start, f, key, lane);
+    else chunk_step<P, G, BITS, false, ONCE>(a, e, start, f, key, lane);
+  }
+  if (a.advance) {
+    __syncthreads();   // the block's waves have read the counter
+    if (threadIdx.x == 0) {
+      unsigned long long* step = a.step;
+      const unsigned long long ticket = __hip_atomic_fetch_add(step + 1, 1ull, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      if (ticket == gridDim.x - 1) {
+        __hip_atomic_store(step + 1, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(step, (unsigned long long)t, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+  }
+}
+
+template <class T, int BITS>
+__global__ __launch_bounds__(256) void k_adamw_moments(const unsigned char* s, int64_t n, T* m, T* v) {
+  const int lane = threadIdx.x & 63;
+  const int64_t blocks = (n + kMomentBlock - 1) / kMomentBlock;
+  for (int64_t b = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); b < blocks; b += int64_t(gridDim.x) * 4) {
+    Moments<BITS> mo;
+    mo.template load<false>(s + b * Moments<BITS>::kBytes, lane);
+    mo.open();
+    if (m) store4<T, false, false>(m, b * kMomentBlock + lane * 4, n, mo.m);
+    if (v) store4<T, false, false>(v, b * kMomentBlock + lane * 4, n, mo.v);
+  }
+}
+
+template <class F>
+hipError_t with_type(int32_t dtype, F&& f) {
+  if (dtype == kF32) return f(float());
+  if (dtype == kBF16) return f(bf16());
+  return f(f16());
+}
+
+}  // namespace
+
+int64_t adamw_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
+
+hipError_t launch_adamw(const AdamwLaunch& a, int32_t pdtype, int32_t gdtype, int32_t bits, bool once, hipStream_t s) {
+  // four blocks of a compute unit hide its memory's latency; a small list gets a wave for every chunk
+  const int64_t need = (int64_t(a.first[a.count]) + 3) / 4;
+  const dim3 grid(unsigned(std::max<int64_t>(1, std::min<int64_t>(need, 2048))));
+  return with_type(pdtype, [&](auto p) {
+    return with_type(gdtype, [&](auto g) {
+      using P = decltype(p);
+      using G = decltype(g);
+      if (bits == 32) {
+        if (once) k_adamw<P, G, 32, true><<<grid, dim3(256), 0, s>>>(a);
+        else k_adamw<P, G, 32, false><<<grid, dim3(256), 0, s>>>(a);
+      } else {
+        if (once) k_adamw<P, G, 8, true><<<grid, dim3(256), 0, s>>>(a);
+        else k_adamw<P, G, 8, false><<<grid, dim3(256), 0, s>>>(a);
+      }
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_adamw_moments(const void* state, int64_t n, int32_t bits, int32_t dtype, void* m, void* v, hipStream_t s) {
+  const int64_t blocks = (n + kMomentBlock - 1) / kMomentBlock;
+  const dim3 grid(unsigned(std::min<int64_t>((blocks + 3) / 4, 8192)));
+  return with_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    const unsigned char* p = static_cast<const unsigned char*>(state);
+    if (bits == 32) k_adamw_moments<T, 32><<<grid, dim3(256), 0, s>>>(p, n, static_cast<T*>(m), static_cast<T*>(v));
+    else k_adamw_moments<T, 8><<<grid, dim3(256), 0, s>>>(p, n, static_cast<T*>(m), static_cast<T*>(v));
+    return hipGetLastError();
+  });
+}
+
+}  // namespace lopt

@@ -1,4 +1,4 @@
-// Launches of the gradient-producing operators, called by lopt_ops_api.cpp
+// Launches of the operators around the learned optimizer's step, called by lopt_ops_api.cpp
 // with validated arguments.  Not part of the public ABI.
 #pragma once
 
@@ -96,5 +96,33 @@ struct DistillBackward {
 
 hipError_t launch_distill_forward(const DistillForward& a, hipStream_t s);
 hipError_t launch_distill_backward(const DistillBackward& a, hipStream_t s);
+
+// ---- AdamW over a list of tensors (lopt_adamw.hip) ----
+constexpr int64_t kMomentBlock = 256;   // elements of a block of moments
+constexpr int kMaxAdamw = 80;           // tensors of one launch
+
+struct AdamwEntry {
+  void* p;
+  const void* g;
+  void* s;       // moments
+  int64_t n;
+  float lr;
+  float decay;   // 1 - lr wd
+};
+
+struct AdamwLaunch {
+  AdamwEntry e[kMaxAdamw];
+  uint32_t first[kMaxAdamw + 1];   // chunks of the tensors before each one, and of all
+  uint32_t place[kMaxAdamw];       // in the caller's list
+  int32_t count, advance;          // advance: the step counter goes on when this launch ends
+  float b1, c1, b2, c2, eps;       // c = 1 - b
+  uint32_t seed;
+  double log_b1, log_b2;
+  unsigned long long* step;        // t, and a ticket that is 0 between launches
+};
+
+int64_t adamw_chunks(int64_t n);
+hipError_t launch_adamw(const AdamwLaunch& a, int32_t pdtype, int32_t gdtype, int32_t bits, bool once, hipStream_t s);
+hipError_t launch_adamw_moments(const void* state, int64_t n, int32_t bits, int32_t dtype, void* m, void* v, hipStream_t s);
 
 }  // namespace lopt

@@ -1,10 +1,13 @@
-// C ABI of the operators that produce a step's gradients (norms, embedding,
-// distillation loss): validation, then the launches of lopt_ops.h.  Nothing is
+// C ABI of the operators around the learned optimizer's step (norms, embedding,
+// distillation loss, AdamW): validation, then the launches of lopt_ops.h.  Nothing is
 // allocated and nothing waits; the calls may be captured into a graph.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <string>
+#include <tuple>
+#include <vector>
 
 #include "../../include/lopt.h"
 #include "lopt_error.h"
@@ -98,6 +101,20 @@ void check_embedding(int64_t n_ids, int64_t rows, int64_t cols, int64_t row0) {
   if (n_ids < 0) fail(LOPT_ERR_INVALID_ARGUMENT, "negative number of ids");
   if (n_ids > kMaxIds) fail(LOPT_ERR_UNSUPPORTED, "more than 2^27 ids in one call");
   if (row0 < 0 || row0 > (int64_t(1) << 40)) fail(LOPT_ERR_INVALID_ARGUMENT, "row0 must lie in [0, 2^40]");
+}
+
+void check_state_bits(int32_t bits) {
+  if (bits != 8 && bits != 32) fail(LOPT_ERR_INVALID_ARGUMENT, "state_bits must be 8 or 32");
+}
+
+void check_moments(int64_t n, int32_t bits) {
+  check_state_bits(bits);
+  if (n < 1) fail(LOPT_ERR_INVALID_ARGUMENT, "a tensor needs at least one element");
+  if (n > (int64_t(1) << 38)) fail(LOPT_ERR_UNSUPPORTED, "a tensor of more than 2^38 elements");
+}
+
+size_t moment_bytes(int64_t n, int32_t bits) {
+  return size_t((n + kMomentBlock - 1) / kMomentBlock) * size_t(bits == 32 ? 8 * kMomentBlock : 2 * kMomentBlock + 16);
 }
 
 }  // namespace
@@ -289,6 +306,108 @@ lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, con
     a.top = top; a.dtype = dtype; a.udtype = u_dtype; a.id_bytes = id_bytes;
     a.tau = temperature; a.inv_tau = 1.f / temperature;
     hip_check(launch_distill_backward(a, static_cast<hipStream_t>(stream)), "distill backward");
+  });
+}
+
+lopt_status lopt_adamw_state_bytes(int64_t n, int32_t state_bits, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(LOPT_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    check_moments(n, state_bits);
+    *bytes = moment_bytes(n, state_bits);
+  });
+}
+
+lopt_status lopt_adamw_step(const lopt_adamw_tensor* ts, int32_t n, int32_t state_bits, double beta1, double beta2,
+                            double eps, uint32_t seed, int64_t* step, void* stream) {
+  return guarded([&] {
+    if (n < 0) fail(LOPT_ERR_INVALID_ARGUMENT, "negative number of tensors");
+    if (n && !ts) fail(LOPT_ERR_INVALID_ARGUMENT, "ts is NULL");
+    check_state_bits(state_bits);
+    for (const double b : {beta1, beta2})
+      if (!(b >= 0.0 && b < 1.0)) fail(LOPT_ERR_INVALID_ARGUMENT, "beta1 and beta2 must lie in [0, 1)");
+    if (!(eps >= 0.0) || !std::isfinite(float(eps))) fail(LOPT_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+    if (n == 0) return;
+    std::vector<Buffer> bufs;
+    bufs.reserve(3 * size_t(n) + 1);
+    const auto add = [&](const std::string& name, const void* p, int64_t bytes, uintptr_t align, bool written) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      if (!p) fail(LOPT_ERR_INVALID_ARGUMENT, name + " is NULL");
+      if (at % align) fail(LOPT_ERR_UNSUPPORTED, name + " is not aligned to " + std::to_string(align) + " bytes");
+      bufs.push_back({nullptr, at, at + uintptr_t(bytes), written});
+    };
+    add("step", step, 16, 8, true);
+    // launches of one pair of types, in the order of the list
+    std::vector<std::pair<std::pair<int32_t, int32_t>, std::vector<int32_t>>> groups;
+    int64_t bytes = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      const lopt_adamw_tensor& t = ts[i];
+      const auto name = [&](const char* what) { return std::string(what) + " of tensor " + std::to_string(i); };
+      check_moments(t.n, state_bits);
+      check_dtype(t.p_dtype, "param");
+      if (t.grad) check_dtype(t.g_dtype, "grad");
+      if (!std::isfinite(float(t.lr)) || !std::isfinite(float(t.lr * t.weight_decay)))
+        fail(LOPT_ERR_INVALID_ARGUMENT, name("lr or weight_decay") + " is not finite");
+      const int64_t p = elem_bytes(t.p_dtype), s = int64_t(moment_bytes(t.n, state_bits));
+      add(name("param"), t.param, t.n * p, uintptr_t(p), true);
+      add(name("state"), t.state, s, 16, true);
+      if (!t.grad) continue;
+      const int64_t g = elem_bytes(t.g_dtype);
+      add(name("grad"), t.grad, t.n * g, uintptr_t(g), false);
+      bytes += t.n * (p + g) + s;
+      const std::pair<int32_t, int32_t> types(t.p_dtype, t.g_dtype);
+      auto at = std::find_if(groups.begin(), groups.end(), [&](const auto& x) { return x.first == types; });
+      if (at == groups.end()) at = groups.insert(at, {types, {}});
+      at->second.push_back(i);
+    }
+    // by address: a buffer may begin before the last written one ends, or, if written, before any does
+    std::sort(bufs.begin(), bufs.end(), [](const Buffer& x, const Buffer& y) { return std::tie(x.a, x.b) < std::tie(y.a, y.b); });
+    uintptr_t any = 0, written = 0;
+    for (const Buffer& b : bufs) {
+      if (b.a < (b.written ? any : written)) fail(LOPT_ERR_INVALID_ARGUMENT, "params, states, gradients or step overlap");
+      any = std::max(any, b.b);
+      if (b.written) written = std::max(written, b.b);
+    }
+    AdamwLaunch a{};
+    a.b1 = float(beta1); a.c1 = float(1.0 - beta1); a.b2 = float(beta2); a.c2 = float(1.0 - beta2);
+    a.log_b1 = std::log(beta1); a.log_b2 = std::log(beta2);   // -inf of 0: no correction
+    a.eps = float(eps); a.seed = seed; a.step = reinterpret_cast<unsigned long long*>(step);
+    const bool once = bytes > 200'000'000;   // what the memory-side cache does not hold until the next step
+    if (groups.empty()) groups.push_back({{LOPT_F32, LOPT_F32}, {}});   // only the count
+    for (size_t k = 0; k < groups.size(); ++k) {
+      const auto& [types, list] = groups[k];
+      size_t next = 0;
+      do {
+        a.count = 0;
+        a.first[0] = 0;
+        while (next < list.size() && a.count < kMaxAdamw) {
+          const lopt_adamw_tensor& t = ts[list[next]];
+          const int64_t chunks = adamw_chunks(t.n);
+          if (a.count && a.first[a.count] + chunks > (int64_t(1) << 31)) break;
+          a.e[a.count] = {t.param, t.grad, t.state, t.n, float(t.lr), float(1.0 - t.lr * t.weight_decay)};
+          a.place[a.count] = uint32_t(list[next]);
+          a.first[a.count + 1] = a.first[a.count] + uint32_t(chunks);
+          ++a.count;
+          ++next;
+        }
+        a.advance = next == list.size() && k + 1 == groups.size();
+        hip_check(launch_adamw(a, types.first, types.second, state_bits, once, static_cast<hipStream_t>(stream)), "adamw");
+      } while (next < list.size());
+    }
+  });
+}
+
+lopt_status lopt_adamw_moments(const void* state, int64_t n, int32_t state_bits, int32_t dtype, void* m, void* v,
+                               void* stream) {
+  return guarded([&] {
+    check_moments(n, state_bits);
+    check_dtype(dtype, "m");
+    Buffers bufs;
+    bufs.add("state", state, int64_t(moment_bytes(n, state_bits)), 16, false);
+    if (m) bufs.add("m", m, n * elem_bytes(dtype), elem_bytes(dtype), true);
+    if (v) bufs.add("v", v, n * elem_bytes(dtype), elem_bytes(dtype), true);
+    bufs.no_overlap();
+    if (!m && !v) return;
+    hip_check(launch_adamw_moments(state, n, state_bits, dtype, m, v, static_cast<hipStream_t>(stream)), "adamw moments");
   });
 }
 

@@ -1,12 +1,13 @@
-"""Norms, embedding and distillation loss over liblopt, for PyTorch tensors.
+"""The operators around the optimizers' steps over liblopt, for PyTorch tensors.
 
-They produce the gradients that ``lopt.LearnedOptimizer`` steps with:
+They produce the gradients that ``lopt.LearnedOptimizer`` and ``lopt.AdamW`` step with:
 
 * ``layer_norm``, ``rms_norm``  a transformer's norms
 * ``embedding``                 a token lookup with scaling, its gradient by sorted tokens
 * ``distill_loss``              a loss from a teacher's top logits, where a backward pass begins
 
-These are differentiable (``torch.autograd``; gradients of gradients are not
+and ``adamw_step`` is the step of ``lopt.AdamW`` on lists of tensors.  All but it
+are differentiable (``torch.autograd``; gradients of gradients are not
 supported).  The ``*_forward`` and ``*_backward`` functions below them make
 one call of the library each (include/lopt.h has the formulas); they take
 buffers for the parameters' gradients and can add to what is there, so a
@@ -123,3 +124,28 @@ def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temper
     grad_loss: one float32 value a row.  out: a contiguous buffer like logits;
     it may be logits itself, which the gradient then replaces."""
     return _C.distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temperature, out)
+
+
+# ---------------------------------------------------------------------------
+# AdamW over a list of tensors
+
+def adamw_state(param, state_bits: int = 32):
+    """Zero moments for a parameter: a flat buffer for ``adamw_step`` (layout of include/lopt.h), float32 or, with 8 bits,
+    uint8."""
+    return _C.adamw_state(param, state_bits)
+
+
+def adamw_step(params, grads, states, step, *, lr, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=1e-2,
+               state_bits: int = 32, seed: int = 0):
+    """One AdamW step over a list of contiguous tensors, in place; ``lopt.AdamW`` is the optimizer over it.
+
+    grads: one a parameter, of any of the types, or None (the parameter is skipped).  states: from ``adamw_state``, zero
+    before the first step.  step: int64 tensor of two elements, [steps taken, 0]; the call advances the first and keeps
+    the second.  lr, weight_decay: numbers, or one a parameter."""
+    per = lambda x: [float(x)] if isinstance(x, (int, float)) else [float(v) for v in x]  # noqa: E731
+    _C.adamw_step(params, grads, states, step, per(lr), betas[0], betas[1], eps, per(weight_decay), state_bits, seed)
+
+
+def adamw_moments(state, n: int, *, state_bits: int = 32, dtype: torch.dtype = torch.float32):
+    """(m, v) of the first n elements of a buffer of moments, as vectors of dtype (8-bit moments are exact in bfloat16)."""
+    return _C.adamw_moments(state, n, state_bits, dtype)

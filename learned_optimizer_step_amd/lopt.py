@@ -40,7 +40,7 @@ LOPT_LAUNCH_SINGLE = 2   # one kernel per step (the five passes behind grid-wide
 LOPT_MAX_TIME = 11
 LOPT_N_FEATURES = 28     # small_fc_lopt's per-element features
 LOPT_VELO_FEATURES = 19  # the VeLO-shaped variant's (features 0..18)
-LOPT_F32 = 0             # element types of the norm, embedding and distillation calls
+LOPT_F32 = 0             # element types of the operators' calls
 LOPT_BF16 = 1
 LOPT_F16 = 2
 LOPT_NORM_LAYER = 0
@@ -69,6 +69,12 @@ class lopt_tensor(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class lopt_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("state", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("lr", ctypes.c_double), ("weight_decay", ctypes.c_double), ("p_dtype", ctypes.c_int32),
+                ("g_dtype", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -87,6 +93,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib = ctypes.CDLL(p)
     st = ctypes.c_int
     i32, i64, f32, ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+    f64, u32, size = ctypes.c_double, ctypes.c_uint32, ctypes.POINTER(ctypes.c_size_t)
     sig = {
         "lopt_default_config": (st, [ctypes.POINTER(lopt_config)]),
         "lopt_mlp_floats": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -126,6 +133,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "lopt_distill_forward": (st, [i64, i64, i32, ptr, i64, i32, ptr, i64, i32, ptr, i64, i32, f32, ptr, ptr, ptr]),
         "lopt_distill_backward": (st, [i64, i64, i32, ptr, i64, ptr, i64, i32, ptr, i64, i32, ptr, i64, i32, f32, ptr,
                                        ptr, i64, ptr]),
+        "lopt_adamw_state_bytes": (st, [i64, i32, size]),
+        "lopt_adamw_step": (st, [ctypes.POINTER(lopt_adamw_tensor), i32, i32, f64, f64, f64, u32, ptr, ptr]),
+        "lopt_adamw_moments": (st, [ptr, i64, i32, i32, ptr, ptr, ptr]),
         "lopt_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -302,7 +312,7 @@ def lopt_set_timing_events(h, events: Sequence[int]) -> None:
     _check(load_library().lopt_set_timing_events(h, arr, len(events)))
 
 
-# The norm, embedding and distillation calls take the arguments of
+# The operators' calls take the arguments of
 # include/lopt.h in their order, with device addresses as integers (None: NULL).
 # learned_optimizer_step_amd.layers makes them from torch tensors.
 
@@ -340,6 +350,22 @@ def lopt_distill_forward(*args) -> None:
 
 def lopt_distill_backward(*args) -> None:
     _check((_lib or load_library()).lopt_distill_backward(*args))
+
+
+def lopt_adamw_state_bytes(n: int, state_bits: int) -> int:
+    out = ctypes.c_size_t()
+    _check((_lib or load_library()).lopt_adamw_state_bytes(n, state_bits, ctypes.byref(out)))
+    return out.value
+
+
+def lopt_adamw_step(ts: Sequence[lopt_adamw_tensor], state_bits: int, beta1: float, beta2: float, eps: float, seed: int,
+                    step: Optional[int], stream: Optional[int]) -> None:
+    arr = (lopt_adamw_tensor * max(1, len(ts)))(*ts)
+    _check((_lib or load_library()).lopt_adamw_step(arr, len(ts), state_bits, beta1, beta2, eps, seed, step, stream))
+
+
+def lopt_adamw_moments(*args) -> None:
+    _check((_lib or load_library()).lopt_adamw_moments(*args))
 
 
 def config_from(**overrides) -> lopt_config:
@@ -617,3 +643,82 @@ class LearnedOptimizer(_torch_optimizer_base()):
         for dst, src in zip(self.lopt.states, lo["states"]):
             dst.copy_(src.to(device=dst.device, dtype=dst.dtype))
         self.lopt.t = int(lo["t"])
+
+
+class AdamW(_torch_optimizer_base()):
+    """AdamW as a ``torch.optim.Optimizer`` over device parameters (fp32, bf16 or fp16), moments in 32 bits or in 8.
+
+    Each ``step()`` is one ``lopt_adamw_step`` over every parameter, with the gradients in ``p.grad``; a parameter whose
+    ``grad`` is None is skipped, and the count of steps, which all parameters share, goes on.  ``lr`` and
+    ``weight_decay`` are read from the parameter groups at every step, so ``torch.optim.lr_scheduler`` schedules drive
+    them; ``betas`` and ``eps`` are the whole optimizer's.  With ``state_bits=8`` the moments take 2.06 bytes an element
+    instead of 8; their codes are rounded at random, from ``seed``.  The count is on the device, so a step can be
+    captured into a HIP graph (with the gradients of that moment and its learning rates) and counts as it is replayed.
+    The moments live in ``self.states`` (layout of ``include/lopt.h``); ``moments(i)`` gives them as numbers.
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2, *,
+                 state_bits: int = 32, seed: int = 0):
+        import torch
+        from . import layers    # the compiled calls, over this module's library
+        self.states = None
+        self._layers = layers
+        self.betas, self.eps, self.state_bits, self.seed = (float(betas[0]), float(betas[1])), float(eps), int(state_bits), int(seed)
+        super().__init__(params, dict(lr=lr, weight_decay=weight_decay))
+        for g in self.param_groups:
+            if "betas" in g or "eps" in g:
+                raise ValueError("betas and eps are the whole optimizer's: a parameter group cannot have its own")
+        self.params = [p for g in self.param_groups for p in g["params"]]
+        dev = self.params[0].device
+        for p in self.params:
+            if not p.is_cuda or p.device != dev or not p.is_contiguous():
+                raise ValueError("parameters must be contiguous tensors on one GPU")
+        self.states = [layers.adamw_state(p, state_bits) for p in self.params]
+        self.step_count = torch.zeros(2, dtype=torch.int64, device=dev)
+
+    def add_param_group(self, param_group):
+        if self.states is not None:
+            raise ValueError("parameters cannot be added to an AdamW that has been made: its parameters share one count of steps")
+        super().add_param_group(param_group)
+
+    def step(self, closure=None):
+        import torch
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        hyper = [(float(g["lr"]), float(g["weight_decay"])) for g in self.param_groups for _ in g["params"]]
+        self._layers.adamw_step(self.params, [p.grad for p in self.params], self.states, self.step_count,
+                                lr=[a for a, _ in hyper], betas=self.betas, eps=self.eps,
+                                weight_decay=[b for _, b in hyper], state_bits=self.state_bits, seed=self.seed)
+        return loss
+
+    @property
+    def t(self) -> int:
+        """Steps taken (waits for the device)."""
+        return int(self.step_count[0])
+
+    def moments(self, i: int):
+        """(m, v) of parameter i, float32 and of its shape."""
+        p = self.params[i]
+        return tuple(x.view(p.shape) for x in self._layers.adamw_moments(self.states[i], p.numel(), state_bits=self.state_bits))
+
+    def state_dict(self):
+        """torch's optimizer state (parameter groups) plus the moments' buffers, the count of steps and the seed."""
+        sd = super().state_dict()
+        sd["adamw"] = {"t": self.t, "state_bits": self.state_bits, "seed": self.seed, "betas": self.betas, "eps": self.eps,
+                       "states": [s.clone() for s in self.states]}
+        return sd
+
+    def load_state_dict(self, state_dict):
+        sd = dict(state_dict)
+        st = sd.pop("adamw", None)
+        if st is None:
+            raise ValueError("the state dict holds no AdamW state")
+        if int(st["state_bits"]) != self.state_bits or [s.numel() for s in st["states"]] != [s.numel() for s in self.states]:
+            raise ValueError("the state dict belongs to another parameter list or another width of moments")
+        super().load_state_dict(sd)
+        for dst, src in zip(self.states, st["states"]):
+            dst.copy_(src)
+        self.step_count[0], self.seed = int(st["t"]), int(st["seed"])
+        self.betas, self.eps = (float(st["betas"][0]), float(st["betas"][1])), float(st["eps"])
