@@ -482,6 +482,43 @@ lopt_status lopt_norm_backward(int32_t kind, int64_t rows, int64_t cols, int32_t
                                const float* rstd, void* dx, int64_t lddx, void* dweight, void* dbias, int32_t g_dtype,
                                int32_t accumulate, void* workspace, size_t ws_bytes, void* stream);
 
+typedef enum lopt_gate_kind { LOPT_GATE_NONE = 0, LOPT_GATE_VECTOR = 1, LOPT_GATE_MATRIX = 2 } lopt_gate_kind;
+
+/* The residual update between two blocks, with the norms on both sides of it, for
+ * every row of x (the residual stream) and y (a block's output), rows x cols of type dtype:
+ *   u = norm1(y) if post, else y;   h = alpha x + beta gate u;   z = norm2(h) if pre.
+ * norm1 has post_weight and post_bias, norm2 weight and bias (lopt_norm_forward's formula, of one
+ * kind and eps); at least one of post and pre is not 0.  gate: none (1), a vector of cols
+ * elements, or a matrix rows x cols of type dtype and row stride ldg.  h is rounded to its type, and z is the
+ * norm of the rounded h.  Vectors have type w_dtype; NULL: weights of 1, biases of 0.  An RMS norm has no bias.
+ * z: NULL without pre.  stats: 4 rows floats (mean and rstd of y, then of h, rows of each; an RMS norm leaves the
+ * means, a missing norm both, as they were) that lopt_residual_norm_backward takes; NULL: not kept. */
+lopt_status lopt_residual_norm_forward(int32_t kind, int32_t post, int32_t pre, int64_t rows, int64_t cols, int32_t dtype,
+                                       const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t gate_kind,
+                                       const void* gate, int64_t ldg, const void* post_weight, const void* post_bias,
+                                       const void* weight, const void* bias, int32_t w_dtype, float alpha, float beta,
+                                       float eps, void* h, int64_t ldh, void* z, int64_t ldz, float* stats, void* stream);
+
+/* Bytes of workspace that lopt_residual_norm_backward needs for gradients of vectors.  Host only. */
+lopt_status lopt_residual_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradients of lopt_residual_norm_forward from those of h and z (type dtype; NULL: 0).  With hh and yh the normalised h and y:
+ *   D = dh + norm2's gradient of dz,  dx = alpha D,  E = beta D,  dgate = E u,
+ *   dy = norm1's gradient of E gate (or E gate),
+ *   dweight = sum dz hh, dbias = sum dz, dpost_weight = sum E gate yh, dpost_bias = sum E gate  (over rows),
+ * and a gate vector's dgate is summed over the rows too.  y, h, stats and the parameters as in the forward call (h is not
+ * needed without pre, post_bias only for dgate); x is not needed.  dx, dy and a gate matrix's dgate (row stride lddg) have type
+ * dtype, the vectors' gradients type g_dtype (added to what is there if accumulate is not 0); any may be NULL: it is
+ * not computed.  workspace: as for lopt_norm_backward; not needed without gradients of vectors. */
+lopt_status lopt_residual_norm_backward(int32_t kind, int32_t post, int32_t pre, int64_t rows, int64_t cols, int32_t dtype,
+                                        const void* dh, int64_t lddh, const void* dz, int64_t lddz, const void* y, int64_t ldy,
+                                        const void* h, int64_t ldh, const float* stats, int32_t gate_kind, const void* gate,
+                                        int64_t ldg, const void* post_weight, const void* post_bias, const void* weight,
+                                        int32_t w_dtype, float alpha, float beta, void* dx, int64_t lddx, void* dy,
+                                        int64_t lddy, void* dgate, int64_t lddg, void* dpost_weight, void* dpost_bias,
+                                        void* dweight, void* dbias, int32_t g_dtype, int32_t accumulate, void* workspace,
+                                        size_t ws_bytes, void* stream);
+
 /* Embedding lookup: out[t] = scale * table[ids[t] - row0] for n_ids ids.
  * table: rows x cols of type t_dtype, the rows [row0, row0 + rows) of the whole
  * table (row0 = 0: all of it; a rank's rows of a sharded one otherwise, whose

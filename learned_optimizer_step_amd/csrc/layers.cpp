@@ -40,6 +40,9 @@ struct Library {
   decltype(&lopt_norm_forward) norm_forward;
   decltype(&lopt_norm_backward_workspace) norm_backward_workspace;
   decltype(&lopt_norm_backward) norm_backward;
+  decltype(&lopt_residual_norm_forward) residual_norm_forward;
+  decltype(&lopt_residual_norm_backward_workspace) residual_norm_backward_workspace;
+  decltype(&lopt_residual_norm_backward) residual_norm_backward;
   decltype(&lopt_embedding_forward) embedding_forward;
   decltype(&lopt_embedding_backward_workspace) embedding_backward_workspace;
   decltype(&lopt_embedding_backward) embedding_backward;
@@ -61,6 +64,9 @@ void bind(uintptr_t handle) {
   find(l.norm_forward, "lopt_norm_forward");
   find(l.norm_backward_workspace, "lopt_norm_backward_workspace");
   find(l.norm_backward, "lopt_norm_backward");
+  find(l.residual_norm_forward, "lopt_residual_norm_forward");
+  find(l.residual_norm_backward_workspace, "lopt_residual_norm_backward_workspace");
+  find(l.residual_norm_backward, "lopt_residual_norm_backward");
   find(l.embedding_forward, "lopt_embedding_forward");
   find(l.embedding_backward_workspace, "lopt_embedding_backward_workspace");
   find(l.embedding_backward, "lopt_embedding_backward");
@@ -254,6 +260,192 @@ class Norm : public Function<Norm> {
                                 !some ? nullptr : rms ? at : at + stats.size(1), rms, std::nullopt, std::nullopt, false,
                                 ctx->needs_input_grad(0), nw, nb, type);
     return differentiable_once({g.dx, g.dw, g.db, Tensor(), Tensor()});
+  }
+};
+
+// ---------------------------------------------------------------------------
+// the residual update with its norms
+
+struct Residual {
+  float alpha, beta;
+  bool rms, post, pre;
+};
+
+// The vectors and the gate of a call, checked against rows of x's kind.
+struct ResidualParams {
+  Tensor w1, b1, w2, b2, row_gate;   // row_gate: a vector, the same for every row
+  std::optional<Matrix> own_gate;    // a gate like y
+  at::ScalarType type = at::kFloat;
+  int32_t gate_kind() const { return own_gate ? LOPT_GATE_MATRIX : row_gate.defined() ? LOPT_GATE_VECTOR : LOPT_GATE_NONE; }
+  const void* gate() const { return own_gate ? own_gate->data() : ptr(row_gate); }
+  int64_t ldg() const { return own_gate ? own_gate->ld : 0; }
+
+  ResidualParams(const Tensor& y, int64_t cols, const Residual& o, const Maybe& gate, const Maybe& post_weight, const Maybe& post_bias,
+                 const Maybe& weight, const Maybe& bias) {
+    const c10::Device device = y.device();
+    w1 = vector(post_weight, cols, device, "post_weight");
+    b1 = vector(post_bias, cols, device, "post_bias");
+    w2 = vector(weight, cols, device, "weight");
+    b2 = vector(bias, cols, device, "bias");
+    if (!o.post && (w1.defined() || b1.defined())) bad("post_weight and post_bias are of the norm of y, which post=False leaves out");
+    if (!o.pre && (w2.defined() || b2.defined())) bad("weight and bias are of the norm of h, which pre=False leaves out");
+    if (!o.post && !o.pre) bad("neither norm: post and pre are False");
+    if (o.rms && (b1.defined() || b2.defined())) bad("an RMS norm has no bias");
+    if (gate && gate->defined()) {
+      if (gate->dim() == 1 && y.dim() != 1) {
+        row_gate = vector(gate, cols, device, "gate");
+      } else {
+        on(device, *gate, "gate");
+        if (gate->sizes() != y.sizes() || gate->scalar_type() != y.scalar_type()) bad("gate must be a vector of the last dimension, or have y's shape and type");
+        own_gate = matrix(*gate, "gate");
+      }
+    }
+    bool first = true;
+    for (const Tensor* t : {&w1, &b1, &w2, &b2, &row_gate}) {
+      if (!t->defined()) continue;
+      if (!first && t->scalar_type() != type) bad("the weights, the biases and a gate vector must have the same type");
+      type = t->scalar_type();
+      first = false;
+    }
+    dtype_code(type, "weight");
+  }
+};
+
+struct ResidualOut {
+  Tensor h, z, stats;
+};
+
+ResidualOut residual_forward(const Tensor& x, const Tensor& y, const Maybe& gate, const Maybe& post_weight, const Maybe& post_bias,
+                             const Maybe& weight, const Maybe& bias, double eps, const Residual& o) {
+  const c10::Device device = gpu(x, "x");
+  on(device, y, "y");
+  const int32_t code = dtype_code(x.scalar_type(), "x");
+  if (y.sizes() != x.sizes() || y.scalar_type() != x.scalar_type()) bad("y must have the shape and type of x");
+  const Matrix mx = matrix(x, "x"), my = matrix(y, "y");
+  const ResidualParams p(y, my.cols, o, gate, post_weight, post_bias, weight, bias);
+  const c10::DeviceGuard guard(device);
+  ResidualOut out;
+  out.h = empty(x.sizes(), x.scalar_type(), device);
+  if (o.pre) out.z = empty(x.sizes(), x.scalar_type(), device);
+  out.stats = empty({4, mx.rows}, at::kFloat, device);
+  check(lib.residual_norm_forward(o.rms ? LOPT_NORM_RMS : LOPT_NORM_LAYER, o.post, o.pre, mx.rows, mx.cols, code, mx.data(), mx.ld,
+                                  my.data(), my.ld, p.gate_kind(), p.gate(), p.ldg(), ptr(p.w1), ptr(p.b1), ptr(p.w2), ptr(p.b2),
+                                  dtype_code(p.type, "weight"), o.alpha, o.beta, float(eps), out.h.data_ptr(), mx.cols, ptr(out.z),
+                                  mx.cols, static_cast<float*>(out.stats.data_ptr()), stream(device)));
+  return out;
+}
+
+struct ResidualNeeds {
+  bool x, y, gate, w1, b1, w2, b2;
+};
+struct ResidualBuffers {
+  Maybe gate, w1, b1, w2, b2;
+};
+struct ResidualGrads {
+  Tensor dx, dy, dgate, w1, b1, w2, b2;
+};
+
+ResidualGrads residual_backward(const Tensor& dh, const Tensor& dz, const Tensor& y, const Tensor& h, const Tensor& stats, const Maybe& gate,
+                                const Maybe& post_weight, const Maybe& post_bias, const Maybe& weight, const Residual& o,
+                                const ResidualNeeds& need, const ResidualBuffers& to, bool accumulate, std::optional<at::ScalarType> grad_dtype) {
+  const c10::Device device = gpu(y, "y");
+  const int32_t code = dtype_code(y.scalar_type(), "y");
+  const auto like = [&](const Tensor& t, const char* name) -> std::optional<Matrix> {
+    if (!t.defined()) return std::nullopt;
+    on(device, t, name);
+    if (t.sizes() != y.sizes() || t.scalar_type() != y.scalar_type()) bad(std::string(name) + " must have the shape and type of y");
+    return matrix(t, name);
+  };
+  const Matrix my = matrix(y, "y");
+  const auto mdh = like(dh, "grad_h"), mdz = like(dz, "grad_z"), mh = like(h, "h");
+  if (o.pre && !mh) bad("h is missing");
+  if (!o.pre && mdz) bad("grad_z is of the norm of h, which pre=False leaves out");
+  on(device, stats, "stats");
+  if (stats.scalar_type() != at::kFloat || !stats.is_contiguous() || stats.sizes() != at::IntArrayRef({4, my.rows}))
+    bad("stats must be the forward call's");
+  const ResidualParams p(y, my.cols, o, gate, post_weight, post_bias, weight, std::nullopt);
+  const c10::DeviceGuard guard(device);
+  ResidualGrads g;
+  at::ScalarType make = grad_dtype.value_or(p.type), made = at::kFloat;
+  bool first = true;
+  const auto sum = [&](bool wanted, const Maybe& buffer, const char* name) {
+    if (!wanted) return Tensor();
+    if (accumulate && !buffer) bad("accumulate needs the buffers to add to");
+    Tensor t = output(buffer, {my.cols}, device, first ? make : made, name);
+    if (!first && t.scalar_type() != made) bad("the vectors' gradients must have the same type");
+    made = t.scalar_type();
+    first = false;
+    return t;
+  };
+  // a given buffer's type is that of the others
+  for (const Maybe* b : {&to.gate, &to.w1, &to.b1, &to.w2, &to.b2})
+    if (*b && !grad_dtype) make = (*b)->scalar_type();
+  g.w1 = sum(o.post && need.w1, to.w1, "grad_post_weight");
+  g.b1 = sum(o.post && !o.rms && need.b1, to.b1, "grad_post_bias");
+  g.w2 = sum(o.pre && need.w2, to.w2, "grad_weight");
+  g.b2 = sum(o.pre && !o.rms && need.b2, to.b2, "grad_bias");
+  if (p.own_gate) {
+    if (to.gate) bad("grad_gate is for a gate vector");
+    if (need.gate) g.dgate = empty(y.sizes(), y.scalar_type(), device);
+  } else {
+    g.dgate = sum(p.row_gate.defined() && need.gate, to.gate, "grad_gate");
+  }
+  if (need.x) g.dx = empty(y.sizes(), y.scalar_type(), device);
+  if (need.y) g.dy = empty(y.sizes(), y.scalar_type(), device);
+  Tensor ws;
+  size_t bytes = 0;
+  if (!first) {
+    check(lib.residual_norm_backward_workspace(my.rows, my.cols, &bytes));
+    ws = empty({int64_t(bytes)}, at::kByte, device);
+  }
+  const auto data = [](const std::optional<Matrix>& m) { return m ? m->data() : nullptr; };
+  const auto ld = [](const std::optional<Matrix>& m) { return m ? m->ld : 0; };
+  check(lib.residual_norm_backward(o.rms ? LOPT_NORM_RMS : LOPT_NORM_LAYER, o.post, o.pre, my.rows, my.cols, code, data(mdh), ld(mdh),
+                                   data(mdz), ld(mdz), my.data(), my.ld, o.pre ? data(mh) : nullptr, ld(mh),
+                                   static_cast<const float*>(stats.data_ptr()), p.gate_kind(), p.gate(), p.ldg(), ptr(p.w1), ptr(p.b1),
+                                   ptr(p.w2), dtype_code(p.type, "weight"), o.alpha, o.beta, ptr(g.dx), my.cols, ptr(g.dy), my.cols,
+                                   ptr(g.dgate), my.cols, ptr(g.w1), ptr(g.b1), ptr(g.w2), ptr(g.b2),
+                                   first ? LOPT_F32 : dtype_code(made, "a gradient"), accumulate, ptr(ws), bytes, stream(device)));
+  return g;
+}
+
+class ResidualNorm : public Function<ResidualNorm> {
+ public:
+  static variable_list forward(AutogradContext* ctx, const Tensor& x, const Tensor& y, const Maybe& gate, const Maybe& post_weight,
+                               const Maybe& post_bias, const Maybe& weight, const Maybe& bias, double eps, double alpha, double beta,
+                               bool rms, bool post, bool pre) {
+    const Residual o{float(alpha), float(beta), rms, post, pre};
+    ResidualOut out = residual_forward(x, y, gate, post_weight, post_bias, weight, bias, eps, o);
+    const auto some = [](const Maybe& t) { return t ? *t : Tensor(); };
+    ctx->set_materialize_grads(false);
+    ctx->save_for_backward({y, some(gate), some(post_weight), some(post_bias), some(weight), out.h, out.stats});
+    ctx->saved_data["flags"] = int64_t(rms) | int64_t(post) << 1 | int64_t(pre) << 2 | int64_t(bool(gate)) << 3 | int64_t(bool(post_weight)) << 4 |
+                               int64_t(bool(post_bias)) << 5 | int64_t(bool(weight)) << 6 | int64_t(bool(bias)) << 7;
+    ctx->saved_data["alpha"] = alpha;
+    ctx->saved_data["beta"] = beta;
+    for (const Maybe* v : {&post_weight, &post_bias, &weight, &bias})   // the gradients' type: that of the vectors
+      if (*v) ctx->saved_data["type"] = (*v)->scalar_type();
+    if (!pre) return {out.h};
+    return {out.h, out.z};
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list s = ctx->get_saved_variables();
+    const int64_t flags = ctx->saved_data["flags"].toInt();
+    const auto flag = [&](int k) { return (flags >> k & 1) != 0; };
+    const Residual o{float(ctx->saved_data["alpha"].toDouble()), float(ctx->saved_data["beta"].toDouble()), flag(0), flag(1), flag(2)};
+    // edges are those of the tensors that there are
+    size_t edge = 2;
+    const auto needs = [&](int k) { return flag(k) && ctx->needs_input_grad(edge++); };
+    ResidualNeeds need{ctx->needs_input_grad(0), ctx->needs_input_grad(1), needs(3), needs(4), needs(5), needs(6), needs(7)};
+    const Tensor dh = grads[0], dz = o.pre ? grads[1] : Tensor();
+    ResidualGrads g;
+    if (dh.defined() || dz.defined()) {
+      const auto maybe = [](const Tensor& t) { return t.defined() ? Maybe(t) : Maybe(); };
+      std::optional<at::ScalarType> type;
+      if (ctx->saved_data.count("type")) type = ctx->saved_data["type"].toScalarType();
+      g = residual_backward(dh, dz, s[0], s[5], s[6], maybe(s[1]), maybe(s[2]), maybe(s[3]), maybe(s[4]), o, need, {}, false, type);
+    }
+    return differentiable_once({g.dx, g.dy, g.dgate, g.w1, g.b1, g.w2, g.b2, Tensor(), Tensor(), Tensor(), Tensor(), Tensor(), Tensor()});
   }
 };
 
@@ -506,6 +698,27 @@ PYBIND11_MODULE(_layers, m) {
     return std::make_tuple(maybe(g.dx), maybe(g.dw), maybe(g.db));
   });
   m.def("norm", [](const Tensor& x, const Maybe& w, const Maybe& b, double eps, bool rms) { return Norm::apply(x, w, b, eps, rms); });
+  m.def("residual_norm_forward", [](const Tensor& x, const Tensor& y, const Maybe& gate, const Maybe& w1, const Maybe& b1, const Maybe& w2,
+                                    const Maybe& b2, double eps, double alpha, double beta, bool rms, bool post, bool pre) {
+    const ResidualOut out = residual_forward(x, y, gate, w1, b1, w2, b2, eps, {float(alpha), float(beta), rms, post, pre});
+    return std::make_tuple(out.h, pre ? Maybe(out.z) : Maybe(), out.stats);
+  });
+  m.def("residual_norm_backward", [](const Maybe& dh, const Maybe& dz, const Tensor& y, const Maybe& h, const Tensor& stats, const Maybe& gate,
+                                     const Maybe& w1, const Maybe& b1, const Maybe& w2, double alpha, double beta, bool rms, bool post,
+                                     bool pre, bool need_x, bool need_y, bool need_params, const Maybe& ggate, const Maybe& gw1,
+                                     const Maybe& gb1, const Maybe& gw2, const Maybe& gb2, bool accumulate, const py::object& dtype) {
+    const auto some = [](const Maybe& t) { return t ? *t : Tensor(); };
+    const bool n = need_params;
+    const ResidualGrads g = residual_backward(some(dh), some(dz), y, some(h), stats, gate, w1, b1, w2, {float(alpha), float(beta), rms, post, pre},
+                                              {need_x, need_y, n, n, n, n, n}, {ggate, gw1, gb1, gw2, gb2}, accumulate, scalar_type(dtype));
+    const auto maybe = [](const Tensor& t) { return t.defined() ? Maybe(t) : Maybe(); };
+    return std::make_tuple(maybe(g.dx), maybe(g.dy), maybe(g.dgate), maybe(g.w1), maybe(g.b1), maybe(g.w2), maybe(g.b2));
+  });
+  m.def("residual_norm", [](const Tensor& x, const Tensor& y, const Maybe& gate, const Maybe& w1, const Maybe& b1, const Maybe& w2, const Maybe& b2,
+                            double eps, double alpha, double beta, bool rms, bool post, bool pre) {
+    const variable_list out = ResidualNorm::apply(x, y, gate, w1, b1, w2, b2, eps, alpha, beta, rms, post, pre);
+    return std::make_tuple(out[0], pre ? Maybe(out[1]) : Maybe());
+  });
   m.def("embedding_forward", [](const Tensor& ids, const Tensor& w, double scale, int64_t row0, const py::object& dtype) {
     return embedding_forward(ids, w, scale, row0, scalar_type(dtype));
   });

@@ -4,41 +4,10 @@
 // registers between the two sums and the output.
 #include <hip/hip_runtime.h>
 
-#include <cfloat>
-
 #include "lopt_norm.h"
 
 namespace lopt {
 namespace {
-
-// The mean comes from a sum in 64 bits: fp32's would be off by 2^-24 of the
-// values' size, which is much of the spread of a row far from zero, and much of
-// a mean that cancels (65536 x 200 fp32: 28 us, 25 with fp32 sums; bf16, whose
-// threads add in fp32 without roundings, within 2 %).  What fp32 cannot hold of it goes into the spread and
-// the output.
-struct Moments {
-  float mean, rest, rstd;   // mu = mean + rest
-};
-
-__device__ __forceinline__ Moments mean_of(double sum, int64_t n) {
-  Moments m;
-  const double mu = sum / double(n);
-  m.mean = float(mu);
-  m.rest = float(mu - double(m.mean));
-  m.rstd = 0.f;
-  return m;
-}
-
-// s2: the sum of (x - mean)^2; inv_n: the rounded 1 / n.  The product of the two is off by its rounding in every element
-// of every row (the mean square of 41 ones is not 1): what it leaves of s2 gives the quotient's last bit (131072 x 128
-// bf16 RMS: 27.1 us, 26.6 without it and 28.6 with a division).
-__device__ __forceinline__ void spread(Moments& m, float s2, float n, float inv_n, float eps) {
-  const float q = s2 * inv_n, mean2 = fmaf(fmaf(-q, n, s2), inv_n, q);
-  const float var = fmaxf(mean2 - m.rest * m.rest, 0.f);
-  m.rstd = 1.f / sqrtf(var + eps);
-  // fmaxf drops a NaN: a row that holds one has no norm; one whose squares add up to more than fp32 holds has rstd 0
-  if (!(s2 <= FLT_MAX)) m.rstd = s2 == INFINITY ? 0.f : s2;
-}
 
 template <class T, class L, int MODE>
 __global__ __launch_bounds__(L::BLOCK) void k_norm_forward(NormForward a) {

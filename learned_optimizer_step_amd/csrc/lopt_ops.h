@@ -97,6 +97,49 @@ struct DistillBackward {
 hipError_t launch_distill_forward(const DistillForward& a, hipStream_t s);
 hipError_t launch_distill_backward(const DistillBackward& a, hipStream_t s);
 
+// ---- residual update with its norms (lopt_residual_norm_forward.hip, lopt_residual_norm_backward.hip) ----
+enum : int32_t { kNoGate = 0, kGateVector = 1, kGateMatrix = 2 };
+
+struct ResidualForward {
+  const void* x;
+  const void* y;
+  const void* gate;   // vector: type wdtype; matrix: type dtype
+  const void* w1;     // of the norm of y; NULL: 1
+  const void* b1;     // NULL: 0
+  const void* w2;     // of the norm of h
+  const void* b2;
+  void* h;
+  void* z;            // NULL without the second norm
+  float* stats;       // [4][rows]: mean and rstd of y, mean and rstd of h; NULL: not written
+  int64_t rows, cols, ldx, ldy, ldg, ldh, ldz;
+  int32_t dtype, wdtype, gate_kind, rms, post, pre;
+  float alpha, beta, eps;
+};
+
+struct ResidualBackward {
+  const void* dh;     // NULL: 0
+  const void* dz;     // NULL: 0
+  const void* y;
+  const void* h;
+  const float* stats;
+  const void* gate;
+  const void* w1;
+  const void* b1;
+  const void* w2;
+  void* dx;           // NULL: not computed, as those below
+  void* dy;
+  void* dgate;
+  void* sums[5];      // gradients of w1, b1, w2, b2 and of a gate vector
+  float* part;        // workspace
+  int64_t rows, cols, lddh, lddz, ldy, ldh, ldg, lddx, lddy, lddg;
+  int32_t dtype, wdtype, gdtype, gate_kind, rms, post, pre, accumulate;
+  float alpha, beta;
+};
+
+size_t residual_backward_bytes(int64_t rows, int64_t cols);
+hipError_t launch_residual_forward(const ResidualForward& a, hipStream_t s);
+hipError_t launch_residual_backward(const ResidualBackward& a, hipStream_t s);
+
 // ---- AdamW over a list of tensors (lopt_adamw.hip) ----
 constexpr int64_t kMomentBlock = 256;   // elements of a block of moments
 constexpr int kMaxAdamw = 80;           // tensors of one launch

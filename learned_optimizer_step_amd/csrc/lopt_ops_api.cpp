@@ -41,7 +41,7 @@ struct Buffer {
 };
 
 struct Buffers {
-  static constexpr size_t kMost = 12;   // no call has more
+  static constexpr size_t kMost = 20;   // no call has more
   Buffer list[kMost];
   size_t count = 0;
 
@@ -101,6 +101,13 @@ void check_embedding(int64_t n_ids, int64_t rows, int64_t cols, int64_t row0) {
   if (n_ids < 0) fail(LOPT_ERR_INVALID_ARGUMENT, "negative number of ids");
   if (n_ids > kMaxIds) fail(LOPT_ERR_UNSUPPORTED, "more than 2^27 ids in one call");
   if (row0 < 0 || row0 > (int64_t(1) << 40)) fail(LOPT_ERR_INVALID_ARGUMENT, "row0 must lie in [0, 2^40]");
+}
+
+void check_residual(int32_t kind, int32_t post, int32_t pre, int32_t gate_kind, float alpha, float beta) {
+  check_kind(kind);
+  if (!post && !pre) fail(LOPT_ERR_INVALID_ARGUMENT, "neither norm: post and pre are 0");
+  if (gate_kind < LOPT_GATE_NONE || gate_kind > LOPT_GATE_MATRIX) fail(LOPT_ERR_INVALID_ARGUMENT, "unknown kind of gate");
+  if (!std::isfinite(alpha) || !std::isfinite(beta)) fail(LOPT_ERR_INVALID_ARGUMENT, "alpha and beta must be finite");
 }
 
 void check_state_bits(int32_t bits) {
@@ -191,6 +198,117 @@ lopt_status lopt_norm_backward(int32_t kind, int64_t rows, int64_t cols, int32_t
     a.rows = rows; a.cols = cols; a.lddy = lddy; a.ldx = ldx; a.lddx = lddx;
     a.dtype = dtype; a.wdtype = w_dtype; a.gdtype = g_dtype; a.rms = rms; a.accumulate = accumulate != 0;
     hip_check(launch_norm_backward(a, static_cast<hipStream_t>(stream)), "norm backward");
+  });
+}
+
+lopt_status lopt_residual_norm_forward(int32_t kind, int32_t post, int32_t pre, int64_t rows, int64_t cols, int32_t dtype,
+                                       const void* x, int64_t ldx, const void* y, int64_t ldy, int32_t gate_kind,
+                                       const void* gate, int64_t ldg, const void* post_weight, const void* post_bias,
+                                       const void* weight, const void* bias, int32_t w_dtype, float alpha, float beta,
+                                       float eps, void* h, int64_t ldh, void* z, int64_t ldz, float* stats, void* stream) {
+  return guarded([&] {
+    check_residual(kind, post, pre, gate_kind, alpha, beta);
+    check_dims(rows, cols);
+    check_dtype(dtype, "x");
+    if (post_weight || post_bias || weight || bias || gate_kind == LOPT_GATE_VECTOR) check_dtype(w_dtype, "weight");
+    if (!(eps >= 0.f) || !std::isfinite(eps)) fail(LOPT_ERR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+    const bool rms = kind == LOPT_NORM_RMS;
+    if (rms && (post_bias || bias)) fail(LOPT_ERR_INVALID_ARGUMENT, "an RMS norm has no bias");
+    if (!post && (post_weight || post_bias)) fail(LOPT_ERR_INVALID_ARGUMENT, "post_weight or post_bias without the norm of y");
+    if (!pre && (weight || bias || z)) fail(LOPT_ERR_INVALID_ARGUMENT, "weight, bias or z without the norm of h");
+    Buffers bufs;
+    const int64_t size = elem_bytes(dtype), wsize = elem_bytes(w_dtype);
+    const auto vec = [&](const char* name, const void* p) {
+      if (rows && p) bufs.add(name, p, cols * wsize, wsize, false);
+    };
+    bufs.matrix("x", x, rows, cols, ldx, size, false);
+    bufs.matrix("y", y, rows, cols, ldy, size, false);
+    if (gate_kind == LOPT_GATE_MATRIX) bufs.matrix("gate", gate, rows, cols, ldg, size, false);
+    else if (gate_kind == LOPT_GATE_VECTOR && rows) bufs.add("gate", gate, cols * wsize, wsize, false);
+    vec("post_weight", post_weight);
+    vec("post_bias", post_bias);
+    vec("weight", weight);
+    vec("bias", bias);
+    bufs.matrix("h", h, rows, cols, ldh, size, true);
+    if (pre) bufs.matrix("z", z, rows, cols, ldz, size, true);
+    if (rows && stats) bufs.add("stats", stats, 16 * rows, 4, true);
+    bufs.no_overlap();
+    ResidualForward a{};
+    a.x = x; a.y = y; a.gate = gate; a.w1 = post_weight; a.b1 = post_bias; a.w2 = weight; a.b2 = bias;
+    a.h = h; a.z = z; a.stats = stats;
+    a.rows = rows; a.cols = cols; a.ldx = ldx; a.ldy = ldy; a.ldg = ldg; a.ldh = ldh; a.ldz = ldz;
+    a.dtype = dtype; a.wdtype = w_dtype; a.gate_kind = gate_kind; a.rms = rms; a.post = post != 0; a.pre = pre != 0;
+    a.alpha = alpha; a.beta = beta; a.eps = eps;
+    hip_check(launch_residual_forward(a, static_cast<hipStream_t>(stream)), "residual norm forward");
+  });
+}
+
+lopt_status lopt_residual_norm_backward_workspace(int64_t rows, int64_t cols, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(LOPT_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    check_dims(rows, cols);
+    *bytes = residual_backward_bytes(rows, cols);
+  });
+}
+
+lopt_status lopt_residual_norm_backward(int32_t kind, int32_t post, int32_t pre, int64_t rows, int64_t cols, int32_t dtype,
+                                        const void* dh, int64_t lddh, const void* dz, int64_t lddz, const void* y, int64_t ldy,
+                                        const void* h, int64_t ldh, const float* stats, int32_t gate_kind, const void* gate,
+                                        int64_t ldg, const void* post_weight, const void* post_bias, const void* weight,
+                                        int32_t w_dtype, float alpha, float beta, void* dx, int64_t lddx, void* dy,
+                                        int64_t lddy, void* dgate, int64_t lddg, void* dpost_weight, void* dpost_bias,
+                                        void* dweight, void* dbias, int32_t g_dtype, int32_t accumulate, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_residual(kind, post, pre, gate_kind, alpha, beta);
+    check_dims(rows, cols);
+    check_dtype(dtype, "y");
+    const bool rms = kind == LOPT_NORM_RMS, vector_gate = gate_kind == LOPT_GATE_VECTOR;
+    if (post_weight || post_bias || weight || vector_gate) check_dtype(w_dtype, "weight");
+    void* const sums[5] = {dpost_weight, dpost_bias, dweight, dbias, vector_gate ? dgate : nullptr};
+    const bool any = std::any_of(sums, sums + 5, [](const void* p) { return p != nullptr; });
+    if (any) check_dtype(g_dtype, "dweight");
+    if (rms && (post_bias || dpost_bias || dbias)) fail(LOPT_ERR_INVALID_ARGUMENT, "an RMS norm has no bias");
+    if (!post && (post_weight || post_bias || dpost_weight || dpost_bias))
+      fail(LOPT_ERR_INVALID_ARGUMENT, "post_weight, post_bias or a gradient of theirs without the norm of y");
+    if (!pre && (weight || dweight || dbias || dz)) fail(LOPT_ERR_INVALID_ARGUMENT, "weight, dz or a gradient of the weight or bias without the norm of h");
+    if (gate_kind == LOPT_GATE_NONE && dgate) fail(LOPT_ERR_INVALID_ARGUMENT, "dgate without a gate");
+    Buffers bufs;
+    const int64_t size = elem_bytes(dtype), wsize = elem_bytes(w_dtype), gsize = elem_bytes(g_dtype);
+    const auto vec = [&](const char* name, const void* p, int64_t s, bool written) {
+      if (p && (rows || written)) bufs.add(name, p, cols * s, s, written);
+    };
+    if (dh) bufs.matrix("dh", dh, rows, cols, lddh, size, false);
+    if (dz) bufs.matrix("dz", dz, rows, cols, lddz, size, false);
+    bufs.matrix("y", y, rows, cols, ldy, size, false);
+    if (pre) bufs.matrix("h", h, rows, cols, ldh, size, false);
+    if (rows) bufs.add("stats", stats, 16 * rows, 4, false);
+    if (gate_kind == LOPT_GATE_MATRIX) bufs.matrix("gate", gate, rows, cols, ldg, size, false);
+    else if (vector_gate && rows) bufs.add("gate", gate, cols * wsize, wsize, false);
+    vec("post_weight", post_weight, wsize, false);
+    vec("post_bias", post_bias, wsize, false);
+    vec("weight", weight, wsize, false);
+    if (dx) bufs.matrix("dx", dx, rows, cols, lddx, size, true);
+    if (dy) bufs.matrix("dy", dy, rows, cols, lddy, size, true);
+    if (dgate && !vector_gate) bufs.matrix("dgate", dgate, rows, cols, lddg, size, true);
+    const char* const names[5] = {"dpost_weight", "dpost_bias", "dweight", "dbias", "dgate"};
+    for (int k = 0; k < 5; ++k) vec(names[k], sums[k], gsize, true);
+    if (any) {
+      const size_t need = residual_backward_bytes(rows, cols);
+      check_workspace(workspace, ws_bytes, need);
+      if (need) bufs.add("workspace", workspace, int64_t(need), 256, true);
+    }
+    bufs.no_overlap();
+    ResidualBackward a{};
+    a.dh = dh; a.dz = dz; a.y = y; a.h = h; a.stats = stats; a.gate = gate;
+    a.w1 = post_weight; a.b1 = post_bias; a.w2 = weight; a.dx = dx; a.dy = dy; a.dgate = vector_gate ? nullptr : dgate;
+    std::copy(sums, sums + 5, a.sums);
+    a.part = any ? static_cast<float*>(workspace) : nullptr;
+    a.rows = rows; a.cols = cols; a.lddh = lddh; a.lddz = lddz; a.ldy = ldy; a.ldh = ldh; a.ldg = ldg;
+    a.lddx = lddx; a.lddy = lddy; a.lddg = lddg;
+    a.dtype = dtype; a.wdtype = w_dtype; a.gdtype = g_dtype; a.gate_kind = gate_kind; a.rms = rms; a.post = post != 0;
+    a.pre = pre != 0; a.accumulate = accumulate != 0; a.alpha = alpha; a.beta = beta;
+    hip_check(launch_residual_backward(a, static_cast<hipStream_t>(stream)), "residual norm backward");
   });
 }
 

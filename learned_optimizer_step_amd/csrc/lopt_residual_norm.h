@@ -1,0 +1,56 @@
+// Row layouts of the residual update's kernels, shared by the forward and backward pass.
+#pragma once
+
+#include "lopt_norm.h"
+
+namespace lopt {
+
+// Longer rows are read again for each of their sums (the *_long kernels).
+constexpr int64_t kLongestResidualRow = 8192;
+
+// Calls f(RowLayout) for the layout that holds rows of n columns: 8 elements a
+// thread, as up to eight vectors of parameters and sums stay in registers beside
+// a row's four.
+template <class F>
+auto with_residual_layout(int64_t n, F&& f) {
+  if (n <= 64) return f(RowLayout<8, 8, 256>());     // eight rows in a wave
+  if (n <= 512) return f(RowLayout<8, 64, 256>());
+  if (n <= 1024) return f(RowLayout<8, 128, 128>());
+  if (n <= 2048) return f(RowLayout<8, 256, 256>());
+  if (n <= 4096) return f(RowLayout<8, 512, 512>());
+  return f(RowLayout<8, 1024, 1024>());
+}
+
+// Calls f(mode) for rows of n columns: the vectors of rows that are whole
+// numbers of them are those of kTail too.
+template <class T, class L, class F>
+void with_residual_mode(int64_t n, F&& f) {
+  if constexpr (L::TPR == 8) {
+    if (n < kVec<T>) return f(std::integral_constant<int, kTiny>());
+  }
+  f(std::integral_constant<int, kTail>());
+}
+
+// The thread's elements of a row, 0 where they are not its own.
+template <class T, class At>
+__device__ __forceinline__ void load_row(const At& at, const T* row, float (&x)[At::NV * At::V]) {
+  Pack<T, At::V> p[At::NV];
+#pragma unroll
+  for (int k = 0; k < At::NV; ++k) p[k] = at[k].load(row);
+#pragma unroll
+  for (int k = 0; k < At::NV; ++k)
+#pragma unroll
+    for (int i = 0; i < At::V; ++i) x[k * At::V + i] = at[k].own(i) ? to_f32(p[k].v[i]) : 0.f;
+}
+template <class T, class At>
+__device__ __forceinline__ void store_row(const At& at, T* row, const float (&x)[At::NV * At::V]) {
+#pragma unroll
+  for (int k = 0; k < At::NV; ++k) {
+    Pack<T, At::V> p;
+#pragma unroll
+    for (int i = 0; i < At::V; ++i) p.v[i] = from_f32<T>(x[k * At::V + i]);
+    at[k].store(row, p);
+  }
+}
+
+}  // namespace lopt

@@ -3,6 +3,7 @@
 They produce the gradients that ``lopt.LearnedOptimizer`` and ``lopt.AdamW`` step with:
 
 * ``layer_norm``, ``rms_norm``  a transformer's norms
+* ``residual_norm``             the residual update between two blocks with its gate and the norms on both sides
 * ``embedding``                 a token lookup with scaling, its gradient by sorted tokens
 * ``distill_loss``              a loss from a teacher's top logits, where a backward pass begins
 
@@ -69,6 +70,43 @@ def norm_backward(grad_y, x, weight, mean, rstd, *, rms: bool = False, grad_weig
     float32).  An RMS norm has no grad_bias."""
     return _C.norm_backward(grad_y, x, weight, mean, rstd, rms, grad_weight, grad_bias, accumulate, need_x, need_weight,
                             not rms if need_bias is None else need_bias, grad_dtype)
+
+
+# ---------------------------------------------------------------------------
+# the residual update between two blocks
+
+def residual_norm(x, y, gate=None, post_weight=None, post_bias=None, weight=None, bias=None, eps: float = 1e-5, *,
+                  alpha: float = 1.0, beta: float = 1.0, rms: bool = False, post: bool = True, pre: bool = True):
+    """(h, z): h = alpha x + beta gate norm(y), the residual stream x after a block's output y, and z = norm(h), the next
+    block's input; differentiable in every tensor.  See ``residual_norm_forward``."""
+    return _C.residual_norm(x, y, gate, post_weight, post_bias, weight, bias, eps, alpha, beta, rms, post, pre)
+
+
+def residual_norm_forward(x, y, gate=None, post_weight=None, post_bias=None, weight=None, bias=None, eps: float = 1e-5, *,
+                          alpha: float = 1.0, beta: float = 1.0, rms: bool = False, post: bool = True, pre: bool = True):
+    """(h, z, stats) over the last dimension: u = norm(y; post_weight, post_bias) (y itself without post),
+    h = alpha x + beta gate u, z = norm(h; weight, bias) (None without pre).
+
+    x, y, h and z have one shape and type; z is the norm of h as it is kept in that type.  gate: None, a vector of the
+    last dimension, or a tensor like y.  Vectors have one type.  The norms are layer norms, or RMS norms without biases.
+    stats: float32, (4, rows), for ``residual_norm_backward``."""
+    return _C.residual_norm_forward(x, y, gate, post_weight, post_bias, weight, bias, eps, alpha, beta, rms, post, pre)
+
+
+def residual_norm_backward(grad_h, grad_z, y, h, stats, gate=None, post_weight=None, post_bias=None, weight=None, *,
+                           alpha: float = 1.0, beta: float = 1.0, rms: bool = False, post: bool = True, pre: bool = True,
+                           need_x: bool = True, need_y: bool = True, need_params: bool = True, grad_gate=None,
+                           grad_post_weight=None, grad_post_bias=None, grad_weight=None, grad_bias=None,
+                           accumulate: bool = False, grad_dtype: Optional[torch.dtype] = None):
+    """Gradients (x, y, gate, post_weight, post_bias, weight, bias) of ``residual_norm_forward``, None where there is none.
+
+    grad_h, grad_z: None for zeros (grad_z also without pre).  grad_*: buffers to write for the vectors, or, with
+    accumulate, to add to (all that are computed are needed then); made anew where None, of grad_dtype, else of the
+    vectors' type, else float32.  Both norms' weights (and a layer norm's biases) have gradients, whether they were
+    given or not; need_params=False leaves out these and the gate's."""
+    return _C.residual_norm_backward(grad_h, grad_z, y, h, stats, gate, post_weight, post_bias, weight, alpha, beta, rms, post, pre,
+                                     need_x, need_y, need_params, grad_gate, grad_post_weight, grad_post_bias, grad_weight,
+                                     grad_bias, accumulate, grad_dtype)
 
 
 # ---------------------------------------------------------------------------

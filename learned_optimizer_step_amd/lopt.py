@@ -45,6 +45,9 @@ LOPT_BF16 = 1
 LOPT_F16 = 2
 LOPT_NORM_LAYER = 0
 LOPT_NORM_RMS = 1
+LOPT_GATE_NONE = 0
+LOPT_GATE_VECTOR = 1
+LOPT_GATE_MATRIX = 2
 LOPT_MAX_TOP = 1024      # entries of a teacher's list
 
 
@@ -126,6 +129,12 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "lopt_norm_backward_workspace": (st, [i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
         "lopt_norm_backward": (st, [i32, i64, i64, i32, ptr, i64, ptr, i64, ptr, i32, ptr, ptr, ptr, i64, ptr, ptr, i32,
                                     i32, ptr, ctypes.c_size_t, ptr]),
+        "lopt_residual_norm_forward": (st, [i32, i32, i32, i64, i64, i32, ptr, i64, ptr, i64, i32, ptr, i64, ptr, ptr, ptr, ptr,
+                                            i32, f32, f32, f32, ptr, i64, ptr, i64, ptr, ptr]),
+        "lopt_residual_norm_backward_workspace": (st, [i64, i64, size]),
+        "lopt_residual_norm_backward": (st, [i32, i32, i32, i64, i64, i32, ptr, i64, ptr, i64, ptr, i64, ptr, i64, ptr, i32,
+                                             ptr, i64, ptr, ptr, ptr, i32, f32, f32, ptr, i64, ptr, i64, ptr, i64, ptr, ptr,
+                                             ptr, ptr, i32, i32, ptr, ctypes.c_size_t, ptr]),
         "lopt_embedding_forward": (st, [i64, ptr, i32, i64, i64, i64, ptr, i64, i32, f32, ptr, i64, i32, ptr]),
         "lopt_embedding_backward_workspace": (st, [i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]),
         "lopt_embedding_backward": (st, [i64, ptr, i32, ptr, i64, i32, i64, i64, i64, f32, ptr, i64, i32, i32, ptr,
@@ -328,6 +337,20 @@ def lopt_norm_backward_workspace(rows: int, cols: int) -> int:
 
 def lopt_norm_backward(*args) -> None:
     _check((_lib or load_library()).lopt_norm_backward(*args))
+
+
+def lopt_residual_norm_forward(*args) -> None:
+    _check((_lib or load_library()).lopt_residual_norm_forward(*args))
+
+
+def lopt_residual_norm_backward_workspace(rows: int, cols: int) -> int:
+    out = ctypes.c_size_t()
+    _check((_lib or load_library()).lopt_residual_norm_backward_workspace(rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def lopt_residual_norm_backward(*args) -> None:
+    _check((_lib or load_library()).lopt_residual_norm_backward(*args))
 
 
 def lopt_embedding_forward(*args) -> None:

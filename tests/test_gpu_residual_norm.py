@@ -1,0 +1,332 @@
+"""The residual update with its norms on the GPU against its definition in 64 bits."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("no GPU", allow_module_level=True)
+
+from learned_optimizer_step_amd import layers  # noqa: E402
+from learned_optimizer_step_amd import lopt as L  # noqa: E402
+from ops_cases import CODE, TYPES, U, close, norm_forward, norm_forward_tols  # noqa: E402
+from residual_cases import backward, bound, update  # noqa: E402
+
+# one row to thousands; every row layout with its first and last width, widths that no vector divides, rows too long for registers
+SHAPES = [(1, 1), (3, 2), (1, 768), (5, 7), (1000, 8), (67, 64), (130, 65), (33, 197), (9, 512), (6, 513), (2049, 768), (70, 1000),
+          (5, 1024), (7, 1025), (300, 2048), (4, 2049), (3, 4096), (5, 4099), (3, 8192), (2, 8193), (3, 20001), (5000, 24)]
+NORMS = [(True, True), (True, False), (False, True)]
+GATES = ["none", "vector", "matrix"]
+NAMES = ("x", "y", "gate", "post_weight", "post_bias", "weight", "bias")
+
+
+def make(rows, cols, t, wt, seed, gate="none", post=True, pre=True, rms=False):
+    g = torch.Generator().manual_seed(seed)
+    x = (torch.randn(rows, cols, generator=g) * (0.5 + torch.rand(rows, 1, generator=g)) + torch.randn(1, cols, generator=g)).to(t)
+    y = (0.5 * torch.randn(rows, cols, generator=g) + 0.3 * torch.randn(1, cols, generator=g)).to(t)
+    dh, dz = (0.1 * torch.randn(2, rows, cols, generator=g)).to(t)
+    ws = [(a + 0.2 * torch.randn(cols, generator=g)).to(wt) for a in (1, 0, 1, 0, 0.5)]
+    gt = None if gate == "none" else ws[4] if gate == "vector" else torch.sigmoid(torch.randn(rows, cols, generator=g)).to(t)
+    w1, b1 = (ws[0] if post else None), (ws[1] if post and not rms else None)
+    w2, b2 = (ws[2] if pre else None), (ws[3] if pre and not rms else None)
+    return x, y, gt, w1, b1, w2, b2, dh, dz
+
+
+def gpu(*ts):
+    return [None if v is None else v.cuda() for v in ts]
+
+
+def check(x, y, gate, w1, b1, w2, b2, dh, dz, eps, o, what):
+    t = x.dtype
+    wt = next((v.dtype for v in (w1, b1, w2, b2, gate if gate is not None and gate.dim() == 1 else None) if v is not None), torch.float32)
+    gx, gy, gg, g1, gb1, g2, gb2, gdh, gdz = gpu(x, y, gate, w1, b1, w2, b2, dh, dz)
+    h, z, stats = layers.residual_norm_forward(gx, gy, gg, g1, gb1, g2, gb2, eps, **o)
+    want, tol, s1 = update(x, y, gate, w1, b1, eps, o)
+    close(h, want, bound(want, tol, t), f"{what} h")
+    kept = stats.cpu()
+    if s1 is not None:
+        close(stats[1], s1[2], s1[3], f"{what} rstd of y")
+        if not o["rms"]:
+            close(stats[0], s1[0], s1[1], f"{what} mean of y")
+    if o["pre"]:
+        hc = h.cpu()
+        want = norm_forward(hc, w2, b2, eps, o["rms"])
+        tz, tm, tr = norm_forward_tols(*want, t, hc)
+        close(z, want[0], tz, f"{what} z")
+        close(stats[3], want[2], tr, f"{what} rstd of h")
+        if not o["rms"]:
+            close(stats[2], want[1], tm, f"{what} mean of h")
+    else:
+        assert z is None
+    got = dict(zip(NAMES, layers.residual_norm_backward(gdh, gdz if o["pre"] else None, gy, h if o["pre"] else None, stats, gg, g1, gb1, g2, **o)))
+    ref = backward(dh, dz if o["pre"] else None, y, h.cpu(), kept, gate, w1, b1, w2, o)
+    for k in NAMES:
+        assert (got[k] is None) == (k not in ref), (what, k)
+        if k in ref:
+            ty = t if got[k].dim() == 2 else wt
+            assert got[k].dtype == ty
+            close(got[k], ref[k][0], bound(*ref[k], ty), f"{what} grad of {k}")
+
+
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+@pytest.mark.parametrize("norms", range(3), ids=lambda k: "post" * NORMS[k][0] + "pre" * NORMS[k][1])
+@pytest.mark.parametrize("k", range(len(SHAPES)), ids=lambda k: f"{SHAPES[k][0]}x{SHAPES[k][1]}")
+def test_against_the_definition(k, norms, rms):
+    rows, cols = SHAPES[k]
+    post, pre = NORMS[norms]
+    for gate in GATES:
+        n = k + norms + GATES.index(gate) + rms
+        t = TYPES[n % 3]
+        wt = torch.float32 if n % 2 else t
+        o = dict(alpha=1.0 if n % 4 else 0.7, beta=(1.0, -0.4)[n % 2], rms=rms, post=post, pre=pre)
+        eps = 1e-2 if cols == 1 else 1e-5
+        check(*make(rows, cols, t, wt, rows * 7 + cols + n, gate, post, pre, rms), eps, o, f"{rows}x{cols} {t} {gate}")
+
+
+def test_without_weights_and_with_some():
+    x, y, gate, w1, b1, w2, b2, dh, dz = make(40, 300, torch.bfloat16, torch.float32, 3, "vector")
+    o = dict(alpha=1.0, beta=1.0, rms=False, post=True, pre=True)
+    check(x, y, None, None, None, None, None, dh, dz, 1e-6, o, "none")
+    check(x, y, gate, None, None, None, None, dh, dz, 1e-6, o, "gate")
+    check(x, y, gate, None, b1, w2, None, dh, dz, 1e-6, o, "some")
+    check(x, y, None, w1, None, None, b2, dh, dz, 1e-6, o, "others")
+    check(x, y, gate, w1, b1, w2, b2, None, dz, 1e-6, o, "no gradient of h")
+    check(x, y, gate, w1, b1, w2, b2, dh, None, 1e-6, o, "no gradient of z")
+
+
+def test_the_norms_of_the_library():
+    """z is layer_norm's of h to the last bit, and a gate of None with alpha 0 and beta 1 leaves norm(y) as h."""
+    for cols in (64, 500, 768, 3000, 9000):
+        x, y, _, w1, b1, w2, b2, *_ = gpu(*make(20, cols, torch.float32, torch.float32, cols))
+        for rms in (False, True):
+            c1, c2 = (None, None) if rms else (b1, b2)
+            h, z, _ = layers.residual_norm_forward(x, y, None, w1, c1, w2, c2, 1e-5, alpha=0.0, rms=rms)
+            a = layers.norm_forward(y, w1, c1, 1e-5, rms=rms)[0]
+            b = layers.norm_forward(h, w2, c2, 1e-5, rms=rms)[0]
+            # other threads add in another order
+            assert bool(((h - a).abs() <= 300 * U * (a.abs() + 1)).all()) and bool(((z - b).abs() <= 300 * U * (b.abs() + 1)).all())
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_row_with_nan_or_infinity_spoils_no_other(bad):
+    for cols in (60, 500, 1001, 3000, 9000):
+        args = make(9, cols, torch.float32, torch.float32, cols, "matrix")
+        for where in (0, 1, 2):          # x, y, gate
+            a = [v.clone() for v in args]
+            a[where][4, cols // 2] = bad
+            x, y, gate, w1, b1, w2, b2, dh, dz = gpu(*a)
+            h, z, stats = layers.residual_norm_forward(x, y, gate, w1, b1, w2, b2)
+            g = layers.residual_norm_backward(dh, dz, y, h, stats, gate, w1, b1, w2)
+            for v in (z, g[0], g[1], g[2]):
+                assert torch.isfinite(v).all(1).cpu().tolist()[:4] == [True] * 4 and torch.isfinite(v[5:]).all(), (cols, where)
+            assert not torch.isfinite(z[4]).all()
+
+
+def test_strided_rows_and_rows_behind_the_last():
+    """Inputs as slices of wider tensors, outputs with a row stride through the library's call: what lies between and behind
+    the rows is left as it was."""
+    rows, cols, ld = 37, 193, 260
+    g = torch.Generator().manual_seed(8)
+    for t in TYPES:
+        big = torch.randn(rows + 4, ld, generator=g).to(t).cuda()
+        x, y, gate, dh, dz = (big[k % 4:rows + k % 4, 3 + 11 * k:3 + 11 * k + cols] for k in range(5))
+        w1, b1, w2, b2 = (torch.randn(cols, generator=g).cuda() for _ in range(4))
+        dense = [v.contiguous() for v in (x, y, gate, dh, dz)]
+        want = layers.residual_norm_forward(*dense[:3], w1, b1, w2, b2)
+        got = layers.residual_norm_forward(x, y, gate, w1, b1, w2, b2)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        grads = layers.residual_norm_backward(*dense[3:], dense[1], want[0], want[2], dense[2], w1, b1, w2)
+        again = layers.residual_norm_backward(dh, dz, y, want[0], want[2], gate, w1, b1, w2)
+        assert all(torch.equal(a, b) for a, b in zip(grads, again))
+        outs = [torch.full((rows + 2, ld), 7.0, dtype=t, device="cuda") for _ in range(5)]
+        stream, code, size = torch.cuda.current_stream().cuda_stream, CODE[t], outs[0].element_size()
+        at = [v.data_ptr() + 5 * size for v in outs]
+        L.lopt_residual_norm_forward(0, 1, 1, rows, cols, code, x.data_ptr(), ld, y.data_ptr(), ld, 2, gate.data_ptr(), ld, w1.data_ptr(),
+                                     b1.data_ptr(), w2.data_ptr(), b2.data_ptr(), 0, 1.0, 1.0, 1e-5, at[0], ld, at[1], ld, None, stream)
+        L.lopt_residual_norm_backward(0, 1, 1, rows, cols, code, dh.data_ptr(), ld, dz.data_ptr(), ld, y.data_ptr(), ld, at[0], ld,
+                                      want[2].data_ptr(), 2, gate.data_ptr(), ld, w1.data_ptr(), b1.data_ptr(), w2.data_ptr(), 0, 1.0, 1.0,
+                                      at[2], ld, at[3], ld, at[4], ld, None, None, None, None, 0, 0, None, 0, stream)
+        for out, ref in zip(outs, (want[0], want[1], grads[0], grads[1], grads[2])):
+            assert torch.equal(out[:rows, 5:5 + cols], ref)
+            out[:rows, 5:5 + cols] = 7.0
+            assert bool((out == 7.0).all())
+
+
+def test_accumulating_and_leaving_out():
+    x, y, gate, w1, b1, w2, b2, dh, dz = gpu(*make(500, 321, torch.bfloat16, torch.float32, 11, "vector"))
+    h, z, stats = layers.residual_norm_forward(x, y, gate, w1, b1, w2, b2)
+    call = lambda **kw: layers.residual_norm_backward(dh, dz, y, h, stats, gate, w1, b1, w2, **kw)  # noqa: E731
+    want = call()
+    assert all(torch.equal(a, b) for a, b in zip(want, call())), "the same inputs give the same bits"
+    base = torch.randn(5, 321, device="cuda")
+    bufs = dict(zip(("grad_gate", "grad_post_weight", "grad_post_bias", "grad_weight", "grad_bias"), base.clone()))
+    got = call(accumulate=True, need_x=False, **bufs)
+    assert got[0] is None and torch.equal(got[1], want[1])
+    for k, (b, buf) in enumerate(zip(base, bufs.values())):
+        assert got[2 + k] is buf or got[2 + k].data_ptr() == buf.data_ptr()
+        assert torch.equal(buf, b + want[2 + k])
+    got = call(need_params=False, need_y=False)
+    assert torch.equal(got[0], want[0]) and got[1:] == (None,) * 6
+    half = call(grad_dtype=torch.bfloat16)
+    assert all(torch.equal(a, b.bfloat16()) for a, b in zip(half[2:], want[2:]))
+    one = torch.empty(321, dtype=torch.float16, device="cuda")
+    got = call(grad_weight=one)
+    assert all(torch.equal(a, b.half()) for a, b in zip(got[2:], want[2:]))
+
+
+def test_no_rows():
+    x, w = torch.empty(0, 50, device="cuda"), torch.ones(50, device="cuda")
+    h, z, stats = layers.residual_norm_forward(x, x, w, w, w, w, w)
+    assert h.shape == z.shape == (0, 50) and stats.shape == (4, 0)
+    g = layers.residual_norm_backward(x, x, x, h, stats, w, w, w, w)
+    assert g[0].shape == (0, 50) and all(not v.any() for v in g[2:])
+    gw = torch.full((50,), 2.0, device="cuda")
+    with pytest.raises(ValueError, match="accumulate"):
+        layers.residual_norm_backward(x, x, x, h, stats, w, w, w, w, grad_weight=gw, accumulate=True)
+
+
+@pytest.mark.parametrize("gate", GATES)
+@pytest.mark.parametrize("rms", [False, True], ids=["layer", "rms"])
+def test_autograd_and_differences(rms, gate):
+    """Gradients through autograd against central differences of the definition in 64 bits, in random directions."""
+    args = make(12, 90, torch.float32, torch.float32, 21, gate, rms=rms)
+    o = dict(alpha=0.8, beta=1.3, rms=rms, post=True, pre=True)
+    leaves = [None if v is None else v.cuda().requires_grad_(True) for v in args[:7]]
+    shaped = [v.view(3, 4, 90) if v is not None and v.dim() == 2 else v for v in leaves]
+    h, z = layers.residual_norm(*shaped, 1e-5, **o)
+    assert h.shape == z.shape == (3, 4, 90)
+    dh, dz = (v.view(3, 4, 90).cuda() for v in args[7:])
+    have = [v for v in leaves if v is not None]
+    grads = torch.autograd.grad([h, z], have, [dh, dz])
+    h2, z2 = layers.residual_norm(*shaped, 1e-5, **o)
+    only_z = torch.autograd.grad(z2, have, dz, retain_graph=True)
+    only_h = torch.autograd.grad(h2, [leaves[0], leaves[1]], dh)
+    assert all(bool(((a + b - c).abs() <= 1e-5 * (c.abs() + c.abs().max())).all()) for a, b, c in zip(only_z, only_h, grads[:2]))
+
+    def f(x, y, gt, w1, b1, w2, b2):
+        u = norm_forward(y, w1, b1, 1e-5, rms)[0]
+        v = o["alpha"] * x + o["beta"] * (u if gt is None else gt * u)
+        return (norm_forward(v, w2, b2, 1e-5, rms)[0] * args[8].double()).sum() + (v * args[7].double()).sum()
+
+    g = torch.Generator().manual_seed(2)
+    ps = [None if v is None else v.double() for v in args[:7]]
+    index = [k for k in range(7) if ps[k] is not None]
+    for k, grad in zip(index, grads):
+        d = torch.randn(ps[k].shape, generator=g, dtype=torch.float64)
+        s = 1e-4
+        plus = f(*[v if j != k else v + s * d for j, v in enumerate(ps)])
+        minus = f(*[v if j != k else v - s * d for j, v in enumerate(ps)])
+        want = (plus - minus) / (2 * s)
+        got = (grad.double().cpu() * d).sum()
+        # differences: s^2 of the third derivative (about the value's size here), and 2^-52 / s; the gradient: its roundings
+        tol = 1e-6 * abs(want) + 200 * U * (grad.double().cpu() * d).abs().sum() + 2e-7 * (1 + args[7].double().abs().sum() + args[8].double().abs().sum())
+        assert abs(got - want) <= tol, (NAMES[k], got, want)
+
+
+@pytest.mark.parametrize("which", ["x", "y", "gate", "post_weight", "post_bias", "weight", "bias", "x weight", "gate bias", "y post_bias bias"])
+@pytest.mark.parametrize("given", ["gate post_weight post_bias weight bias", "gate post_bias bias", "post_weight weight", ""])
+def test_autograd_of_any_of_the_tensors(given, which):
+    """Each gradient reaches its own tensor, whichever are there and whichever want one."""
+    given, which = given.split() + ["x", "y"], which.split()
+    if not set(which) <= set(given):
+        return
+    args = dict(zip(NAMES, gpu(*make(20, 130, torch.float32, torch.float32, 51, "vector")[:7])))
+    dh, dz = gpu(*make(20, 130, torch.float32, torch.float32, 51, "vector")[7:])
+    args = {k: v if k in given else None for k, v in args.items()}
+    h, _, stats = layers.residual_norm_forward(**args)
+    want = dict(zip(NAMES, layers.residual_norm_backward(dh, dz, args["y"], h, stats, args["gate"], args["post_weight"], args["post_bias"], args["weight"])))
+    for k in which:
+        args[k].requires_grad_(True)
+    h, z = layers.residual_norm(**args)
+    got = torch.autograd.grad([h, z], [args[k] for k in which], [dh, dz])
+    assert all(torch.equal(g, want[k]) for g, k in zip(got, which))
+
+
+def test_biases_of_another_type_than_fp32_alone():
+    x, y, *_ , b2, dh, dz = gpu(*make(20, 130, torch.bfloat16, torch.bfloat16, 5))
+    b2.requires_grad_(True)
+    h, z = layers.residual_norm(x, y, bias=b2)
+    d, = torch.autograd.grad(z, b2, dz)
+    assert d.dtype == torch.bfloat16
+    want = dz.double().sum(0)
+    assert bool(((d.double() - want).abs() <= 2.0 ** -8 * want.abs() + 200 * U * dz.double().abs().sum(0)).all())
+
+
+def test_gradients_cannot_be_differentiated_and_saved_tensors_are_watched():
+    x, y, *_ = gpu(*make(5, 64, torch.float32, torch.float32, 4))
+    x.requires_grad_(True)
+    h, z = layers.residual_norm(x, y)
+    grad, = torch.autograd.grad(z.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="cannot be differentiated"):
+        grad.sum().backward()
+    h, z = layers.residual_norm(x, y)
+    y.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        z.sum().backward()
+
+
+def test_on_another_stream_and_in_a_graph():
+    args = gpu(*make(700, 768, torch.bfloat16, torch.float32, 31, "vector"))
+    x, y, gate, w1, b1, w2, b2, dh, dz = args
+    run = lambda x, y: (lambda f: f + layers.residual_norm_backward(dh, dz, y, f[0], f[2], gate, w1, b1, w2))(  # noqa: E731
+        layers.residual_norm_forward(x, y, gate, w1, b1, w2, b2))
+    want = run(x, y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run(x, y)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(p, q) for p, q in zip(want, got))
+    xs, ys = x.clone(), y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(xs, ys)
+    for k in range(4):
+        xs.copy_(x * (1 + k))
+        ys.copy_(y * (2 - k))
+        eager = run(xs, ys)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(eager, out)), k
+
+
+def test_more_elements_than_32_bits_count():
+    """2^31 + elements: the last rows against the same rows alone."""
+    cols, rows = 2048, (1 << 20) + 3
+    x = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    y = torch.ones(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-70:] = torch.randn(70, cols, device="cuda")
+    y[-70:] = torch.randn(70, cols, device="cuda")
+    w = torch.randn(cols, device="cuda")
+    h, z, stats = layers.residual_norm_forward(x, y, None, w, None, w, None, rms=True)
+    ph, pz, ps = layers.residual_norm_forward(x[-70:].clone(), y[-70:].clone(), None, w, None, w, None, rms=True)
+    assert torch.equal(h[-70:], ph) and torch.equal(z[-70:], pz) and torch.equal(stats[1::2, -70:], ps[1::2])
+    dz = torch.zeros_like(x)
+    dz[-70:] = torch.randn(70, cols, device="cuda")
+    g = layers.residual_norm_backward(None, dz, y, h, stats, None, w, None, w, rms=True)
+    p = layers.residual_norm_backward(None, dz[-70:].clone(), y[-70:].clone(), ph, ps, None, w, None, w, rms=True)
+    assert torch.equal(g[0][-70:], p[0]) and torch.equal(g[1][-70:], p[1])
+    for a, b in ((g[3], p[3]), (g[5], p[5])):
+        assert bool(((a - b).abs() <= 400 * U * (70 * 40.0)).all())
+
+
+def test_refusals_of_the_tensors():
+    x, w = torch.ones(4, 8, device="cuda"), torch.ones(8, device="cuda")
+    h, z, stats = layers.residual_norm_forward(x, x, None, w, w, w, w)
+    fwd, bwd = layers.residual_norm_forward, layers.residual_norm_backward
+    for call in (lambda: fwd(x, x[:2]), lambda: fwd(x, x.half()), lambda: fwd(x, x.cpu()), lambda: fwd(x, x, w[:4]), lambda: fwd(x, x, x[:2]),
+                 lambda: fwd(x, x, x.half()), lambda: fwd(x, x, None, w, w.half()), lambda: fwd(x, x, w.half(), w), lambda: fwd(x, x, None, w, post=False),
+                 lambda: fwd(x, x, None, None, None, w, pre=False), lambda: fwd(x, x, None, None, None, w, w, rms=True),
+                 lambda: fwd(x, x, post=False, pre=False), lambda: fwd(x.double(), x.double()), lambda: bwd(x, x, x, None, stats),
+                 lambda: bwd(x, x, x, h, stats[:2]), lambda: bwd(x, x, x, h, stats.t()), lambda: bwd(x, x[:2], x, h, stats),
+                 lambda: bwd(x, x, x, h, stats, pre=False), lambda: bwd(x, x, x, h, stats, accumulate=True),
+                 lambda: bwd(x, x, x, h, stats, grad_weight=torch.ones(7, device="cuda")),
+                 lambda: bwd(x, x, x, h, stats, grad_weight=w.clone(), grad_bias=w.half()),
+                 lambda: bwd(x, x, x, h, stats, x, grad_gate=w.clone())):
+        with pytest.raises(ValueError):
+            call()
+    for kw in (dict(eps=-1.0), dict(alpha=float("nan")), dict(beta=float("inf"))):
+        with pytest.raises(L.LoptError):
+            fwd(x, x, **kw)
