@@ -580,6 +580,33 @@ lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, con
                                   int32_t id_bytes, const void* teacher, int64_t ldu, int32_t u_dtype, float temperature,
                                   const float* lse, void* dlogits, int64_t lddz, void* stream);
 
+/* Cross entropy of a linear layer's logits, without the logits in memory.  For each
+ * row of x (rows x cols), with the layer's weight w (vocab x cols), both of type dtype, and a target t:
+ *   z = x w^T,  lse = log sum_v exp(z_v),  loss = lse - z_t;
+ * a row whose target lies outside [0, vocab) (an id to ignore) has loss 0.  Products of 16-bit elements
+ * are exact and added in fp32.  targets: rows signed integers of id_bytes (4 or 8) bytes.  loss, lse: rows floats,
+ * NULL: not written.  At most 2^24 rows and 2^20 columns, and vocab / 256 * rows / 256 below 2^31. */
+lopt_status lopt_linear_ce_forward(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, const void* x, int64_t ldx,
+                                   const void* w, int64_t ldw, const void* targets, int32_t id_bytes, float* loss, float* lse,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace (256-byte aligned) that the forward and the backward call need.  The backward call's holds a piece of the
+ * logits' gradient at a time: 128 MiB or 1024 entries of the vocabulary, whichever is more.  Host only. */
+lopt_status lopt_linear_ce_forward_workspace(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, size_t* bytes);
+lopt_status lopt_linear_ce_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, size_t* bytes);
+
+/* Gradients of lopt_linear_ce_forward: with G = dloss (exp(z - lse) - onehot(t)), 0 for a row to ignore,
+ *   dx = G w,  dw = G^T x.
+ * G is rounded to type dtype (for fp16 scaled by a power of two first, so that its smallest steps are 2^-35 of the largest
+ * |dloss|); its sums are fp32.  A row to ignore is not read: whatever x holds there, its gradient is 0 and dw does not see it.
+ * dloss: one float a row, dloss_stride apart (0: one value for all rows).  lse: as lopt_linear_ce_forward wrote it.  dx: rows x
+ * cols of type dtype; dw: vocab x cols of type g_dtype, added to what is there if accumulate is not 0; NULL: not computed. */
+lopt_status lopt_linear_ce_backward(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, const float* dloss,
+                                    int64_t dloss_stride, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                    const void* targets, int32_t id_bytes, const float* lse, void* dx, int64_t lddx, void* dw,
+                                    int64_t lddw, int32_t g_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
 /* ---------------------------------------------------------------------------
  * AdamW over a list of tensors, beside the learned optimizer's step: decoupled
  * weight decay, moments in 32 bits or in 8.  The rules of the operators above

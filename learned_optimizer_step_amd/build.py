@@ -23,7 +23,8 @@ SOURCES = [("lopt_kernels.hip", []), ("lopt_apply.hip", ["-fno-honor-nans"]),
            ("lopt_single.hip", ["-fno-honor-nans"]), ("lopt_api.cpp", []), ("lopt_norm_forward.hip", []),
            ("lopt_norm_backward.hip", []), ("lopt_embedding.hip", []), ("lopt_distill.hip", []), ("lopt_ops_api.cpp", []),
            ("lopt_adamw.hip", []),
-           ("lopt_residual_norm_forward.hip", []), ("lopt_residual_norm_backward.hip", [])]
+           ("lopt_residual_norm_forward.hip", []), ("lopt_residual_norm_backward.hip", []),
+           ("lopt_linear_ce.hip", [])]
 ARCH = "gfx950"
 
 # Packed-fp32 VALU instructions are disabled for all device code.

@@ -48,6 +48,10 @@ struct Library {
   decltype(&lopt_embedding_backward) embedding_backward;
   decltype(&lopt_distill_forward) distill_forward;
   decltype(&lopt_distill_backward) distill_backward;
+  decltype(&lopt_linear_ce_forward_workspace) linear_ce_forward_workspace;
+  decltype(&lopt_linear_ce_forward) linear_ce_forward;
+  decltype(&lopt_linear_ce_backward_workspace) linear_ce_backward_workspace;
+  decltype(&lopt_linear_ce_backward) linear_ce_backward;
   decltype(&lopt_adamw_state_bytes) adamw_state_bytes;
   decltype(&lopt_adamw_step) adamw_step;
   decltype(&lopt_adamw_moments) adamw_moments;
@@ -72,6 +76,10 @@ void bind(uintptr_t handle) {
   find(l.embedding_backward, "lopt_embedding_backward");
   find(l.distill_forward, "lopt_distill_forward");
   find(l.distill_backward, "lopt_distill_backward");
+  find(l.linear_ce_forward_workspace, "lopt_linear_ce_forward_workspace");
+  find(l.linear_ce_forward, "lopt_linear_ce_forward");
+  find(l.linear_ce_backward_workspace, "lopt_linear_ce_backward_workspace");
+  find(l.linear_ce_backward, "lopt_linear_ce_backward");
   find(l.adamw_state_bytes, "lopt_adamw_state_bytes");
   find(l.adamw_step, "lopt_adamw_step");
   find(l.adamw_moments, "lopt_adamw_moments");
@@ -586,6 +594,83 @@ class Distill : public Function<Distill> {
 };
 
 // ---------------------------------------------------------------------------
+// cross entropy of a linear layer's logits
+
+struct Linear {
+  c10::Device device;
+  int32_t code, nb;
+  Matrix x, w;
+  Tensor targets;
+};
+
+Linear linear(const Tensor& x, const Tensor& weight, const Tensor& targets) {
+  const c10::Device device = gpu(x, "x");
+  on(device, weight, "weight");
+  on(device, targets, "targets");
+  const int32_t code = dtype_code(x.scalar_type(), "x"), nb = id_bytes(targets, "targets");
+  if (x.dim() == 0 || targets.sizes() != x.sizes().slice(0, x.dim() - 1)) bad("targets must have the shape of x but for the last dimension");
+  if (weight.dim() != 2 || weight.size(1) != x.size(-1)) bad("weight must have two dimensions, the second of x's last size");
+  if (weight.scalar_type() != x.scalar_type()) bad("weight must have the type of x");
+  if (weight.size(0) == 0) bad("weight: no entries");
+  return {device, code, nb, matrix(x, "x"), matrix(weight, "weight"), targets.contiguous()};
+}
+
+std::tuple<Tensor, Tensor> linear_ce_forward(const Tensor& x, const Tensor& weight, const Tensor& targets) {
+  const Linear l = linear(x, weight, targets);
+  const c10::DeviceGuard guard(l.device);
+  Tensor loss = empty(targets.sizes(), at::kFloat, l.device), lse = empty(targets.sizes(), at::kFloat, l.device);
+  size_t bytes = 0;
+  check(lib.linear_ce_forward_workspace(l.x.rows, l.x.cols, l.w.rows, l.code, &bytes));
+  const Tensor ws = empty({int64_t(bytes)}, at::kByte, l.device);
+  check(lib.linear_ce_forward(l.x.rows, l.x.cols, l.w.rows, l.code, l.x.data(), l.x.ld, l.w.data(), l.w.ld, l.targets.data_ptr(), l.nb,
+                              static_cast<float*>(loss.data_ptr()), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), bytes,
+                              stream(l.device)));
+  return {loss, lse};
+}
+
+std::tuple<Tensor, Tensor> linear_ce_backward(const Tensor& grad_loss, const Tensor& x, const Tensor& weight, const Tensor& targets,
+                                              const Tensor& lse, const Maybe& to, bool accumulate, bool need_x, bool need_weight,
+                                              std::optional<at::ScalarType> grad_dtype) {
+  const Linear l = linear(x, weight, targets);
+  for (const auto& [t, name] : {std::pair<const Tensor*, const char*>{&grad_loss, "grad_loss"}, {&lse, "lse"}}) {
+    on(l.device, *t, name);
+    if (t->scalar_type() != at::kFloat || t->sizes() != targets.sizes()) bad(std::string(name) + " must be float32, one value a token");
+  }
+  if (accumulate && need_weight && !to) bad("accumulate needs a buffer to add to");
+  const c10::DeviceGuard guard(l.device);
+  Tensor dx, dw;
+  if (need_x) dx = empty(x.sizes(), x.scalar_type(), l.device);
+  if (need_weight) dw = output(to, {l.w.rows, l.w.cols}, l.device, grad_dtype.value_or(weight.scalar_type()), "grad_weight");
+  Tensor g = grad_loss.dim() == 1 ? grad_loss : grad_loss.reshape({-1});
+  if (g.numel() > 1 && g.stride(0) >= (int64_t(1) << 28)) g = g.contiguous();
+  const int64_t step = g.numel() > 1 ? g.stride(0) : 0;   // a single element's stride can be anything
+  const Tensor s = lse.contiguous();
+  size_t bytes = 0;
+  check(lib.linear_ce_backward_workspace(l.x.rows, l.x.cols, l.w.rows, l.code, &bytes));
+  const Tensor ws = empty({int64_t(bytes)}, at::kByte, l.device);
+  check(lib.linear_ce_backward(l.x.rows, l.x.cols, l.w.rows, l.code, static_cast<const float*>(g.data_ptr()), step, l.x.data(), l.x.ld,
+                               l.w.data(), l.w.ld, l.targets.data_ptr(), l.nb, static_cast<const float*>(s.data_ptr()), ptr(dx), l.x.cols,
+                               ptr(dw), l.w.cols, dw.defined() ? dtype_code(dw.scalar_type(), "grad_weight") : LOPT_F32, accumulate,
+                               ws.data_ptr(), bytes, stream(l.device)));
+  return {dx, dw};
+}
+
+class LinearCe : public Function<LinearCe> {
+ public:
+  static Tensor forward(AutogradContext* ctx, const Tensor& x, const Tensor& weight, const Tensor& targets) {
+    auto [loss, lse] = linear_ce_forward(x, weight, targets);
+    ctx->save_for_backward({x, weight, targets, lse});
+    return loss;
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const variable_list s = ctx->get_saved_variables();
+    auto [dx, dw] = linear_ce_backward(grads[0], s[0], s[1], s[2], s[3], std::nullopt, false, ctx->needs_input_grad(0), ctx->needs_input_grad(1),
+                                       std::nullopt);
+    return differentiable_once({dx, dw, Tensor()});
+  }
+};
+
+// ---------------------------------------------------------------------------
 // AdamW
 
 at::ScalarType moment_type(int64_t bits) { return bits == 8 ? at::kByte : at::kFloat; }
@@ -729,6 +814,13 @@ PYBIND11_MODULE(_layers, m) {
   m.def("embedding", [](const Tensor& ids, const Tensor& w, double scale, int64_t row0, const py::object& dtype) {
     return Embedding::apply(ids, w, scale, row0, scalar_type(dtype));
   });
+  m.def("linear_ce_forward", &linear_ce_forward);
+  m.def("linear_ce_backward", [](const Tensor& g, const Tensor& x, const Tensor& w, const Tensor& targets, const Tensor& lse, const Maybe& to,
+                                 bool accumulate, bool need_x, bool need_weight, const py::object& dtype) {
+    auto [dx, dw] = linear_ce_backward(g, x, w, targets, lse, to, accumulate, need_x, need_weight, scalar_type(dtype));
+    return std::make_tuple(need_x ? Maybe(dx) : Maybe(), need_weight ? Maybe(dw) : Maybe());
+  });
+  m.def("linear_ce", [](const Tensor& x, const Tensor& w, const Tensor& targets) { return LinearCe::apply(x, w, targets); });
   m.def("adamw_state", &adamw_state);
   m.def("adamw_step", &adamw_step);
   m.def("adamw_moments", [](const Tensor& state, int64_t n, int64_t bits, const py::object& dtype) {

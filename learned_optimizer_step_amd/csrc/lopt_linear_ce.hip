@@ -1,0 +1,771 @@
+// Cross entropy of a linear layer's logits, which are never kept.  With x (N
+// tokens of D), the weight w (V x D), z = x w^T and a target t per token:
+//   lse = log sum_v exp(z_v),  loss = lse - z_t
+//   G = g (exp(z - lse) - onehot(t)),  dx = G w,  dw = G^T x
+// Forward: one product whose tiles end in the running maximum and sum of their
+// part of the vocabulary.  Backward: the vocabulary in pieces; of each, the
+// product again, its tiles ending in G, which is kept for the piece alone, and
+// from it the piece's share of dx and its rows of dw.  Bound by the matrix
+// units: 2 N V D operations forward, 6 N V D backward.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "lopt_ops.h"
+#include "lopt_ops_device.h"
+
+namespace lopt {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// ---------------------------------------------------------------------------
+// The product C[m][n] = sum_k A[m][k] B[n][k] of a block: 256 x 256 of C, 8
+// waves of 128 x 64 each as 4 x 2 matrix instructions of 32 x 32.  Operands
+// go to LDS in stages of 128 bytes of k, straight from memory, one stage ahead.
+// An operand may lie with k contiguous ("rows") or with m or n contiguous
+// ("columns", a transposed read from LDS): no operand is ever transposed in memory.
+constexpr int kTile = 256, kThreads = 512, kStageBytes = 2 * kTile * 128;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+#define LDS_PTR(T, p) ((__attribute__((address_space(3))) T*)(p))
+#define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(p))
+
+template <class T>
+__device__ __forceinline__ void multiply(f32x16& c, u32x4 a, u32x4 b) {
+  if constexpr (std::is_same_v<T, bf16>) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else if constexpr (std::is_same_v<T, f16>) {
+    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  } else {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
+  }
+}
+
+struct Operand {
+  const char* p;
+  int64_t ld;     // bytes from a row to the next (rows), from one k to the next (columns)
+  int64_t last;   // the last row, or the last k, that there is: those behind it read it again
+  int64_t edge;   // columns: the byte in a k where the last 16 begin
+};
+
+// One operand's share of a stage: 32 loads of a wave, 4 for each of the 8 waves.
+template <class T, bool COLUMNS>
+struct Loader {
+  static constexpr int S = sizeof(T), kStep = 128 / S;
+  const char* p[4];
+  int64_t ld, last;
+  int kr[4];
+
+  __device__ __forceinline__ void begin(const Operand& o, int64_t tile0, int64_t k0, int wave, int lane) {
+    ld = o.ld;
+    last = o.last;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int q = wave * 4 + i;
+      if constexpr (!COLUMNS) {
+        // 8 rows of 128 bytes; 16-byte piece c of row r lies in place c ^ (r / 2 % 8), so that a read of 16 rows at one k meets every bank once
+        const int r = q * 8 + lane / 8, c = (lane % 8) ^ (r / 2 % 8);
+        p[i] = o.p + min(tile0 + r, last) * ld + k0 * S + c * 16;
+      } else {
+        constexpr int PER = kTile * S / 16;   // 16-byte pieces of a k
+        kr[i] = q * (64 / PER) + lane / PER;
+        // 16-bit: the 64-byte groups of the four k that one transposed read takes lie in different banks
+        const int c = (lane % PER) ^ (S == 2 ? (kr[i] & 3) << 2 : 0);
+        p[i] = o.p + min(tile0 * S + c * 16, o.edge);
+      }
+    }
+  }
+  // The stage at k0 into `to`; rows: k0 is the next one each time.
+  __device__ __forceinline__ void load(char* to, int64_t k0, int wave) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const char* from = p[i];
+      if constexpr (COLUMNS) from += min(k0 + kr[i], last) * ld;
+      else p[i] += 128;
+      __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from), LDS_PTR(void, to + (wave * 4 + i) * 1024), 16, 0, 0);
+    }
+  }
+};
+
+// 32 rows (m or n, from row0) at the j-th quarter of a stage, as the matrix
+// instructions take them: lane l has row l % 32 and the k of half l / 32.
+template <class T, bool COLUMNS>
+__device__ __forceinline__ u32x4 fragment(const char* s, int row0, int j, int lane) {
+  const int l = lane % 32, h = lane / 32;
+  if constexpr (!COLUMNS) {
+    return *reinterpret_cast<const u32x4*>(s + (row0 + l) * 128 + (((2 * j + h) ^ (l / 2 % 8)) * 16));
+  } else if constexpr (sizeof(T) == 2) {
+    const int g = lane / 16, i = lane % 16;
+    const char* at = s + (16 * j + 8 * h + i / 4) * 512 + ((((row0 / 32) ^ (i / 4)) * 4 + (g & 1) * 2 + (i & 3) / 2) * 16 + (i & 1) * 8);
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at + 4 * 512));
+    return __builtin_bit_cast(u32x4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(s + (8 * j + 4 * h) * 1024 + (row0 + l) * 4);
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = at[e * 256];
+    return v;
+  }
+}
+
+// acc += the block's product over `steps` stages from k0.  Everything that was read is read when it returns.
+template <class T, bool AC, bool BC>
+__device__ __forceinline__ void product(f32x16 (&acc)[4][2], const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k0,
+                                        int64_t steps, char* lds) {
+  constexpr int kStep = 128 / int(sizeof(T));
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = wave % 2, wn = wave / 2;
+  Loader<T, AC> la;
+  Loader<T, BC> lb;
+  la.begin(a, m0, k0, wave, lane);
+  lb.begin(b, n0, k0, wave, lane);
+  if (steps > 0) {
+    la.load(lds, k0, wave);
+    lb.load(lds + kStageBytes / 2, k0, wave);
+  }
+  for (int64_t s = 0; s < steps; ++s) {
+    const char* now = lds + (s & 1) * kStageBytes;
+    char* next = lds + (~s & 1) * kStageBytes;
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the stage is there
+    __syncthreads();                      // everyone's is, and the stage before is read
+    if (s + 1 < steps) {
+      la.load(next, k0 + (s + 1) * kStep, wave);
+      lb.load(next + kStageBytes / 2, k0 + (s + 1) * kStep, wave);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      u32x4 fa[4], fb[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fa[i] = fragment<T, AC>(now, wm * 128 + i * 32, j, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) fb[i] = fragment<T, BC>(now + kStageBytes / 2, wn * 64 + i * 32, j, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) multiply<T>(acc[i][k], fa[i], fb[k]);
+    }
+  }
+  __syncthreads();
+}
+
+// Element e of acc[i][k] is C[m][n] with these, from the block's first.
+__device__ __forceinline__ int tile_m(int i, int e) {
+  const int wave = threadIdx.x >> 6, h = (threadIdx.x & 63) / 32;
+  return (wave % 2) * 128 + i * 32 + 8 * (e / 4) + 4 * h + e % 4;
+}
+__device__ __forceinline__ int tile_n(int k) {
+  const int wave = threadIdx.x >> 6;
+  return (wave / 2) * 64 + k * 32 + threadIdx.x % 32;
+}
+
+__device__ __forceinline__ void clear(f32x16 (&acc)[4][2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
+}
+
+// A block's tile.  Blocks go to the eight dies in turn, each with a cache of its
+// own: a die gets neighbours, 8 tiles of m by a run of n at a time.
+struct Place {
+  int64_t m, n;
+};
+__device__ __forceinline__ Place place(uint32_t id, uint32_t mt, uint32_t nt) {
+  const uint32_t total = mt * nt, per = total / 8, rest = total % 8, die = id % 8;
+  id = die * per + min(die, rest) + id / 8;
+  const uint32_t group = id / (8 * nt), first = group * 8, rows = min(8u, mt - first), in = id - group * 8 * nt;
+  return {first + in % rows, in / rows};
+}
+
+// What the backward pass keeps on the device: tokens with a target (the others
+// have no gradient), and the power of two that G is scaled by.
+struct Header {
+  int32_t n;
+  float scale, inv_scale;
+};
+
+// A token of those with a target.
+struct Row {
+  float lse;      // of its logits, times log2(e)
+  float g;        // its gradient, scaled
+  int32_t target;
+  int32_t from;   // its row of x
+};
+
+__device__ __forceinline__ int64_t load_id(const void* ids, int32_t bytes, int64_t i) {
+  return bytes == 8 ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
+}
+
+// ---------------------------------------------------------------------------
+// Forward
+
+struct Stats {
+  Operand w, x;
+  const void* targets;
+  float2* part;    // [vocabulary tile][np]: largest logit, and the sum of exp of the rest
+  float* hit;      // the target's logit
+  int64_t v0, vend, n, np, steps;
+  uint32_t mt, nt;
+  int32_t id_bytes;
+};
+
+template <class T>
+__global__ __launch_bounds__(kThreads, 2) void k_ce_stats(Stats a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+  const Place t = place(blockIdx.x, a.mt, a.nt);
+  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
+  f32x16 acc[4][2];
+  clear(acc);
+  product<T, false, false>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
+  const int64_t v0 = a.v0 + m0;
+  if (v0 + kTile > a.vend) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (v0 + tile_m(i, e) >= a.vend) acc[i][0][e] = acc[i][1][e] = -INFINITY;
+  }
+  float2* red = reinterpret_cast<float2*>(lds);   // [2][256]
+  const int wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t tok = n0 + tile_n(k);
+    const int64_t at = tok < a.n ? load_id(a.targets, a.id_bytes, tok) - v0 : -1;
+    const bool here = at >= 0 && at < kTile && v0 + at < a.vend;
+    if (__ballot(here)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (here && at == tile_m(i, e)) a.hit[tok] = acc[i][k][e];
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][k][e]);
+    const Two both = swap32(m);
+    m = fmaxf(both.a, both.b);
+    const float mc = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s += exp2_hw((acc[i][k][e] - mc) * kLog2e);
+    const Two sums = swap32(s);
+    s = sums.a + sums.b;
+    if ((threadIdx.x & 63) < 32) red[(wave % 2) * kTile + tile_n(k)] = make_float2(m, s);
+  }
+  __syncthreads();
+  if (threadIdx.x < kTile && n0 + threadIdx.x < a.n) {
+    const float2 x = red[threadIdx.x], y = red[kTile + threadIdx.x];
+    const float m = fmaxf(x.x, y.x), mc = m == -INFINITY ? 0.f : m;
+    const float s = x.y * exp2_hw((x.x - mc) * kLog2e) + y.y * exp2_hw((y.x - mc) * kLog2e);
+    a.part[(v0 / kTile) * a.np + n0 + threadIdx.x] = make_float2(m, s);
+  }
+}
+
+// Per token, the tiles' maxima and sums in their order: 64 tokens a block, 4 threads a token.
+__global__ __launch_bounds__(256) void k_ce_loss(const float2* part, int64_t tiles, int64_t np, int64_t n, int64_t vocab, const void* targets,
+                                                 int32_t id_bytes, const float* hit, float* loss, float* lse) {
+  __shared__ float2 red[4][64];
+  const int64_t tok = int64_t(blockIdx.x) * 64 + threadIdx.x % 64;
+  const int q = threadIdx.x / 64;
+  float m = -INFINITY, s = 0.f;
+  if (tok < n) {
+    for (int64_t t = q; t < tiles; t += 4) m = fmaxf(m, part[t * np + tok].x);
+    const float mc = m == -INFINITY ? 0.f : m;
+    for (int64_t t = q; t < tiles; t += 4) {
+      const float2 x = part[t * np + tok];
+      s = fmaf(x.y, exp2_hw((x.x - mc) * kLog2e), s);
+    }
+  }
+  red[q][threadIdx.x % 64] = make_float2(m, s);
+  __syncthreads();
+  if (q || tok >= n) return;
+  m = fmaxf(fmaxf(red[0][threadIdx.x].x, red[1][threadIdx.x].x), fmaxf(red[2][threadIdx.x].x, red[3][threadIdx.x].x));
+  const float mc = m == -INFINITY ? 0.f : m;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) s = fmaf(red[k][threadIdx.x].y, exp2_hw((red[k][threadIdx.x].x - mc) * kLog2e), s);
+  const float log_s = kLn2 * log2f(s);
+  if (lse) lse[tok] = m + log_s;
+  if (loss) {
+    const int64_t t = load_id(targets, id_bytes, tok);
+    loss[tok] = t >= 0 && t < vocab ? (m - hit[tok]) + log_s : 0.f;   // small terms, whatever the logits' common offset is
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Rows laid out for the product: 16-byte aligned, filled up with zeros to whole stages of k.
+
+template <class T>
+__global__ __launch_bounds__(256) void k_ce_pack(const T* from, int64_t ld, int64_t rows, int64_t cols, T* to, int64_t dp) {
+  constexpr int V = kVec<T>;
+  const int64_t per = dp / V, all = rows * per;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / per, c = (i - r * per) * V;
+    reinterpret_cast<Pack<T, V>*>(to + r * dp + c)[0] = load_pack<T, V>(from + r * ld, c, cols);
+  }
+}
+
+// The tokens with a target, in their order: rows[k] of the k-th, pos[r] its k (-1: none); the scale of G.  One block.
+__global__ __launch_bounds__(1024) void k_ce_rows(int64_t n, int64_t vocab, const void* targets, int32_t id_bytes, const float* g, int64_t g_stride,
+                                                  const float* lse, int32_t scaled, Header* head, Row* rows, int32_t* pos) {
+  __shared__ int32_t count[16];
+  __shared__ float most[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float scale = 1.f;
+  if (scaled) {   // |G| up to 2^11: fp16's smallest steps are then 2^-35 of the largest gradient
+    float top = 0.f;
+    for (int64_t r = threadIdx.x; r < n; r += 1024) {
+      const int64_t t = load_id(targets, id_bytes, r);
+      const float x = fabsf(g[r * g_stride]);
+      if (t >= 0 && t < vocab && x < INFINITY) top = fmaxf(top, x);
+    }
+    top = lanes_reduce<64>(top, Max());
+    if (lane == 0) most[wave] = top;
+    __syncthreads();
+    for (int k = 0; k < 16; ++k) top = fmaxf(top, most[k]);
+    const int e = int(__float_as_uint(top) >> 23) - 127;   // floor of the logarithm, of normal numbers
+    const int k = 10 - e;
+    if (top > 0.f) scale = __builtin_ldexpf(1.f, k < -126 ? -126 : k > 126 ? 126 : k);
+  }
+  int32_t before = 0;
+  for (int64_t r0 = 0; r0 < n; r0 += 1024) {
+    const int64_t r = r0 + threadIdx.x;
+    const int64_t t = r < n ? load_id(targets, id_bytes, r) : -1;
+    const bool there = t >= 0 && t < vocab;
+    const uint64_t mask = __ballot(there);
+    const int32_t mine = __popcll(mask & ((1ull << lane) - 1));
+    if (lane == 0) count[wave] = __popcll(mask);
+    __syncthreads();
+    int32_t at = before, all = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k < wave) at += count[k];
+      all += count[k];
+    }
+    if (there) rows[at + mine] = {lse[r] * kLog2e, g[r * g_stride] * scale, int32_t(t), int32_t(r)};
+    if (r < n) pos[r] = there ? at + mine : -1;
+    before += all;
+    __syncthreads();   // count is written again
+  }
+  if (threadIdx.x == 0) *head = {before, scale, 1.f / scale};
+}
+
+// The rows of x of those tokens, and zeros up to a whole tile.
+template <class T>
+__global__ __launch_bounds__(256) void k_ce_gather(const T* x, int64_t ldx, int64_t cols, const Header* head, Row* rows, T* to, int64_t dp) {
+  constexpr int V = kVec<T>;
+  const int64_t n = head->n, all_rows = (n + kTile - 1) / kTile * kTile, per = dp / V, all = all_rows * per;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / per, c = (i - r * per) * V;
+    Pack<T, V> p;
+    if (r < n) {
+      p = load_pack<T, V>(x + rows[r].from * ldx, c, cols);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) p.v[k] = T(0.f);
+      if (c == 0) rows[r] = {0.f, 0.f, -1, -1};
+    }
+    reinterpret_cast<Pack<T, V>*>(to + r * dp + c)[0] = p;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward
+
+struct Grad {
+  Operand w, x;
+  const Header* head;
+  const Row* rows;
+  void* out;       // G of the piece: [tokens][width]
+  int64_t v0, vend, width, steps;
+  uint32_t mt, nt;
+};
+
+template <class T>
+__global__ __launch_bounds__(kThreads, 2) void k_ce_grad(Grad a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+  const Place t = place(blockIdx.x, a.mt, a.nt);
+  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
+  if (n0 >= a.head->n) return;
+  f32x16 acc[4][2];
+  clear(acc);
+  product<T, false, false>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
+  const int64_t v0 = a.v0 + m0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t tok = n0 + tile_n(k);
+    const Row r = a.rows[tok];
+    const int64_t target = r.target - v0;
+    T* out = static_cast<T*>(a.out) + tok * a.width + m0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int m = tile_m(i, e);
+        Pack<T, 4> p;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          // a probability is at most 1, whatever half a step of a large lse is (NaN stays NaN)
+          const float x = exp2_hw(__builtin_elementwise_minimum(fmaf(acc[i][k][e + q], kLog2e, -r.lse), 0.f));
+          p.v[q] = from_f32<T>(v0 + m + q < a.vend ? r.g * (x - (target == m + q ? 1.f : 0.f)) : 0.f);
+        }
+        *reinterpret_cast<Pack<T, 4>*>(out + m) = p;
+      }
+  }
+}
+
+// A product's tiles as fp32 sums: C[m][n] at out[split][n][m].
+struct Sums {
+  Operand a, b;
+  const Header* head;
+  float* out;
+  int64_t ldo, pitch;        // of a row n, of a split
+  int64_t k;                 // the whole sum's length; unused where it goes over the tokens
+  uint32_t mt, nt;
+  int32_t splits, add;       // add: to what the piece before left
+};
+
+// Splits share the stages of k; the first ones take one more where they do not divide.
+__device__ __forceinline__ void share(int64_t steps, int32_t splits, int64_t z, int64_t& first, int64_t& count) {
+  const int64_t per = steps / splits, rest = steps % splits;
+  first = z * per + min(z, rest);
+  count = per + (z < rest ? 1 : 0);
+}
+
+template <class T, bool BC>
+__global__ __launch_bounds__(kThreads, 2) void k_ce_sums(Sums a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+  constexpr int kStep = 128 / int(sizeof(T));
+  const int64_t n = a.head->n;
+  const uint32_t tiles = a.mt * a.nt, z = blockIdx.x / tiles;
+  const Place t = place(blockIdx.x - z * tiles, a.mt, a.nt);
+  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
+  if (!BC && n0 >= n) return;   // n: tokens
+  int64_t first, count;
+  share(((BC ? n : a.k) + kStep - 1) / kStep, a.splits, z, first, count);
+  f32x16 acc[4][2];
+  clear(acc);
+  product<T, true, BC>(acc, a.a, a.b, m0, n0, first * kStep, count, lds);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float* out = a.out + z * a.pitch + (n0 + tile_n(k)) * a.ldo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int64_t m = m0 + tile_m(i, e);
+        if (m >= a.ldo) continue;
+        f32x4 v = {acc[i][k][e], acc[i][k][e + 1], acc[i][k][e + 2], acc[i][k][e + 3]};
+        f32x4* to = reinterpret_cast<f32x4*>(out + m);
+        if (a.add) v += *to;
+        *to = v;
+      }
+  }
+}
+
+// dw of the piece's rows, from the whole sum over the tokens.
+struct WeightGrad {
+  Operand a, b;
+  const Header* head;
+  void* out;        // row 0 of the piece
+  int64_t ldo, rows, cols;
+  uint32_t mt, nt;
+  int32_t dtype, accumulate;
+};
+
+template <class T>
+__global__ __launch_bounds__(kThreads, 2) void k_ce_weight(WeightGrad a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+  constexpr int kStep = 128 / int(sizeof(T));
+  const Place t = place(blockIdx.x, a.mt, a.nt);
+  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
+  f32x16 acc[4][2];
+  clear(acc);
+  product<T, true, true>(acc, a.a, a.b, m0, n0, 0, (int64_t(a.head->n) + kStep - 1) / kStep, lds);
+  const float inv = a.head->inv_scale;
+  const auto write = [&](auto type) {
+    using W = decltype(type);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t r = n0 + tile_n(k);
+      if (r >= a.rows) continue;
+      W* out = static_cast<W*>(a.out) + r * a.ldo;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const int64_t m = m0 + tile_m(i, e);
+          if (m >= a.cols) continue;
+          Pack<W, 4> p;
+          if (a.accumulate) p = load_pack<W, 4>(out, m, a.cols);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) p.v[q] = from_f32<W>((a.accumulate ? to_f32(p.v[q]) : 0.f) + inv * acc[i][k][e + q]);
+          store_pack<W, 4>(out, m, a.cols, p);
+        }
+    }
+  };
+  if (a.dtype == kF32) write(float());
+  else if (a.dtype == kBF16) write(bf16());
+  else write(f16());
+}
+
+// Rows of fp32 sums, their splits added in order: dx (pos: the token's row of the sums, -1: zeros) or, without pos, dw.
+__global__ __launch_bounds__(256) void k_ce_join(const float* sums, int64_t ld, int64_t pitch, int32_t splits, const Header* head, const int32_t* pos,
+                                                 int64_t rows, int64_t cols, void* out, int64_t ldo, int32_t dtype, int32_t accumulate) {
+  const float inv = head->inv_scale;
+  const int64_t per = (cols + 3) / 4, all = rows * per;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / per, c = (i - r * per) * 4, from = pos ? pos[r] : r;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (from >= 0)
+      for (int32_t z = 0; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(sums + z * pitch + from * ld + c);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k < cols) store_any(out, dtype, r * ldo + c + k, (accumulate ? load_any(out, dtype, r * ldo + c + k) : 0.f) + inv * v[k]);
+  }
+}
+
+// A matrix of zeros: the gradient of a weight without tokens.
+__global__ __launch_bounds__(256) void k_ce_zero(void* out, int64_t ldo, int64_t rows, int64_t cols, int32_t dtype) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * cols; i += int64_t(gridDim.x) * 256) store_any(out, dtype, i / cols * ldo + i % cols, 0.f);
+}
+
+template <class F>
+hipError_t with_type(int32_t dtype, F&& f) {
+  if (dtype == kF32) return f(float());
+  if (dtype == kBF16) return f(bf16());
+  return f(f16());
+}
+
+int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+int64_t size_of(int32_t dtype) { return dtype == kF32 ? 4 : 2; }
+
+// Where things lie in the workspace.
+struct Plan {
+  int64_t s, np, dp, mt_all;     // element bytes; tokens and columns filled up; tiles of the vocabulary
+  int64_t width;                 // of a piece of the vocabulary
+  int32_t splits_x, splits_w;
+  int64_t bytes = 0;
+  int64_t take(int64_t n) {
+    const int64_t at = bytes;
+    bytes += up(n, 1024);
+    return at;
+  }
+  int64_t part, hit, x, w, head, rows, pos, g, sum_x, sum_w;
+};
+
+constexpr int64_t kPieceBytes = int64_t(128) << 20;   // of G, or of a piece of the weight that is laid out anew
+
+Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) {
+  Plan p{};
+  p.s = size_of(dtype);
+  p.np = up(n, kTile);
+  p.dp = up(cols, 128 / p.s);
+  p.mt_all = up(vocab, kTile) / kTile;
+  const int64_t all = up(vocab, kTile);
+  const int64_t most = std::max(backward ? p.np : 0, p.dp) * p.s;
+  p.width = std::min(all, std::max<int64_t>(kPieceBytes / most / kTile, 4) * kTile);
+  p.x = p.take(p.np * p.dp * p.s);
+  p.w = p.take(p.width * p.dp * p.s);
+  if (!backward) {
+    p.part = p.take(p.mt_all * p.np * 8);
+    p.hit = p.take(n * 4);
+    return p;
+  }
+  p.head = p.take(sizeof(Header));
+  p.rows = p.take(p.np * int64_t(sizeof(Row)));
+  p.pos = p.take(n * 4);
+  p.g = p.take(p.np * p.width * p.s);
+  // enough blocks for the chip where a product has few tiles
+  const int64_t mt = up(p.dp, kTile) / kTile;
+  const auto splits = [&](int64_t tiles, int64_t steps) { return int32_t(std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 8))); };
+  p.splits_x = splits(mt * (p.np / kTile), p.width * p.s / 128);
+  p.splits_w = splits(mt * (p.width / kTile), p.np * p.s / 128);
+  p.sum_x = p.take(p.splits_x * p.np * p.dp * 4);
+  p.sum_w = p.splits_w > 1 ? p.take(p.splits_w * p.width * p.dp * 4) : 0;
+  return p;
+}
+
+bool direct(const void* p, int64_t ld, int64_t cols, int64_t s) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * s % 16 == 0 && cols * s % 128 == 0;
+}
+
+template <class T>
+void pack(const void* from, int64_t ld, int64_t rows, int64_t cols, void* to, int64_t dp, hipStream_t s) {
+  const int64_t blocks = (rows * (dp / kVec<T>) + 255) / 256;
+  k_ce_pack<T><<<dim3(unsigned(std::min<int64_t>(blocks, 8192))), dim3(256), 0, s>>>(static_cast<const T*>(from), ld, rows, cols, static_cast<T*>(to), dp);
+}
+
+template <class T>
+hipError_t forward(const LinearCeForward& a, hipStream_t s) {
+  const Plan p = plan(a.rows, a.vocab, a.cols, a.dtype, false);
+  unsigned char* ws = a.ws;
+  Stats g{};
+  g.steps = p.dp * p.s / 128;
+  g.n = a.rows;
+  g.np = p.np;
+  g.nt = p.np / kTile;
+  g.targets = a.targets;
+  g.id_bytes = a.id_bytes;
+  g.part = reinterpret_cast<float2*>(ws + p.part);
+  g.hit = reinterpret_cast<float*>(ws + p.hit);
+  if (direct(a.x, a.ldx, a.cols, p.s)) {
+    g.x = {static_cast<const char*>(a.x), a.ldx * p.s, a.rows - 1, 0};
+  } else {
+    pack<T>(a.x, a.ldx, a.rows, a.cols, ws + p.x, p.dp, s);
+    g.x = {reinterpret_cast<const char*>(ws + p.x), p.dp * p.s, a.rows - 1, 0};
+  }
+  const bool whole = direct(a.w, a.ldw, a.cols, p.s);
+  const int64_t width = whole ? a.vocab : p.width;
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += width) {
+    const int64_t rows = std::min(width, a.vocab - v0);
+    const char* w = static_cast<const char*>(a.w) + v0 * a.ldw * p.s;
+    if (whole) {
+      g.w = {w, a.ldw * p.s, rows - 1, 0};
+    } else {
+      pack<T>(w, a.ldw, rows, a.cols, ws + p.w, p.dp, s);
+      g.w = {reinterpret_cast<const char*>(ws + p.w), p.dp * p.s, rows - 1, 0};
+    }
+    g.v0 = v0;
+    g.vend = v0 + rows;
+    g.mt = (rows + kTile - 1) / kTile;
+    k_ce_stats<T><<<dim3(unsigned(g.mt * g.nt)), dim3(kThreads), 0, s>>>(g);
+  }
+  k_ce_loss<<<dim3(unsigned((a.rows + 63) / 64)), dim3(256), 0, s>>>(g.part, p.mt_all, p.np, a.rows, a.vocab, a.targets, a.id_bytes, g.hit, a.loss, a.lse);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
+  const Plan p = plan(a.rows, a.vocab, a.cols, a.dtype, true);
+  unsigned char* ws = a.ws;
+  Header* head = reinterpret_cast<Header*>(ws + p.head);
+  Row* rows = reinterpret_cast<Row*>(ws + p.rows);
+  int32_t* pos = reinterpret_cast<int32_t*>(ws + p.pos);
+  T* x = reinterpret_cast<T*>(ws + p.x);
+  k_ce_rows<<<dim3(1), dim3(1024), 0, s>>>(a.rows, a.vocab, a.targets, a.id_bytes, a.dloss, a.lddl, a.lse, a.dtype == kF16, head, rows, pos);
+  const int64_t blocks = (p.np * (p.dp / kVec<T>) + 255) / 256;
+  k_ce_gather<T><<<dim3(unsigned(std::min<int64_t>(blocks, 8192))), dim3(256), 0, s>>>(static_cast<const T*>(a.x), a.ldx, a.cols, head, rows, x, p.dp);
+  const Operand xr{reinterpret_cast<const char*>(x), p.dp * p.s, p.np - 1, 0}, xc{xr.p, xr.ld, p.np - 1, p.dp * p.s - 16};
+  const bool whole = direct(a.w, a.ldw, a.cols, p.s);
+  const int64_t mt = up(p.dp, kTile) / kTile, nt = p.np / kTile;
+  float* sum_x = reinterpret_cast<float*>(ws + p.sum_x);
+  float* sum_w = reinterpret_cast<float*>(ws + p.sum_w);
+  char* G = reinterpret_cast<char*>(ws + p.g);
+  for (int64_t v0 = 0; v0 < a.vocab; v0 += p.width) {
+    const int64_t n = std::min(p.width, a.vocab - v0), tiles = (n + kTile - 1) / kTile;
+    const char* w = static_cast<const char*>(a.w) + v0 * a.ldw * p.s;
+    int64_t ldw = a.ldw * p.s;
+    if (!whole) {
+      pack<T>(w, a.ldw, n, a.cols, ws + p.w, p.dp, s);
+      w = reinterpret_cast<const char*>(ws + p.w);
+      ldw = p.dp * p.s;
+    }
+    Grad g{};
+    g.w = {w, ldw, n - 1, 0};
+    g.x = xr;
+    g.head = head;
+    g.rows = rows;
+    g.out = G;
+    g.v0 = v0;
+    g.vend = v0 + n;
+    g.width = p.width;
+    g.steps = p.dp * p.s / 128;
+    g.mt = tiles;
+    g.nt = nt;
+    k_ce_grad<T><<<dim3(unsigned(g.mt * g.nt)), dim3(kThreads), 0, s>>>(g);
+    if (a.dx) {
+      Sums q{};
+      q.a = {w, ldw, n - 1, p.dp * p.s - 16};
+      q.b = {G, p.width * p.s, p.np - 1, 0};
+      q.head = head;
+      q.out = sum_x;
+      q.ldo = p.dp;
+      q.pitch = p.np * p.dp;
+      q.k = tiles * kTile;
+      q.mt = mt;
+      q.nt = nt;
+      q.splits = p.splits_x;
+      q.add = v0 > 0;
+      k_ce_sums<T, false><<<dim3(unsigned(mt * nt * q.splits)), dim3(kThreads), 0, s>>>(q);
+    }
+    if (a.dw) {
+      const Operand gc{G, p.width * p.s, p.np - 1, p.width * p.s - 16};
+      char* out = static_cast<char*>(a.dw) + v0 * a.lddw * size_of(a.gdtype);
+      if (p.splits_w > 1) {
+        Sums q{};
+        q.a = xc;
+        q.b = gc;
+        q.head = head;
+        q.out = sum_w;
+        q.ldo = p.dp;
+        q.pitch = p.width * p.dp;
+        q.mt = mt;
+        q.nt = tiles;
+        q.splits = p.splits_w;
+        k_ce_sums<T, true><<<dim3(unsigned(mt * tiles * q.splits)), dim3(kThreads), 0, s>>>(q);
+        const int64_t work = (n * ((a.cols + 3) / 4) + 255) / 256;
+        k_ce_join<<<dim3(unsigned(std::min<int64_t>(work, 8192))), dim3(256), 0, s>>>(sum_w, p.dp, q.pitch, p.splits_w, head, nullptr, n, a.cols, out, a.lddw,
+                                                                                    a.gdtype, a.accumulate);
+      } else {
+        WeightGrad q{};
+        q.a = xc;
+        q.b = gc;
+        q.head = head;
+        q.out = out;
+        q.ldo = a.lddw;
+        q.rows = n;
+        q.cols = a.cols;
+        q.mt = mt;
+        q.nt = tiles;
+        q.dtype = a.gdtype;
+        q.accumulate = a.accumulate;
+        k_ce_weight<T><<<dim3(unsigned(mt * tiles)), dim3(kThreads), 0, s>>>(q);
+      }
+    }
+  }
+  if (a.dx) {
+    const int64_t work = (a.rows * ((a.cols + 3) / 4) + 255) / 256;
+    k_ce_join<<<dim3(unsigned(std::min<int64_t>(work, 8192))), dim3(256), 0, s>>>(sum_x, p.dp, p.np * p.dp, p.splits_x, head, pos, a.rows, a.cols, a.dx, a.lddx,
+                                                                                a.dtype, 0);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t linear_ce_bytes(int64_t rows, int64_t vocab, int64_t cols, int32_t dtype, bool backward_pass) {
+  return rows ? size_t(plan(rows, vocab, cols, dtype, backward_pass).bytes) : 0;
+}
+
+hipError_t launch_linear_ce_forward(const LinearCeForward& a, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  return with_type(a.dtype, [&](auto t) { return forward<decltype(t)>(a, s); });
+}
+
+hipError_t launch_linear_ce_backward(const LinearCeBackward& a, hipStream_t s) {
+  if (a.rows == 0) {
+    if (a.dw && !a.accumulate) k_ce_zero<<<dim3(4096), dim3(256), 0, s>>>(a.dw, a.lddw, a.vocab, a.cols, a.gdtype);
+    return hipGetLastError();
+  }
+  return with_type(a.dtype, [&](auto t) { return backward<decltype(t)>(a, s); });
+}
+
+}  // namespace lopt

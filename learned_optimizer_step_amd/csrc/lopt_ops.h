@@ -140,6 +140,35 @@ size_t residual_backward_bytes(int64_t rows, int64_t cols);
 hipError_t launch_residual_forward(const ResidualForward& a, hipStream_t s);
 hipError_t launch_residual_backward(const ResidualBackward& a, hipStream_t s);
 
+// ---- cross entropy of a linear layer's logits (lopt_linear_ce.hip) ----
+struct LinearCeForward {
+  const void* x;        // [rows][cols]
+  const void* w;        // [vocab][cols]
+  const void* targets;
+  float* loss;          // NULL: not written, as lse
+  float* lse;
+  unsigned char* ws;
+  int64_t rows, cols, vocab, ldx, ldw;
+  int32_t dtype, id_bytes;
+};
+
+struct LinearCeBackward {
+  const float* dloss;   // lddl apart
+  const void* x;
+  const void* w;
+  const void* targets;
+  const float* lse;
+  void* dx;             // NULL: not computed, as dw
+  void* dw;
+  unsigned char* ws;
+  int64_t rows, cols, vocab, lddl, ldx, ldw, lddx, lddw;
+  int32_t dtype, id_bytes, gdtype, accumulate;
+};
+
+size_t linear_ce_bytes(int64_t rows, int64_t vocab, int64_t cols, int32_t dtype, bool backward_pass);
+hipError_t launch_linear_ce_forward(const LinearCeForward& a, hipStream_t s);
+hipError_t launch_linear_ce_backward(const LinearCeBackward& a, hipStream_t s);
+
 // ---- AdamW over a list of tensors (lopt_adamw.hip) ----
 constexpr int64_t kMomentBlock = 256;   // elements of a block of moments
 constexpr int kMaxAdamw = 80;           // tensors of one launch

@@ -1,5 +1,5 @@
 // C ABI of the operators around the learned optimizer's step (norms, embedding,
-// distillation loss, AdamW): validation, then the launches of lopt_ops.h.  Nothing is
+// distillation loss, linear cross entropy, AdamW): validation, then the launches of lopt_ops.h.  Nothing is
 // allocated and nothing waits; the calls may be captured into a graph.
 #include <hip/hip_runtime.h>
 
@@ -108,6 +108,14 @@ void check_residual(int32_t kind, int32_t post, int32_t pre, int32_t gate_kind, 
   if (!post && !pre) fail(LOPT_ERR_INVALID_ARGUMENT, "neither norm: post and pre are 0");
   if (gate_kind < LOPT_GATE_NONE || gate_kind > LOPT_GATE_MATRIX) fail(LOPT_ERR_INVALID_ARGUMENT, "unknown kind of gate");
   if (!std::isfinite(alpha) || !std::isfinite(beta)) fail(LOPT_ERR_INVALID_ARGUMENT, "alpha and beta must be finite");
+}
+
+void check_linear_ce(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype) {
+  if (rows < 0 || cols < 1 || vocab < 1) fail(LOPT_ERR_INVALID_ARGUMENT, "rows must be >= 0, cols and vocab >= 1");
+  if (rows > (int64_t(1) << 24) || cols > (int64_t(1) << 20)) fail(LOPT_ERR_UNSUPPORTED, "more than 2^24 rows or 2^20 columns");
+  const int64_t tiles = (vocab + 255) / 256;
+  if (vocab >= kMaxDim || tiles * ((rows + 255) / 256) >= kMaxDim) fail(LOPT_ERR_UNSUPPORTED, "vocab / 256 * rows / 256 must be below 2^31");
+  check_dtype(dtype, "x");
 }
 
 void check_state_bits(int32_t bits) {
@@ -424,6 +432,81 @@ lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, con
     a.top = top; a.dtype = dtype; a.udtype = u_dtype; a.id_bytes = id_bytes;
     a.tau = temperature; a.inv_tau = 1.f / temperature;
     hip_check(launch_distill_backward(a, static_cast<hipStream_t>(stream)), "distill backward");
+  });
+}
+
+lopt_status lopt_linear_ce_forward_workspace(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(LOPT_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    check_linear_ce(rows, cols, vocab, dtype);
+    *bytes = linear_ce_bytes(rows, vocab, cols, dtype, false);
+  });
+}
+
+lopt_status lopt_linear_ce_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) fail(LOPT_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    check_linear_ce(rows, cols, vocab, dtype);
+    *bytes = linear_ce_bytes(rows, vocab, cols, dtype, true);
+  });
+}
+
+lopt_status lopt_linear_ce_forward(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, const void* x, int64_t ldx,
+                                   const void* w, int64_t ldw, const void* targets, int32_t id_bytes, float* loss, float* lse,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    check_linear_ce(rows, cols, vocab, dtype);
+    check_ids(id_bytes);
+    Buffers bufs;
+    bufs.matrix("x", x, rows, cols, ldx, elem_bytes(dtype), false);
+    if (rows) {
+      bufs.matrix("w", w, vocab, cols, ldw, elem_bytes(dtype), false);
+      bufs.add("targets", targets, rows * id_bytes, id_bytes, false);
+      if (loss) bufs.add("loss", loss, rows * 4, 4, true);
+      if (lse) bufs.add("lse", lse, rows * 4, 4, true);
+      const size_t need = linear_ce_bytes(rows, vocab, cols, dtype, false);
+      check_workspace(workspace, ws_bytes, need);
+      bufs.add("workspace", workspace, int64_t(need), 256, true);
+    }
+    bufs.no_overlap();
+    LinearCeForward a{};
+    a.x = x; a.w = w; a.targets = targets; a.loss = loss; a.lse = lse; a.ws = static_cast<unsigned char*>(workspace);
+    a.rows = rows; a.cols = cols; a.vocab = vocab; a.ldx = ldx; a.ldw = ldw; a.dtype = dtype; a.id_bytes = id_bytes;
+    hip_check(launch_linear_ce_forward(a, static_cast<hipStream_t>(stream)), "linear cross entropy forward");
+  });
+}
+
+lopt_status lopt_linear_ce_backward(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, const float* dloss,
+                                    int64_t dloss_stride, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                    const void* targets, int32_t id_bytes, const float* lse, void* dx, int64_t lddx, void* dw,
+                                    int64_t lddw, int32_t g_dtype, int32_t accumulate, void* workspace, size_t ws_bytes,
+                                    void* stream) {
+  return guarded([&] {
+    check_linear_ce(rows, cols, vocab, dtype);
+    check_ids(id_bytes);
+    if (dw) check_dtype(g_dtype, "dw");
+    if (dloss_stride < 0 || dloss_stride >= (int64_t(1) << 28)) fail(LOPT_ERR_INVALID_ARGUMENT, "dloss_stride must lie in [0, 2^28)");
+    Buffers bufs;
+    bufs.matrix("x", x, rows, cols, ldx, elem_bytes(dtype), false);
+    if (rows) {
+      bufs.matrix("w", w, vocab, cols, ldw, elem_bytes(dtype), false);
+      bufs.add("targets", targets, rows * id_bytes, id_bytes, false);
+      bufs.add("dloss", dloss, ((rows - 1) * dloss_stride + 1) * 4, 4, false);
+      bufs.add("lse", lse, rows * 4, 4, false);
+      const size_t need = linear_ce_bytes(rows, vocab, cols, dtype, true);
+      check_workspace(workspace, ws_bytes, need);
+      bufs.add("workspace", workspace, int64_t(need), 256, true);
+    }
+    if (dx) bufs.matrix("dx", dx, rows, cols, lddx, elem_bytes(dtype), true);
+    if (dw) bufs.matrix("dw", dw, vocab, cols, lddw, elem_bytes(g_dtype), true);
+    bufs.no_overlap();
+    if (!dx && !dw) return;
+    LinearCeBackward a{};
+    a.dloss = dloss; a.x = x; a.w = w; a.targets = targets; a.lse = lse; a.dx = dx; a.dw = dw;
+    a.ws = static_cast<unsigned char*>(workspace);
+    a.rows = rows; a.cols = cols; a.vocab = vocab; a.lddl = dloss_stride; a.ldx = ldx; a.ldw = ldw; a.lddx = lddx; a.lddw = lddw;
+    a.dtype = dtype; a.id_bytes = id_bytes; a.gdtype = g_dtype; a.accumulate = accumulate != 0;
+    hip_check(launch_linear_ce_backward(a, static_cast<hipStream_t>(stream)), "linear cross entropy backward");
   });
 }
 

@@ -6,6 +6,7 @@ They produce the gradients that ``lopt.LearnedOptimizer`` and ``lopt.AdamW`` ste
 * ``residual_norm``             the residual update between two blocks with its gate and the norms on both sides
 * ``embedding``                 a token lookup with scaling, its gradient by sorted tokens
 * ``distill_loss``              a loss from a teacher's top logits, where a backward pass begins
+* ``linear_cross_entropy``      the output layer and its cross entropy, without the logits in memory
 
 and ``adamw_step`` is the step of ``lopt.AdamW`` on lists of tensors.  All but it
 are differentiable (``torch.autograd``; gradients of gradients are not
@@ -162,6 +163,34 @@ def distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temper
     grad_loss: one float32 value a row.  out: a contiguous buffer like logits;
     it may be logits itself, which the gradient then replaces."""
     return _C.distill_backward(grad_loss, logits, teacher_ids, teacher_logits, lse, temperature, out)
+
+
+# ---------------------------------------------------------------------------
+# cross entropy of a linear layer's logits
+
+def linear_cross_entropy(x, weight, targets):
+    """The cross entropy of every token of x (float32) under the logits x weight^T, which are never kept; see
+    ``linear_ce_forward``.  Differentiable in x and weight."""
+    return _C.linear_ce(x, weight, targets)
+
+
+def linear_ce_forward(x, weight, targets):
+    """(loss, lse), float32 and of the targets' shape: log sum exp of the logits x weight^T less the target's logit, and
+    that logarithm, for ``linear_ce_backward``.
+
+    x: targets.shape + (D,); weight: (V, D), of x's type.  A target outside the vocabulary (say -1 or -100) is ignored:
+    its loss and gradient are 0."""
+    return _C.linear_ce_forward(x, weight, targets)
+
+
+def linear_ce_backward(grad_loss, x, weight, targets, lse, *, grad_weight=None, accumulate: bool = False,
+                       need_x: bool = True, need_weight: bool = True, grad_dtype: Optional[torch.dtype] = None):
+    """(grad_x, grad_weight) of ``linear_ce_forward``'s loss; None where not needed.
+
+    The logits are made again in pieces of the vocabulary, each piece's gradient rounded to x's type.  grad_loss: one float32
+    value a token.  grad_weight: a buffer to write, or, with accumulate, to add to; made anew where None, of grad_dtype,
+    else of the weight's type."""
+    return _C.linear_ce_backward(grad_loss, x, weight, targets, lse, grad_weight, accumulate, need_x, need_weight, grad_dtype)
 
 
 # ---------------------------------------------------------------------------

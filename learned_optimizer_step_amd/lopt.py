@@ -142,6 +142,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "lopt_distill_forward": (st, [i64, i64, i32, ptr, i64, i32, ptr, i64, i32, ptr, i64, i32, f32, ptr, ptr, ptr]),
         "lopt_distill_backward": (st, [i64, i64, i32, ptr, i64, ptr, i64, i32, ptr, i64, i32, ptr, i64, i32, f32, ptr,
                                        ptr, i64, ptr]),
+        "lopt_linear_ce_forward_workspace": (st, [i64, i64, i64, i32, size]),
+        "lopt_linear_ce_forward": (st, [i64, i64, i64, i32, ptr, i64, ptr, i64, ptr, i32, ptr, ptr, ptr, ctypes.c_size_t, ptr]),
+        "lopt_linear_ce_backward_workspace": (st, [i64, i64, i64, i32, size]),
+        "lopt_linear_ce_backward": (st, [i64, i64, i64, i32, ptr, i64, ptr, i64, ptr, i64, ptr, i32, ptr, ptr, i64, ptr, i64,
+                                         i32, i32, ptr, ctypes.c_size_t, ptr]),
         "lopt_adamw_state_bytes": (st, [i64, i32, size]),
         "lopt_adamw_step": (st, [ctypes.POINTER(lopt_adamw_tensor), i32, i32, f64, f64, f64, u32, ptr, ptr]),
         "lopt_adamw_moments": (st, [ptr, i64, i32, i32, ptr, ptr, ptr]),
@@ -373,6 +378,26 @@ def lopt_distill_forward(*args) -> None:
 
 def lopt_distill_backward(*args) -> None:
     _check((_lib or load_library()).lopt_distill_backward(*args))
+
+
+def lopt_linear_ce_forward_workspace(rows: int, cols: int, vocab: int, dtype: int) -> int:
+    out = ctypes.c_size_t()
+    _check((_lib or load_library()).lopt_linear_ce_forward_workspace(rows, cols, vocab, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def lopt_linear_ce_forward(*args) -> None:
+    _check((_lib or load_library()).lopt_linear_ce_forward(*args))
+
+
+def lopt_linear_ce_backward_workspace(rows: int, cols: int, vocab: int, dtype: int) -> int:
+    out = ctypes.c_size_t()
+    _check((_lib or load_library()).lopt_linear_ce_backward_workspace(rows, cols, vocab, dtype, ctypes.byref(out)))
+    return out.value
+
+
+def lopt_linear_ce_backward(*args) -> None:
+    _check((_lib or load_library()).lopt_linear_ce_backward(*args))
 
 
 def lopt_adamw_state_bytes(n: int, state_bits: int) -> int:
