@@ -23,12 +23,23 @@ constexpr float kLn2 = 0.693147180559945309417f;
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // ---------------------------------------------------------------------------
-// The product C[m][n] = sum_k A[m][k] B[n][k] of a block: 256 x 256 of C, 8
-// waves of 128 x 64 each as 4 x 2 matrix instructions of 32 x 32.  Operands
-// go to LDS in stages of 128 bytes of k, straight from memory, one stage ahead.
-// An operand may lie with k contiguous ("rows") or with m or n contiguous
-// ("columns", a transposed read from LDS): no operand is ever transposed in memory.
-constexpr int kTile = 256, kThreads = 512, kStageBytes = 2 * kTile * 128;
+// The product C[m][n] = sum_k A[m][k] B[n][k] of a block: WM x WN waves of FM x
+// FN matrix instructions of 32 x 32 each.  Operands go to LDS in stages of 128
+// bytes of k, straight from memory.  An operand may lie with k contiguous
+// ("rows") or with m or n contiguous ("columns", a transposed read from LDS):
+// no operand is ever transposed in memory.
+template <int FM_, int FN_, int WM_, int WN_>
+struct Tile {
+  static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
+  static constexpr int M = 32 * FM * WM, N = 32 * FN * WN, WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int STAGE = (M + N) * 128;   // bytes
+};
+// The large tile reads least from the caches for its operations; where its tiles
+// are fewer than the compute units, smaller ones.
+typedef Tile<4, 2, 2, 4> Large;    // 256 x 256, one block a compute unit
+typedef Tile<2, 2, 2, 2> Middle;   // 128 x 128, two
+typedef Tile<1, 1, 2, 2> Small;    // 64 x 64
+constexpr int kTile = 256;         // tokens and pieces are filled up to whole tiles of any size
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -59,29 +70,32 @@ struct Operand {
   int64_t edge;   // columns: the byte in a k where the last 16 begin
 };
 
-// One operand's share of a stage: 32 loads of a wave, 4 for each of the 8 waves.
-template <class T, bool COLUMNS>
+// Columns of R 16-bit elements: the 64-byte groups of the four k that one transposed read takes lie in different banks.
+template <int R>
+__device__ __forceinline__ int group_swap(int k) { return R == 64 ? k >> 1 & 1 : k & 3; }
+
+// R rows (or columns) of one operand of a stage: R / 8 loads of a wave, shared by the block's waves.
+template <class T, bool COLUMNS, int R, int WAVES>
 struct Loader {
-  static constexpr int S = sizeof(T), kStep = 128 / S;
-  const char* p[4];
+  static constexpr int S = sizeof(T), COUNT = R / 8 / WAVES;
+  const char* p[COUNT];
   int64_t ld, last;
-  int kr[4];
+  int kr[COUNT];
 
   __device__ __forceinline__ void begin(const Operand& o, int64_t tile0, int64_t k0, int wave, int lane) {
     ld = o.ld;
     last = o.last;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = wave * 4 + i;
+    for (int i = 0; i < COUNT; ++i) {
+      const int q = wave * COUNT + i;
       if constexpr (!COLUMNS) {
         // 8 rows of 128 bytes; 16-byte piece c of row r lies in place c ^ (r / 2 % 8), so that a read of 16 rows at one k meets every bank once
         const int r = q * 8 + lane / 8, c = (lane % 8) ^ (r / 2 % 8);
         p[i] = o.p + min(tile0 + r, last) * ld + k0 * S + c * 16;
       } else {
-        constexpr int PER = kTile * S / 16;   // 16-byte pieces of a k
+        constexpr int PER = R * S / 16;   // 16-byte pieces of a k
         kr[i] = q * (64 / PER) + lane / PER;
-        // 16-bit: the 64-byte groups of the four k that one transposed read takes lie in different banks
-        const int c = (lane % PER) ^ (S == 2 ? (kr[i] & 3) << 2 : 0);
+        const int c = (lane % PER) ^ (S == 2 ? group_swap<R>(kr[i]) << 2 : 0);
         p[i] = o.p + min(tile0 * S + c * 16, o.edge);
       }
     }
@@ -89,93 +103,117 @@ struct Loader {
   // The stage at k0 into `to`; rows: k0 is the next one each time.
   __device__ __forceinline__ void load(char* to, int64_t k0, int wave) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < COUNT; ++i) {
       const char* from = p[i];
       if constexpr (COLUMNS) from += min(k0 + kr[i], last) * ld;
       else p[i] += 128;
-      __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from), LDS_PTR(void, to + (wave * 4 + i) * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from), LDS_PTR(void, to + (wave * COUNT + i) * 1024), 16, 0, 0);
     }
   }
 };
 
 // 32 rows (m or n, from row0) at the j-th quarter of a stage, as the matrix
 // instructions take them: lane l has row l % 32 and the k of half l / 32.
-template <class T, bool COLUMNS>
+template <class T, bool COLUMNS, int R>
 __device__ __forceinline__ u32x4 fragment(const char* s, int row0, int j, int lane) {
   const int l = lane % 32, h = lane / 32;
   if constexpr (!COLUMNS) {
     return *reinterpret_cast<const u32x4*>(s + (row0 + l) * 128 + (((2 * j + h) ^ (l / 2 % 8)) * 16));
   } else if constexpr (sizeof(T) == 2) {
     const int g = lane / 16, i = lane % 16;
-    const char* at = s + (16 * j + 8 * h + i / 4) * 512 + ((((row0 / 32) ^ (i / 4)) * 4 + (g & 1) * 2 + (i & 3) / 2) * 16 + (i & 1) * 8);
+    const char* at = s + (16 * j + 8 * h + i / 4) * (2 * R) + ((((row0 / 32) ^ group_swap<R>(i / 4)) * 4 + (g & 1) * 2 + (i & 3) / 2) * 16 + (i & 1) * 8);
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at));
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at + 4 * 512));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at + 4 * (2 * R)));
     return __builtin_bit_cast(u32x4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    const uint32_t* at = reinterpret_cast<const uint32_t*>(s + (8 * j + 4 * h) * 1024 + (row0 + l) * 4);
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(s + (8 * j + 4 * h) * (4 * R) + (row0 + l) * 4);
     u32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = at[e * 256];
+    for (int e = 0; e < 4; ++e) v[e] = at[e * R];
     return v;
   }
 }
 
-// acc += the block's product over `steps` stages from k0.  Everything that was read is read when it returns.
-template <class T, bool AC, bool BC>
-__device__ __forceinline__ void product(f32x16 (&acc)[4][2], const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k0,
-                                        int64_t steps, char* lds) {
+template <class C>
+using Acc = f32x16[C::FM][C::FN];
+
+// A wave's fragments of a quarter of a stage.
+template <class T, bool AC, bool BC, class C>
+struct Fragments {
+  u32x4 a[C::FM], b[C::FN];
+  __device__ __forceinline__ void read(const char* stage, int j, int wm, int wn, int lane) {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) a[i] = fragment<T, AC, C::M>(stage, (wm * C::FM + i) * 32, j, lane);
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) b[i] = fragment<T, BC, C::N>(stage + C::M * 128, (wn * C::FN + i) * 32, j, lane);
+  }
+  __device__ __forceinline__ void multiply_into(Acc<C>& acc) const {
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int k = 0; k < C::FN; ++k) multiply<T>(acc[i][k], a[i], b[k]);
+  }
+};
+
+// acc = the block's product over `steps` stages from k0.  Fragments are read a
+// quarter ahead, the next stage's first ones while the matrix instructions
+// of this one's last quarter run: the barrier between stages stands before
+// those, and the stage after the next goes where this one was read.  All of LDS is read when it returns.
+template <class T, bool AC, bool BC, class C>
+__device__ __forceinline__ void product(Acc<C>& acc, const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k0, int64_t steps, char* lds) {
   constexpr int kStep = 128 / int(sizeof(T));
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = wave % 2, wn = wave / 2;
-  Loader<T, AC> la;
-  Loader<T, BC> lb;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = wave % C::WM, wn = wave / C::WM;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int k = 0; k < C::FN; ++k)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
+  if (steps <= 0) return;
+  Loader<T, AC, C::M, C::WAVES> la;
+  Loader<T, BC, C::N, C::WAVES> lb;
   la.begin(a, m0, k0, wave, lane);
   lb.begin(b, n0, k0, wave, lane);
-  if (steps > 0) {
-    la.load(lds, k0, wave);
-    lb.load(lds + kStageBytes / 2, k0, wave);
-  }
-  for (int64_t s = 0; s < steps; ++s) {
-    const char* now = lds + (s & 1) * kStageBytes;
-    char* next = lds + (~s & 1) * kStageBytes;
-    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the stage is there
-    __syncthreads();                      // everyone's is, and the stage before is read
-    if (s + 1 < steps) {
-      la.load(next, k0 + (s + 1) * kStep, wave);
-      lb.load(next + kStageBytes / 2, k0 + (s + 1) * kStep, wave);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      u32x4 fa[4], fb[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fa[i] = fragment<T, AC>(now, wm * 128 + i * 32, j, lane);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) fb[i] = fragment<T, BC>(now + kStageBytes / 2, wn * 64 + i * 32, j, lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) multiply<T>(acc[i][k], fa[i], fb[k]);
-    }
-  }
+  const auto load = [&](int64_t s) {
+    char* to = lds + (s & 1) * C::STAGE;
+    la.load(to, k0 + s * kStep, wave);
+    lb.load(to + C::M * 128, k0 + s * kStep, wave);
+  };
+  Fragments<T, AC, BC, C> f[2];
+  load(0);
+  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the stage is there
   __syncthreads();
+  if (steps > 1) load(1);
+  f[0].read(lds, 0, wm, wn, lane);
+  for (int64_t s = 0; s < steps; ++s) {
+    const char* now = lds + (s & 1) * C::STAGE;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      f[(j + 1) & 1].read(now, j + 1, wm, wn, lane);
+      __builtin_amdgcn_sched_barrier(0);
+      f[j & 1].multiply_into(acc);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0): the next stage is there, this one is read
+    __syncthreads();
+    if (s + 2 < steps) load(s + 2);
+    if (s + 1 < steps) f[0].read(lds + (~s & 1) * C::STAGE, 0, wm, wn, lane);
+    __builtin_amdgcn_sched_barrier(0);
+    f[1].multiply_into(acc);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 // Element e of acc[i][k] is C[m][n] with these, from the block's first.
+template <class C>
 __device__ __forceinline__ int tile_m(int i, int e) {
   const int wave = threadIdx.x >> 6, h = (threadIdx.x & 63) / 32;
-  return (wave % 2) * 128 + i * 32 + 8 * (e / 4) + 4 * h + e % 4;
+  return ((wave % C::WM) * C::FM + i) * 32 + 8 * (e / 4) + 4 * h + e % 4;
 }
+template <class C>
 __device__ __forceinline__ int tile_n(int k) {
   const int wave = threadIdx.x >> 6;
-  return (wave / 2) * 64 + k * 32 + threadIdx.x % 32;
-}
-
-__device__ __forceinline__ void clear(f32x16 (&acc)[4][2]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
+  return ((wave / C::WM) * C::FN + k) * 32 + threadIdx.x % 32;
 }
 
 // A block's tile.  Blocks go to the eight dies in turn, each with a cache of its
@@ -222,39 +260,40 @@ struct Stats {
   int32_t id_bytes;
 };
 
-template <class T>
-__global__ __launch_bounds__(kThreads, 2) void k_ce_stats(Stats a) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+template <class T, class C>
+__global__ __launch_bounds__(C::THREADS, 2) void k_ce_stats(Stats a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
   const Place t = place(blockIdx.x, a.mt, a.nt);
-  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
-  f32x16 acc[4][2];
-  clear(acc);
-  product<T, false, false>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
+  const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
+  Acc<C> acc;
+  product<T, false, false, C>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
   const int64_t v0 = a.v0 + m0;
-  if (v0 + kTile > a.vend) {
+  if (v0 + C::M > a.vend) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        if (v0 + tile_m(i, e) >= a.vend) acc[i][0][e] = acc[i][1][e] = -INFINITY;
+        if (v0 + tile_m<C>(i, e) >= a.vend)
+#pragma unroll
+          for (int k = 0; k < C::FN; ++k) acc[i][k][e] = -INFINITY;
   }
-  float2* red = reinterpret_cast<float2*>(lds);   // [2][256]
+  float2(*red)[C::N] = reinterpret_cast<float2(*)[C::N]>(lds);
   const int wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t tok = n0 + tile_n(k);
+  for (int k = 0; k < C::FN; ++k) {
+    const int64_t tok = n0 + tile_n<C>(k);
     const int64_t at = tok < a.n ? load_id(a.targets, a.id_bytes, tok) - v0 : -1;
-    const bool here = at >= 0 && at < kTile && v0 + at < a.vend;
+    const bool here = at >= 0 && at < C::M && v0 + at < a.vend;
     if (__ballot(here)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (here && at == tile_m(i, e)) a.hit[tok] = acc[i][k][e];
+          if (here && at == tile_m<C>(i, e)) a.hit[tok] = acc[i][k][e];
     }
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][k][e]);
     const Two both = swap32(m);
@@ -262,45 +301,56 @@ __global__ __launch_bounds__(kThreads, 2) void k_ce_stats(Stats a) {
     const float mc = m == -INFINITY ? 0.f : m;
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s += exp2_hw((acc[i][k][e] - mc) * kLog2e);
     const Two sums = swap32(s);
     s = sums.a + sums.b;
-    if ((threadIdx.x & 63) < 32) red[(wave % 2) * kTile + tile_n(k)] = make_float2(m, s);
+    if ((threadIdx.x & 63) < 32) red[wave % C::WM][tile_n<C>(k)] = make_float2(m, s);
   }
   __syncthreads();
-  if (threadIdx.x < kTile && n0 + threadIdx.x < a.n) {
-    const float2 x = red[threadIdx.x], y = red[kTile + threadIdx.x];
-    const float m = fmaxf(x.x, y.x), mc = m == -INFINITY ? 0.f : m;
-    const float s = x.y * exp2_hw((x.x - mc) * kLog2e) + y.y * exp2_hw((y.x - mc) * kLog2e);
-    a.part[(v0 / kTile) * a.np + n0 + threadIdx.x] = make_float2(m, s);
+  if (threadIdx.x < C::N && n0 + threadIdx.x < a.n) {
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int q = 0; q < C::WM; ++q) m = fmaxf(m, red[q][threadIdx.x].x);
+    const float mc = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int q = 0; q < C::WM; ++q) s = fmaf(red[q][threadIdx.x].y, exp2_hw((red[q][threadIdx.x].x - mc) * kLog2e), s);
+    a.part[v0 / C::M * a.np + n0 + threadIdx.x] = make_float2(m, s);
   }
 }
 
-// Per token, the tiles' maxima and sums in their order: 64 tokens a block, 4 threads a token.
-__global__ __launch_bounds__(256) void k_ce_loss(const float2* part, int64_t tiles, int64_t np, int64_t n, int64_t vocab, const void* targets,
-                                                 int32_t id_bytes, const float* hit, float* loss, float* lse) {
-  __shared__ float2 red[4][64];
-  const int64_t tok = int64_t(blockIdx.x) * 64 + threadIdx.x % 64;
-  const int q = threadIdx.x / 64;
+// Per token, the tiles' maxima and sums in their order: 32 tokens a block, 32 threads a token with every 32nd tile each.
+__global__ __launch_bounds__(1024) void k_ce_loss(const float2* part, int64_t tiles, int64_t np, int64_t n, int64_t vocab, const void* targets,
+                                                  int32_t id_bytes, const float* hit, float* loss, float* lse) {
+  __shared__ float2 red[32][33];
+  const int i = threadIdx.x % 32, q = threadIdx.x / 32;
+  const int64_t tok = int64_t(blockIdx.x) * 32 + i;
   float m = -INFINITY, s = 0.f;
   if (tok < n) {
-    for (int64_t t = q; t < tiles; t += 4) m = fmaxf(m, part[t * np + tok].x);
-    const float mc = m == -INFINITY ? 0.f : m;
-    for (int64_t t = q; t < tiles; t += 4) {
-      const float2 x = part[t * np + tok];
-      s = fmaf(x.y, exp2_hw((x.x - mc) * kLog2e), s);
+    for (int64_t t = q; t < tiles; t += 32 * 8) {
+      float2 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = t + 32 * k < tiles ? part[(t + 32 * k) * np + tok] : make_float2(-INFINITY, 0.f);
+      const float old = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, x[k].x);
+      const float mc = m == -INFINITY ? 0.f : m;
+      s = old == -INFINITY ? s : s * exp2_hw((old - mc) * kLog2e);   // 0 or NaN so far: whatever the tiles hold, m may be far below 0
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = fmaf(x[k].y, exp2_hw((x[k].x - mc) * kLog2e), s);
     }
   }
-  red[q][threadIdx.x % 64] = make_float2(m, s);
+  red[q][i] = make_float2(m, s);
   __syncthreads();
   if (q || tok >= n) return;
-  m = fmaxf(fmaxf(red[0][threadIdx.x].x, red[1][threadIdx.x].x), fmaxf(red[2][threadIdx.x].x, red[3][threadIdx.x].x));
+  m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) m = fmaxf(m, red[k][i].x);
   const float mc = m == -INFINITY ? 0.f : m;
   s = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) s = fmaf(red[k][threadIdx.x].y, exp2_hw((red[k][threadIdx.x].x - mc) * kLog2e), s);
+  for (int k = 0; k < 32; ++k) s = fmaf(red[k][i].y, exp2_hw((red[k][i].x - mc) * kLog2e), s);
   const float log_s = kLn2 * log2f(s);
   if (lse) lse[tok] = m + log_s;
   if (loss) {
@@ -398,27 +448,26 @@ struct Grad {
   uint32_t mt, nt;
 };
 
-template <class T>
-__global__ __launch_bounds__(kThreads, 2) void k_ce_grad(Grad a) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+template <class T, class C>
+__global__ __launch_bounds__(C::THREADS, 2) void k_ce_grad(Grad a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
   const Place t = place(blockIdx.x, a.mt, a.nt);
-  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
+  const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
   if (n0 >= a.head->n) return;
-  f32x16 acc[4][2];
-  clear(acc);
-  product<T, false, false>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
+  Acc<C> acc;
+  product<T, false, false, C>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
   const int64_t v0 = a.v0 + m0;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int64_t tok = n0 + tile_n(k);
+  for (int k = 0; k < C::FN; ++k) {
+    const int64_t tok = n0 + tile_n<C>(k);
     const Row r = a.rows[tok];
     const int64_t target = r.target - v0;
     T* out = static_cast<T*>(a.out) + tok * a.width + m0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
-        const int m = tile_m(i, e);
+        const int m = tile_m<C>(i, e);
         Pack<T, 4> p;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -449,28 +498,27 @@ __device__ __forceinline__ void share(int64_t steps, int32_t splits, int64_t z, 
   count = per + (z < rest ? 1 : 0);
 }
 
-template <class T, bool BC>
-__global__ __launch_bounds__(kThreads, 2) void k_ce_sums(Sums a) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+template <class T, bool BC, class C>
+__global__ __launch_bounds__(C::THREADS, 2) void k_ce_sums(Sums a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
   constexpr int kStep = 128 / int(sizeof(T));
   const int64_t n = a.head->n;
   const uint32_t tiles = a.mt * a.nt, z = blockIdx.x / tiles;
   const Place t = place(blockIdx.x - z * tiles, a.mt, a.nt);
-  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
+  const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
   if (!BC && n0 >= n) return;   // n: tokens
   int64_t first, count;
   share(((BC ? n : a.k) + kStep - 1) / kStep, a.splits, z, first, count);
-  f32x16 acc[4][2];
-  clear(acc);
-  product<T, true, BC>(acc, a.a, a.b, m0, n0, first * kStep, count, lds);
+  Acc<C> acc;
+  product<T, true, BC, C>(acc, a.a, a.b, m0, n0, first * kStep, count, lds);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float* out = a.out + z * a.pitch + (n0 + tile_n(k)) * a.ldo;
+  for (int k = 0; k < C::FN; ++k) {
+    float* out = a.out + z * a.pitch + (n0 + tile_n<C>(k)) * a.ldo;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < C::FM; ++i)
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
-        const int64_t m = m0 + tile_m(i, e);
+        const int64_t m = m0 + tile_m<C>(i, e);
         if (m >= a.ldo) continue;
         f32x4 v = {acc[i][k][e], acc[i][k][e + 1], acc[i][k][e + 2], acc[i][k][e + 3]};
         f32x4* to = reinterpret_cast<f32x4*>(out + m);
@@ -490,28 +538,27 @@ struct WeightGrad {
   int32_t dtype, accumulate;
 };
 
-template <class T>
-__global__ __launch_bounds__(kThreads, 2) void k_ce_weight(WeightGrad a) {
-  __shared__ __attribute__((aligned(1024))) char lds[2 * kStageBytes];
+template <class T, class C>
+__global__ __launch_bounds__(C::THREADS, 2) void k_ce_weight(WeightGrad a) {
+  __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
   constexpr int kStep = 128 / int(sizeof(T));
   const Place t = place(blockIdx.x, a.mt, a.nt);
-  const int64_t m0 = t.m * kTile, n0 = t.n * kTile;
-  f32x16 acc[4][2];
-  clear(acc);
-  product<T, true, true>(acc, a.a, a.b, m0, n0, 0, (int64_t(a.head->n) + kStep - 1) / kStep, lds);
+  const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
+  Acc<C> acc;
+  product<T, true, true, C>(acc, a.a, a.b, m0, n0, 0, (int64_t(a.head->n) + kStep - 1) / kStep, lds);
   const float inv = a.head->inv_scale;
   const auto write = [&](auto type) {
     using W = decltype(type);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t r = n0 + tile_n(k);
+    for (int k = 0; k < C::FN; ++k) {
+      const int64_t r = n0 + tile_n<C>(k);
       if (r >= a.rows) continue;
       W* out = static_cast<W*>(a.out) + r * a.ldo;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const int64_t m = m0 + tile_m(i, e);
+          const int64_t m = m0 + tile_m<C>(i, e);
           if (m >= a.cols) continue;
           Pack<W, 4> p;
           if (a.accumulate) p = load_pack<W, 4>(out, m, a.cols);
@@ -534,8 +581,18 @@ __global__ __launch_bounds__(256) void k_ce_join(const float* sums, int64_t ld, 
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
     const int64_t r = i / per, c = (i - r * per) * 4, from = pos ? pos[r] : r;
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    if (from >= 0)
-      for (int32_t z = 0; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(sums + z * pitch + from * ld + c);
+    if (from >= 0) {
+      const float* at = sums + from * ld + c;
+      int32_t z = 0;
+      for (; z + 4 <= splits; z += 4) {
+        f32x4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const f32x4*>(at + (z + k) * pitch);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v += x[k];
+      }
+      for (; z < splits; ++z) v += *reinterpret_cast<const f32x4*>(at + z * pitch);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (c + k < cols) store_any(out, dtype, r * ldo + c + k, (accumulate ? load_any(out, dtype, r * ldo + c + k) : 0.f) + inv * v[k]);
@@ -557,11 +614,48 @@ hipError_t with_type(int32_t dtype, F&& f) {
 int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 int64_t size_of(int32_t dtype) { return dtype == kF32 ? 4 : 2; }
 
+// A tile of a product of m x n, and in how many parts the sum over k goes.
+enum : int { kLarge = 0, kMiddle = 1, kSmall = 2 };
+struct Shape {
+  int tile;
+  int32_t splits;
+};
+constexpr int64_t kUnits = 256;   // compute units
+int64_t tiles_of(int64_t m, int64_t n, int tile) {
+  const int64_t t = 256 >> tile;
+  return ((m + t - 1) / t) * ((n + t - 1) / t);
+}
+// Whole sums: the largest tile that gives most compute units one (a bf16 1003 x 10007 x 333 product: TODO).
+int whole_tile(int64_t m, int64_t n) {
+  for (int tile = kLarge; tile < kSmall; ++tile)
+    if (tiles_of(m, n, tile) >= kUnits * 3 / 4) return tile;
+  return kSmall;
+}
+// Sums that may be split: the largest tile that does with parts of at least 16, 8 and 4 stages.
+Shape split_tile(int64_t m, int64_t n, int64_t steps) {
+  for (int tile = kLarge; tile < kSmall; ++tile) {
+    const int64_t tiles = tiles_of(m, n, tile), most = std::max<int64_t>(1, steps / (16 >> tile));
+    if (tiles * most >= kUnits * 3 / 4) return {tile, int32_t(std::max<int64_t>(1, std::min(most, kUnits / tiles)))};
+  }
+  const int64_t tiles = tiles_of(m, n, kSmall), most = std::max<int64_t>(1, steps / 4);
+  return {kSmall, int32_t(std::max<int64_t>(1, std::min(most, kUnits / tiles)))};
+}
+template <class F>
+void with_tile(int tile, F&& f) {
+  if (tile == kLarge) f(Large());
+  else if (tile == kMiddle) f(Middle());
+  else f(Small());
+}
+template <class C>
+uint32_t count(int64_t x, bool m) { return uint32_t((x + (m ? C::M : C::N) - 1) / (m ? C::M : C::N)); }
+
 // Where things lie in the workspace.
 struct Plan {
-  int64_t s, np, dp, mt_all;     // element bytes; tokens and columns filled up; tiles of the vocabulary
+  int64_t s, np, dp;             // element bytes; tokens and columns filled up
   int64_t width;                 // of a piece of the vocabulary
-  int32_t splits_x, splits_w;
+  int logits;                    // tiles
+  int64_t parts;                 // tiles of the vocabulary
+  Shape sx, sw;
   int64_t bytes = 0;
   int64_t take(int64_t n) {
     const int64_t at = bytes;
@@ -578,14 +672,17 @@ Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) 
   p.s = size_of(dtype);
   p.np = up(n, kTile);
   p.dp = up(cols, 128 / p.s);
-  p.mt_all = up(vocab, kTile) / kTile;
   const int64_t all = up(vocab, kTile);
   const int64_t most = std::max(backward ? p.np : 0, p.dp) * p.s;
   p.width = std::min(all, std::max<int64_t>(kPieceBytes / most / kTile, 4) * kTile);
+  const int64_t pieces = (all + p.width - 1) / p.width;   // of one length
+  p.width = up((vocab + pieces - 1) / pieces, kTile);
+  p.logits = whole_tile(std::min(vocab, p.width), n);
   p.x = p.take(p.np * p.dp * p.s);
   p.w = p.take(p.width * p.dp * p.s);
   if (!backward) {
-    p.part = p.take(p.mt_all * p.np * 8);
+    p.parts = all / (256 >> p.logits);
+    p.part = p.take(p.parts * p.np * 8);
     p.hit = p.take(n * 4);
     return p;
   }
@@ -593,13 +690,10 @@ Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) 
   p.rows = p.take(p.np * int64_t(sizeof(Row)));
   p.pos = p.take(n * 4);
   p.g = p.take(p.np * p.width * p.s);
-  // enough blocks for the chip where a product has few tiles
-  const int64_t mt = up(p.dp, kTile) / kTile;
-  const auto splits = [&](int64_t tiles, int64_t steps) { return int32_t(std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 8))); };
-  p.splits_x = splits(mt * (p.np / kTile), p.width * p.s / 128);
-  p.splits_w = splits(mt * (p.width / kTile), p.np * p.s / 128);
-  p.sum_x = p.take(p.splits_x * p.np * p.dp * 4);
-  p.sum_w = p.splits_w > 1 ? p.take(p.splits_w * p.width * p.dp * 4) : 0;
+  p.sx = split_tile(p.dp, n, p.width * p.s / 128);
+  p.sw = split_tile(p.dp, std::min(vocab, p.width), p.np * p.s / 128);
+  p.sum_x = p.take(p.sx.splits * p.np * p.dp * 4);
+  p.sum_w = p.sw.splits > 1 ? p.take(p.sw.splits * p.width * p.dp * 4) : 0;
   return p;
 }
 
@@ -621,7 +715,6 @@ hipError_t forward(const LinearCeForward& a, hipStream_t s) {
   g.steps = p.dp * p.s / 128;
   g.n = a.rows;
   g.np = p.np;
-  g.nt = p.np / kTile;
   g.targets = a.targets;
   g.id_bytes = a.id_bytes;
   g.part = reinterpret_cast<float2*>(ws + p.part);
@@ -645,10 +738,15 @@ hipError_t forward(const LinearCeForward& a, hipStream_t s) {
     }
     g.v0 = v0;
     g.vend = v0 + rows;
-    g.mt = (rows + kTile - 1) / kTile;
-    k_ce_stats<T><<<dim3(unsigned(g.mt * g.nt)), dim3(kThreads), 0, s>>>(g);
+    with_tile(p.logits, [&](auto c) {
+      using C = decltype(c);
+      g.mt = count<C>(rows, true);
+      g.nt = count<C>(a.rows, false);
+      k_ce_stats<T, C><<<dim3(g.mt * g.nt), dim3(C::THREADS), 0, s>>>(g);
+    });
   }
-  k_ce_loss<<<dim3(unsigned((a.rows + 63) / 64)), dim3(256), 0, s>>>(g.part, p.mt_all, p.np, a.rows, a.vocab, a.targets, a.id_bytes, g.hit, a.loss, a.lse);
+  const int64_t parts = (a.vocab + (256 >> p.logits) - 1) / (256 >> p.logits);
+  k_ce_loss<<<dim3(unsigned((a.rows + 31) / 32)), dim3(1024), 0, s>>>(g.part, parts, p.np, a.rows, a.vocab, a.targets, a.id_bytes, g.hit, a.loss, a.lse);
   return hipGetLastError();
 }
 
@@ -665,12 +763,11 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
   k_ce_gather<T><<<dim3(unsigned(std::min<int64_t>(blocks, 8192))), dim3(256), 0, s>>>(static_cast<const T*>(a.x), a.ldx, a.cols, head, rows, x, p.dp);
   const Operand xr{reinterpret_cast<const char*>(x), p.dp * p.s, p.np - 1, 0}, xc{xr.p, xr.ld, p.np - 1, p.dp * p.s - 16};
   const bool whole = direct(a.w, a.ldw, a.cols, p.s);
-  const int64_t mt = up(p.dp, kTile) / kTile, nt = p.np / kTile;
   float* sum_x = reinterpret_cast<float*>(ws + p.sum_x);
   float* sum_w = reinterpret_cast<float*>(ws + p.sum_w);
   char* G = reinterpret_cast<char*>(ws + p.g);
   for (int64_t v0 = 0; v0 < a.vocab; v0 += p.width) {
-    const int64_t n = std::min(p.width, a.vocab - v0), tiles = (n + kTile - 1) / kTile;
+    const int64_t n = std::min(p.width, a.vocab - v0);
     const char* w = static_cast<const char*>(a.w) + v0 * a.ldw * p.s;
     int64_t ldw = a.ldw * p.s;
     if (!whole) {
@@ -688,9 +785,13 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
     g.vend = v0 + n;
     g.width = p.width;
     g.steps = p.dp * p.s / 128;
-    g.mt = tiles;
-    g.nt = nt;
-    k_ce_grad<T><<<dim3(unsigned(g.mt * g.nt)), dim3(kThreads), 0, s>>>(g);
+    // whole tiles of any size: what the sums below read of G is written
+    with_tile(p.logits, [&](auto c) {
+      using C = decltype(c);
+      g.mt = count<C>(up(n, kTile), true);
+      g.nt = count<C>(p.np, false);
+      k_ce_grad<T, C><<<dim3(g.mt * g.nt), dim3(C::THREADS), 0, s>>>(g);
+    });
     if (a.dx) {
       Sums q{};
       q.a = {w, ldw, n - 1, p.dp * p.s - 16};
@@ -699,17 +800,20 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
       q.out = sum_x;
       q.ldo = p.dp;
       q.pitch = p.np * p.dp;
-      q.k = tiles * kTile;
-      q.mt = mt;
-      q.nt = nt;
-      q.splits = p.splits_x;
+      q.k = up(n, kTile);
+      q.splits = p.sx.splits;
       q.add = v0 > 0;
-      k_ce_sums<T, false><<<dim3(unsigned(mt * nt * q.splits)), dim3(kThreads), 0, s>>>(q);
+      with_tile(p.sx.tile, [&](auto c) {
+        using C = decltype(c);
+        q.mt = count<C>(p.dp, true);
+        q.nt = count<C>(a.rows, false);
+        k_ce_sums<T, false, C><<<dim3(q.mt * q.nt * unsigned(q.splits)), dim3(C::THREADS), 0, s>>>(q);
+      });
     }
     if (a.dw) {
       const Operand gc{G, p.width * p.s, p.np - 1, p.width * p.s - 16};
       char* out = static_cast<char*>(a.dw) + v0 * a.lddw * size_of(a.gdtype);
-      if (p.splits_w > 1) {
+      if (p.sw.splits > 1) {
         Sums q{};
         q.a = xc;
         q.b = gc;
@@ -717,12 +821,15 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
         q.out = sum_w;
         q.ldo = p.dp;
         q.pitch = p.width * p.dp;
-        q.mt = mt;
-        q.nt = tiles;
-        q.splits = p.splits_w;
-        k_ce_sums<T, true><<<dim3(unsigned(mt * tiles * q.splits)), dim3(kThreads), 0, s>>>(q);
+        q.splits = p.sw.splits;
+        with_tile(p.sw.tile, [&](auto c) {
+          using C = decltype(c);
+          q.mt = count<C>(p.dp, true);
+          q.nt = count<C>(n, false);
+          k_ce_sums<T, true, C><<<dim3(q.mt * q.nt * unsigned(q.splits)), dim3(C::THREADS), 0, s>>>(q);
+        });
         const int64_t work = (n * ((a.cols + 3) / 4) + 255) / 256;
-        k_ce_join<<<dim3(unsigned(std::min<int64_t>(work, 8192))), dim3(256), 0, s>>>(sum_w, p.dp, q.pitch, p.splits_w, head, nullptr, n, a.cols, out, a.lddw,
+        k_ce_join<<<dim3(unsigned(std::min<int64_t>(work, 8192))), dim3(256), 0, s>>>(sum_w, p.dp, q.pitch, q.splits, head, nullptr, n, a.cols, out, a.lddw,
                                                                                     a.gdtype, a.accumulate);
       } else {
         WeightGrad q{};
@@ -733,17 +840,20 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
         q.ldo = a.lddw;
         q.rows = n;
         q.cols = a.cols;
-        q.mt = mt;
-        q.nt = tiles;
         q.dtype = a.gdtype;
         q.accumulate = a.accumulate;
-        k_ce_weight<T><<<dim3(unsigned(mt * tiles)), dim3(kThreads), 0, s>>>(q);
+        with_tile(p.sw.tile, [&](auto c) {
+          using C = decltype(c);
+          q.mt = count<C>(p.dp, true);
+          q.nt = count<C>(n, false);
+          k_ce_weight<T, C><<<dim3(q.mt * q.nt), dim3(C::THREADS), 0, s>>>(q);
+        });
       }
     }
   }
   if (a.dx) {
     const int64_t work = (a.rows * ((a.cols + 3) / 4) + 255) / 256;
-    k_ce_join<<<dim3(unsigned(std::min<int64_t>(work, 8192))), dim3(256), 0, s>>>(sum_x, p.dp, p.np * p.dp, p.splits_x, head, pos, a.rows, a.cols, a.dx, a.lddx,
+    k_ce_join<<<dim3(unsigned(std::min<int64_t>(work, 8192))), dim3(256), 0, s>>>(sum_x, p.dp, p.np * p.dp, p.sx.splits, head, pos, a.rows, a.cols, a.dx, a.lddx,
                                                                                 a.dtype, 0);
   }
   return hipGetLastError();
