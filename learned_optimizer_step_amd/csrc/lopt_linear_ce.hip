@@ -24,24 +24,25 @@ __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2
 
 // ---------------------------------------------------------------------------
 // The product C[m][n] = sum_k A[m][k] B[n][k] of a block: WM x WN waves of FM x
-// FN matrix instructions of 32 x 32 each.  Operands go to LDS in stages of 128
+// FN matrix instructions of 16 x 16 each.  Under load the card's power sets the
+// clock, and these do more for it than those of 32 x 32 (registers of random
+// bf16 numbers alone: 2066 TFLOP/s, 1848).  Operands go to LDS in stages of 128
 // bytes of k, straight from memory.  An operand may lie with k contiguous
 // ("rows") or with m or n contiguous ("columns", a transposed read from LDS):
 // no operand is ever transposed in memory.
 template <int FM_, int FN_, int WM_, int WN_>
 struct Tile {
   static constexpr int FM = FM_, FN = FN_, WM = WM_, WN = WN_;
-  static constexpr int M = 32 * FM * WM, N = 32 * FN * WN, WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int M = 16 * FM * WM, N = 16 * FN * WN, WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int STAGE = (M + N) * 128;   // bytes
 };
 // The large tile reads least from the caches for its operations; where its tiles
 // are fewer than the compute units, smaller ones.
-typedef Tile<4, 2, 2, 4> Large;    // 256 x 256, one block a compute unit
-typedef Tile<2, 2, 2, 2> Middle;   // 128 x 128, two
-typedef Tile<1, 1, 2, 2> Small;    // 64 x 64
+typedef Tile<8, 4, 2, 4> Large;    // 256 x 256, one block a compute unit
+typedef Tile<4, 4, 2, 2> Middle;   // 128 x 128, two
+typedef Tile<2, 2, 2, 2> Small;    // 64 x 64
 constexpr int kTile = 256;         // tokens and pieces are filled up to whole tiles of any size
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -51,15 +52,15 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 #define GLOBAL_PTR(p) ((const __attribute__((address_space(1))) void*)(p))
 
 template <class T>
-__device__ __forceinline__ void multiply(f32x16& c, u32x4 a, u32x4 b) {
+__device__ __forceinline__ void multiply(f32x4& c, u32x4 a, u32x4 b) {
   if constexpr (std::is_same_v<T, bf16>) {
-    c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
   } else if constexpr (std::is_same_v<T, f16>) {
-    c = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   } else {
     const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], y[e], c, 0, 0, 0);
   }
 }
 
@@ -70,63 +71,72 @@ struct Operand {
   int64_t edge;   // columns: the byte in a k where the last 16 begin
 };
 
-// Columns of R 16-bit elements: the 64-byte groups of the four k that one transposed read takes lie in different banks.
-template <int R>
-__device__ __forceinline__ int group_swap(int k) { return R == 64 ? k >> 1 & 1 : k & 3; }
+// Columns: what one read takes at several k lies in different banks.  The place of a 16-byte piece of k's row is its own
+// number with these bits turned: 16-bit elements, 32 bytes at each of the k 0-3 and 8-11 of 32; fp32, 64 bytes at every 4th k of 16.
+template <int S, int R>
+__device__ __forceinline__ int turned(int k) {
+  if (S == 4) return (k >> 2 & 3) << 2;
+  return R == 64 ? ((k >> 1 & 1) | (k >> 3 & 1) << 1) << 1 : ((k & 3) | (k >> 3 & 1) << 2) << 1;
+}
 
 // R rows (or columns) of one operand of a stage: R / 8 loads of a wave, shared by the block's waves.
 template <class T, bool COLUMNS, int R, int WAVES>
 struct Loader {
-  static constexpr int S = sizeof(T), COUNT = R / 8 / WAVES;
+  static constexpr int S = sizeof(T), kStep = 128 / S, COUNT = R / 8 / WAVES, PER = R * S / 16;   // PER: 16-byte pieces of a k (columns)
   const char* p[COUNT];
-  int64_t ld, last;
-  int kr[COUNT];
+  int64_t ld, left;   // left: k from the next stage's first to the last one
+
+  // k of load i's piece in a stage
+  __device__ __forceinline__ static int k_of(int i, int wave, int lane) { return (wave * COUNT + i) * (64 / PER) + lane / PER; }
 
   __device__ __forceinline__ void begin(const Operand& o, int64_t tile0, int64_t k0, int wave, int lane) {
     ld = o.ld;
-    last = o.last;
+    left = o.last - k0;
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
-      const int q = wave * COUNT + i;
       if constexpr (!COLUMNS) {
         // 8 rows of 128 bytes; 16-byte piece c of row r lies in place c ^ (r / 2 % 8), so that a read of 16 rows at one k meets every bank once
-        const int r = q * 8 + lane / 8, c = (lane % 8) ^ (r / 2 % 8);
-        p[i] = o.p + min(tile0 + r, last) * ld + k0 * S + c * 16;
+        const int r = (wave * COUNT + i) * 8 + lane / 8, c = (lane % 8) ^ (r / 2 % 8);
+        p[i] = o.p + min(tile0 + r, o.last) * ld + k0 * S + c * 16;
       } else {
-        constexpr int PER = R * S / 16;   // 16-byte pieces of a k
-        kr[i] = q * (64 / PER) + lane / PER;
-        const int c = (lane % PER) ^ (S == 2 ? group_swap<R>(kr[i]) << 2 : 0);
-        p[i] = o.p + min(tile0 * S + c * 16, o.edge);
+        const int k = k_of(i, wave, lane), c = (lane % PER) ^ turned<S, R>(k);
+        p[i] = o.p + (k0 + k) * ld + min(tile0 * S + c * 16, o.edge);
       }
     }
   }
-  // The stage at k0 into `to`; rows: k0 is the next one each time.
-  __device__ __forceinline__ void load(char* to, int64_t k0, int wave) {
+  // The next stage into `to`.
+  __device__ __forceinline__ void load(char* to, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) {
       const char* from = p[i];
-      if constexpr (COLUMNS) from += min(k0 + kr[i], last) * ld;
-      else p[i] += 128;
+      if (COLUMNS && left < kStep - 1) {
+        const int64_t behind = k_of(i, wave, lane) - left;
+        if (behind > 0) from -= behind * ld;   // the last k
+      }
       __builtin_amdgcn_global_load_lds(GLOBAL_PTR(from), LDS_PTR(void, to + (wave * COUNT + i) * 1024), 16, 0, 0);
+      p[i] += COLUMNS ? kStep * ld : 128;
     }
+    left -= kStep;
   }
 };
 
-// 32 rows (m or n, from row0) at the j-th quarter of a stage, as the matrix
-// instructions take them: lane l has row l % 32 and the k of half l / 32.
+// 16 rows (m or n, from row0) at half j of a stage, as the matrix instructions
+// take them: lane l has row l % 16 and quarter l / 16 of the half's 64 bytes of k.
 template <class T, bool COLUMNS, int R>
 __device__ __forceinline__ u32x4 fragment(const char* s, int row0, int j, int lane) {
-  const int l = lane % 32, h = lane / 32;
+  const int i = lane % 16, g = lane / 16;
   if constexpr (!COLUMNS) {
-    return *reinterpret_cast<const u32x4*>(s + (row0 + l) * 128 + (((2 * j + h) ^ (l / 2 % 8)) * 16));
+    return *reinterpret_cast<const u32x4*>(s + (row0 + i) * 128 + (((4 * j + g) ^ (i / 2 % 8)) * 16));
   } else if constexpr (sizeof(T) == 2) {
-    const int g = lane / 16, i = lane % 16;
-    const char* at = s + (16 * j + 8 * h + i / 4) * (2 * R) + ((((row0 / 32) ^ group_swap<R>(i / 4)) * 4 + (g & 1) * 2 + (i & 3) / 2) * 16 + (i & 1) * 8);
+    // 4 k of 16 columns a read: this lane's address is that of k i / 4 and columns i % 4 * 4, what it gets is column i
+    const int k = 32 * j + 8 * g + i / 4;
+    const char* at = s + k * (2 * R) + ((((row0 / 8) ^ turned<2, R>(k)) + (i & 3) / 2) * 16 + (i & 1) * 8);
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at));
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, at + 4 * (2 * R)));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(LDS_PTR(s16x4, s + (k + 4) * (2 * R) + ((((row0 / 8) ^ turned<2, R>(k + 4)) + (i & 3) / 2) * 16 + (i & 1) * 8)));
     return __builtin_bit_cast(u32x4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
-    const uint32_t* at = reinterpret_cast<const uint32_t*>(s + (8 * j + 4 * h) * (4 * R) + (row0 + l) * 4);
+    const int k = 16 * j + 4 * g;
+    const uint32_t* at = reinterpret_cast<const uint32_t*>(s + k * (4 * R) + (((row0 / 4) ^ turned<4, R>(k)) * 16 + i * 4));
     u32x4 v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = at[e * R];
@@ -135,85 +145,103 @@ __device__ __forceinline__ u32x4 fragment(const char* s, int row0, int j, int la
 }
 
 template <class C>
-using Acc = f32x16[C::FM][C::FN];
+using Acc = f32x4[C::FM][C::FN];
 
-// A wave's fragments of a quarter of a stage.
-template <class T, bool AC, bool BC, class C>
-struct Fragments {
-  u32x4 a[C::FM], b[C::FN];
-  __device__ __forceinline__ void read(const char* stage, int j, int wm, int wn, int lane) {
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i) a[i] = fragment<T, AC, C::M>(stage, (wm * C::FM + i) * 32, j, lane);
-#pragma unroll
-    for (int i = 0; i < C::FN; ++i) b[i] = fragment<T, BC, C::N>(stage + C::M * 128, (wn * C::FN + i) * 32, j, lane);
-  }
-  __device__ __forceinline__ void multiply_into(Acc<C>& acc) const {
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-      for (int k = 0; k < C::FN; ++k) multiply<T>(acc[i][k], a[i], b[k]);
-  }
-};
-
-// acc = the block's product over `steps` stages from k0.  Fragments are read a
-// quarter ahead, the next stage's first ones while the matrix instructions
-// of this one's last quarter run: the barrier between stages stands before
-// those, and the stage after the next goes where this one was read.  All of LDS is read when it returns.
+// acc = the block's product over `steps` stages from k0.  A stage is four steps:
+// both halves of k times both halves of a wave's rows of m, whose fragments are
+// read a step ahead, between the matrix instructions; the next stage's first
+// ones during this one's last step, so the barrier between stages stands before
+// that.  The loads of a stage go out in two parts, B's a step and a half after
+// A's.  (8192 x 32000 x 2048 bf16 on one unit: 914 us with reads and loads each
+// at once, 864 with the reads between, 852 with the loads after the step, 800 with
+// them in two parts.  A fragment more in registers and a longer way for the loads: no less.)
+// All of LDS is read when it returns.
 template <class T, bool AC, bool BC, class C>
 __device__ __forceinline__ void product(Acc<C>& acc, const Operand& a, const Operand& b, int64_t m0, int64_t n0, int64_t k0, int64_t steps, char* lds) {
-  constexpr int kStep = 128 / int(sizeof(T));
+  constexpr int HM = C::FM / 2;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, wm = wave % C::WM, wn = wave / C::WM;
 #pragma unroll
   for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-    for (int k = 0; k < C::FN; ++k)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][k][e] = 0.f;
+    for (int k = 0; k < C::FN; ++k) acc[i][k] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (steps <= 0) return;
   Loader<T, AC, C::M, C::WAVES> la;
   Loader<T, BC, C::N, C::WAVES> lb;
   la.begin(a, m0, k0, wave, lane);
   lb.begin(b, n0, k0, wave, lane);
-  const auto load = [&](int64_t s) {
-    char* to = lds + (s & 1) * C::STAGE;
-    la.load(to, k0 + s * kStep, wave);
-    lb.load(to + C::M * 128, k0 + s * kStep, wave);
+  const auto load_a = [&](int64_t s) { la.load(lds + (s & 1) * C::STAGE, wave, lane); };
+  const auto load_b = [&](int64_t s) { lb.load(lds + (s & 1) * C::STAGE + C::M * 128, wave, lane); };
+  u32x4 fa[2][HM], fb[2][C::FN];
+  const auto read_a = [&](u32x4 (&f)[HM], const char* stage, int j, int half) {
+#pragma unroll
+    for (int i = 0; i < HM; ++i) f[i] = fragment<T, AC, C::M>(stage, (wm * C::FM + half * HM + i) * 16, j, lane);
   };
-  Fragments<T, AC, BC, C> f[2];
-  load(0);
+  const auto read_b = [&](u32x4 (&f)[C::FN], const char* stage, int j) {
+#pragma unroll
+    for (int i = 0; i < C::FN; ++i) f[i] = fragment<T, BC, C::N>(stage + C::M * 128, (wn * C::FN + i) * 16, j, lane);
+  };
+  const auto step = [&](int j, int half) {
+#pragma unroll
+    for (int i = 0; i < HM; ++i)
+#pragma unroll
+      for (int k = 0; k < C::FN; ++k) multiply<T>(acc[half * HM + i][k], fa[half][i], fb[j][k]);
+#pragma unroll
+    for (int q = 0; q < HM * C::FN / 4; ++q) {   // four matrix instructions, two fragments
+      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, (AC || BC) && sizeof(T) == 2 ? 4 : 2, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load_a(0);
+  load_b(0);
   __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the stage is there
   __syncthreads();
-  if (steps > 1) load(1);
-  f[0].read(lds, 0, wm, wn, lane);
+  if (steps > 1) {
+    load_a(1);
+    load_b(1);
+  }
+  read_b(fb[0], lds, 0);
+  read_a(fa[0], lds, 0, 0);
   for (int64_t s = 0; s < steps; ++s) {
-    const char* now = lds + (s & 1) * C::STAGE;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      f[(j + 1) & 1].read(now, j + 1, wm, wn, lane);
-      __builtin_amdgcn_sched_barrier(0);
-      f[j & 1].multiply_into(acc);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    const char *now = lds + (s & 1) * C::STAGE, *next = lds + (~s & 1) * C::STAGE;
+    read_a(fa[1], now, 0, 1);
+    step(0, 0);
+    if (s > 0 && s + 1 < steps) load_b(s + 1);
+    read_b(fb[1], now, 1);
+    read_a(fa[0], now, 1, 0);
+    step(0, 1);
+    read_a(fa[1], now, 1, 1);
+    step(1, 0);
     __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0): the next stage is there, this one is read
     __syncthreads();
-    if (s + 2 < steps) load(s + 2);
-    if (s + 1 < steps) f[0].read(lds + (~s & 1) * C::STAGE, 0, wm, wn, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    f[1].multiply_into(acc);
-    __builtin_amdgcn_sched_barrier(0);
+    if (s + 1 < steps) {
+      read_b(fb[0], next, 0);
+      read_a(fa[0], next, 0, 0);
+    }
+    step(1, 1);
+    if (s + 2 < steps) load_a(s + 2);
   }
 }
 
 // Element e of acc[i][k] is C[m][n] with these, from the block's first.
 template <class C>
 __device__ __forceinline__ int tile_m(int i, int e) {
-  const int wave = threadIdx.x >> 6, h = (threadIdx.x & 63) / 32;
-  return ((wave % C::WM) * C::FM + i) * 32 + 8 * (e / 4) + 4 * h + e % 4;
+  const int wave = threadIdx.x >> 6;
+  return ((wave % C::WM) * C::FM + i) * 16 + (threadIdx.x & 63) / 16 * 4 + e;
 }
 template <class C>
 __device__ __forceinline__ int tile_n(int k) {
   const int wave = threadIdx.x >> 6;
-  return ((wave / C::WM) * C::FN + k) * 32 + threadIdx.x % 32;
+  return ((wave / C::WM) * C::FN + k) * 16 + threadIdx.x % 16;
+}
+
+// Over the four lanes with one n.
+template <class Op>
+__device__ __forceinline__ float rows_reduce(float x, Op op) {
+  const Two a = swap16(x);
+  x = op(a.a, a.b);
+  const Two b = swap32(x);
+  return op(b.a, b.b);
 }
 
 // A block's tile.  Blocks go to the eight dies in turn, each with a cache of its
@@ -272,7 +300,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_stats(Stats a) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
+      for (int e = 0; e < 4; ++e)
         if (v0 + tile_m<C>(i, e) >= a.vend)
 #pragma unroll
           for (int k = 0; k < C::FN; ++k) acc[i][k][e] = -INFINITY;
@@ -288,25 +316,23 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_stats(Stats a) {
 #pragma unroll
       for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 4; ++e)
           if (here && at == tile_m<C>(i, e)) a.hit[tok] = acc[i][k][e];
     }
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[i][k][e]);
-    const Two both = swap32(m);
-    m = fmaxf(both.a, both.b);
+      for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][k][e]);
+    m = rows_reduce(m, Max());
     const float mc = m == -INFINITY ? 0.f : m;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s += exp2_hw((acc[i][k][e] - mc) * kLog2e);
-    const Two sums = swap32(s);
-    s = sums.a + sums.b;
-    if ((threadIdx.x & 63) < 32) red[wave % C::WM][tile_n<C>(k)] = make_float2(m, s);
+      for (int e = 0; e < 4; ++e) s += exp2_hw((acc[i][k][e] - mc) * kLog2e);
+    s = rows_reduce(s, Add());
+    if ((threadIdx.x & 63) < 16) red[wave % C::WM][tile_n<C>(k)] = make_float2(m, s);
   }
   __syncthreads();
   if (threadIdx.x < C::N && n0 + threadIdx.x < a.n) {
@@ -464,19 +490,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_grad(Grad a) {
     const int64_t target = r.target - v0;
     T* out = static_cast<T*>(a.out) + tok * a.width + m0;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+    for (int i = 0; i < C::FM; ++i) {
+      const int m = tile_m<C>(i, 0);
+      Pack<T, 4> p;
 #pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int m = tile_m<C>(i, e);
-        Pack<T, 4> p;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // a probability is at most 1, whatever half a step of a large lse is (NaN stays NaN)
-          const float x = exp2_hw(__builtin_elementwise_minimum(fmaf(acc[i][k][e + q], kLog2e, -r.lse), 0.f));
-          p.v[q] = from_f32<T>(v0 + m + q < a.vend ? r.g * (x - (target == m + q ? 1.f : 0.f)) : 0.f);
-        }
-        *reinterpret_cast<Pack<T, 4>*>(out + m) = p;
+      for (int e = 0; e < 4; ++e) {
+        // a probability is at most 1, whatever half a step of a large lse is (NaN stays NaN)
+        const float x = exp2_hw(__builtin_elementwise_minimum(fmaf(acc[i][k][e], kLog2e, -r.lse), 0.f));
+        p.v[e] = from_f32<T>(v0 + m + e < a.vend ? r.g * (x - (target == m + e ? 1.f : 0.f)) : 0.f);
       }
+      *reinterpret_cast<Pack<T, 4>*>(out + m) = p;
+    }
   }
 }
 
@@ -515,16 +539,12 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_sums(Sums a) {
   for (int k = 0; k < C::FN; ++k) {
     float* out = a.out + z * a.pitch + (n0 + tile_n<C>(k)) * a.ldo;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        const int64_t m = m0 + tile_m<C>(i, e);
-        if (m >= a.ldo) continue;
-        f32x4 v = {acc[i][k][e], acc[i][k][e + 1], acc[i][k][e + 2], acc[i][k][e + 3]};
-        f32x4* to = reinterpret_cast<f32x4*>(out + m);
-        if (a.add) v += *to;
-        *to = v;
-      }
+    for (int i = 0; i < C::FM; ++i) {
+      const int64_t m = m0 + tile_m<C>(i, 0);
+      if (m >= a.ldo) continue;
+      f32x4* to = reinterpret_cast<f32x4*>(out + m);
+      *to = a.add ? acc[i][k] + *to : acc[i][k];
+    }
   }
 }
 
@@ -555,17 +575,15 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_weight(WeightGrad a) {
       if (r >= a.rows) continue;
       W* out = static_cast<W*>(a.out) + r * a.ldo;
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
+      for (int i = 0; i < C::FM; ++i) {
+        const int64_t m = m0 + tile_m<C>(i, 0);
+        if (m >= a.cols) continue;
+        Pack<W, 4> p;
+        if (a.accumulate) p = load_pack<W, 4>(out, m, a.cols);
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          const int64_t m = m0 + tile_m<C>(i, e);
-          if (m >= a.cols) continue;
-          Pack<W, 4> p;
-          if (a.accumulate) p = load_pack<W, 4>(out, m, a.cols);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) p.v[q] = from_f32<W>((a.accumulate ? to_f32(p.v[q]) : 0.f) + inv * acc[i][k][e + q]);
-          store_pack<W, 4>(out, m, a.cols, p);
-        }
+        for (int e = 0; e < 4; ++e) p.v[e] = from_f32<W>((a.accumulate ? to_f32(p.v[e]) : 0.f) + inv * acc[i][k][e]);
+        store_pack<W, 4>(out, m, a.cols, p);
+      }
     }
   };
   if (a.dtype == kF32) write(float());
@@ -653,9 +671,8 @@ uint32_t count(int64_t x, bool m) { return uint32_t((x + (m ? C::M : C::N) - 1) 
 struct Plan {
   int64_t s, np, dp;             // element bytes; tokens and columns filled up
   int64_t width;                 // of a piece of the vocabulary
-  int logits;                    // tiles
+  Shape sx;                      // of dx: its splits are kept from piece to piece
   int64_t parts;                 // tiles of the vocabulary
-  Shape sx, sw;
   int64_t bytes = 0;
   int64_t take(int64_t n) {
     const int64_t at = bytes;
@@ -664,6 +681,9 @@ struct Plan {
   }
   int64_t part, hit, x, w, head, rows, pos, g, sum_x, sum_w;
 };
+
+Shape x_shape(const Plan& p, int64_t n, int64_t width) { return split_tile(p.dp, n, width * p.s / 128); }
+Shape w_shape(const Plan& p, int64_t rows) { return split_tile(p.dp, rows, p.np * p.s / 128); }
 
 constexpr int64_t kPieceBytes = int64_t(128) << 20;   // of G, or of a piece of the weight that is laid out anew
 
@@ -675,13 +695,16 @@ Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) 
   const int64_t all = up(vocab, kTile);
   const int64_t most = std::max(backward ? p.np : 0, p.dp) * p.s;
   p.width = std::min(all, std::max<int64_t>(kPieceBytes / most / kTile, 4) * kTile);
-  const int64_t pieces = (all + p.width - 1) / p.width;   // of one length
-  p.width = up((vocab + pieces - 1) / pieces, kTile);
-  p.logits = whole_tile(std::min(vocab, p.width), n);
+  if (p.width < all && backward) {
+    // whole rounds of tiles: their number, times the tokens' tiles, a multiple of the compute units
+    int64_t tiles = p.width / kTile, whole = kUnits;
+    for (int64_t nt = p.np / kTile; nt % 2 == 0 && whole > 1; nt /= 2) whole /= 2;
+    if (tiles > whole) p.width = tiles / whole * whole * kTile;
+  }
   p.x = p.take(p.np * p.dp * p.s);
   p.w = p.take(p.width * p.dp * p.s);
   if (!backward) {
-    p.parts = all / (256 >> p.logits);
+    p.parts = all / (256 >> kSmall);
     p.part = p.take(p.parts * p.np * 8);
     p.hit = p.take(n * 4);
     return p;
@@ -690,10 +713,15 @@ Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) 
   p.rows = p.take(p.np * int64_t(sizeof(Row)));
   p.pos = p.take(n * 4);
   p.g = p.take(p.np * p.width * p.s);
-  p.sx = split_tile(p.dp, n, p.width * p.s / 128);
-  p.sw = split_tile(p.dp, std::min(vocab, p.width), p.np * p.s / 128);
+  p.sx = x_shape(p, n, p.width);
   p.sum_x = p.take(p.sx.splits * p.np * p.dp * 4);
-  p.sum_w = p.sw.splits > 1 ? p.take(p.sw.splits * p.width * p.dp * 4) : 0;
+  // the pieces and the last one
+  int64_t most_w = 0;
+  for (const int64_t rows : {std::min(vocab, p.width), (vocab - 1) % p.width + 1}) {
+    const Shape w = w_shape(p, rows);
+    if (w.splits > 1) most_w = std::max(most_w, w.splits * up(rows, kTile) * p.dp * 4);
+  }
+  p.sum_w = p.take(most_w);
   return p;
 }
 
@@ -727,6 +755,7 @@ hipError_t forward(const LinearCeForward& a, hipStream_t s) {
   }
   const bool whole = direct(a.w, a.ldw, a.cols, p.s);
   const int64_t width = whole ? a.vocab : p.width;
+  const int tile = whole_tile(std::min(a.vocab, width), a.rows);
   for (int64_t v0 = 0; v0 < a.vocab; v0 += width) {
     const int64_t rows = std::min(width, a.vocab - v0);
     const char* w = static_cast<const char*>(a.w) + v0 * a.ldw * p.s;
@@ -738,14 +767,14 @@ hipError_t forward(const LinearCeForward& a, hipStream_t s) {
     }
     g.v0 = v0;
     g.vend = v0 + rows;
-    with_tile(p.logits, [&](auto c) {
+    with_tile(tile, [&](auto c) {
       using C = decltype(c);
       g.mt = count<C>(rows, true);
       g.nt = count<C>(a.rows, false);
       k_ce_stats<T, C><<<dim3(g.mt * g.nt), dim3(C::THREADS), 0, s>>>(g);
     });
   }
-  const int64_t parts = (a.vocab + (256 >> p.logits) - 1) / (256 >> p.logits);
+  const int64_t parts = (a.vocab + (256 >> tile) - 1) / (256 >> tile);
   k_ce_loss<<<dim3(unsigned((a.rows + 31) / 32)), dim3(1024), 0, s>>>(g.part, parts, p.np, a.rows, a.vocab, a.targets, a.id_bytes, g.hit, a.loss, a.lse);
   return hipGetLastError();
 }
@@ -786,7 +815,7 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
     g.width = p.width;
     g.steps = p.dp * p.s / 128;
     // whole tiles of any size: what the sums below read of G is written
-    with_tile(p.logits, [&](auto c) {
+    with_tile(whole_tile(n, a.rows), [&](auto c) {
       using C = decltype(c);
       g.mt = count<C>(up(n, kTile), true);
       g.nt = count<C>(p.np, false);
@@ -813,16 +842,17 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
     if (a.dw) {
       const Operand gc{G, p.width * p.s, p.np - 1, p.width * p.s - 16};
       char* out = static_cast<char*>(a.dw) + v0 * a.lddw * size_of(a.gdtype);
-      if (p.sw.splits > 1) {
+      const Shape shape = w_shape(p, n);
+      if (shape.splits > 1) {
         Sums q{};
         q.a = xc;
         q.b = gc;
         q.head = head;
         q.out = sum_w;
         q.ldo = p.dp;
-        q.pitch = p.width * p.dp;
-        q.splits = p.sw.splits;
-        with_tile(p.sw.tile, [&](auto c) {
+        q.pitch = up(n, kTile) * p.dp;
+        q.splits = shape.splits;
+        with_tile(shape.tile, [&](auto c) {
           using C = decltype(c);
           q.mt = count<C>(p.dp, true);
           q.nt = count<C>(n, false);
@@ -842,7 +872,7 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
         q.cols = a.cols;
         q.dtype = a.gdtype;
         q.accumulate = a.accumulate;
-        with_tile(p.sw.tile, [&](auto c) {
+        with_tile(shape.tile, [&](auto c) {
           using C = decltype(c);
           q.mt = count<C>(p.dp, true);
           q.nt = count<C>(n, false);
