@@ -26,6 +26,8 @@
 // element's number.  A v that is not 0 does not round to 0, as its root divides.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+
 #include <algorithm>
 #include <cmath>
 
@@ -59,37 +61,35 @@ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 }
 
 struct Highest {   // of non-negative floats by their bits, a NaN above all
-  __device__ __forceinline__ float operator()(float a, float b) const {
-    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-    return __uint_as_float(x > y ? x : y);
-  }
+  __device__ __forceinline__ float operator()(float a, float b) const { return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))); }
 };
 
-// Codes of FIELDS exponents over 3 bits of mantissa.
+// Codes of FIELDS exponents over 3 bits of mantissa, as the highest bits of a
+// float: scaled by 2^kScale and the block's exponent, a code's exponent is the
+// float's own field, and numbers below the least exponent are denormal floats
+// as they are among the codes.
 template <int FIELDS>
 struct Codes {
+  static constexpr int kScale = 128 - FIELDS;
   // Exponent of a block whose largest number is `top`: the next one where top could round up out of the codes.
   static __device__ __forceinline__ int exponent(float top) {
     const int e = int((__float_as_uint(top) + 0x100000u) >> 23) - 127;
-    return e < -100 ? -100 : e > 127 ? 127 : e;
+    return min(max(e, -100), 127);
   }
-  // x >= 0, r: 16 random bits
-  static __device__ __forceinline__ uint32_t encode(float x, int e, uint32_t r) {
-    const float y = __builtin_ldexpf(x, -e);
-    const uint32_t normal = ((__float_as_uint(y) + (r << 4)) >> 20) - uint32_t((128 - FIELDS) << 3);
-    const uint32_t small = uint32_t(__builtin_ldexpf(y, FIELDS + 1) + __builtin_ldexpf(float(r), -16));
-    constexpr float least = 1.f / float(1u << (FIELDS - 2));   // of the codes with a hidden bit
-    return std::min(y >= least ? normal : small, uint32_t(FIELDS * 8 - 1));   // a float's own highest binade has none above
-  }
-  static __device__ __forceinline__ float decode(uint32_t code, int e) {
-    const int f = int(code >> 3);
-    const uint32_t man = f ? (code & 7) | 8 : code & 7;
-    return __builtin_ldexpf(float(man), (f ? f : 1) - FIELDS - 2 + e);
-  }
+  // The code of x >= 0 before it is held to those that there are; r: random bits, 16 of them under the code's last bit.
+  static __device__ __forceinline__ uint32_t encode(float x, int e, uint32_t r) { return (__float_as_uint(__builtin_ldexpf(x, -e - kScale)) + (r << 4)) >> 20; }
+  // bits: the code in its place, from bit 20 on
+  static __device__ __forceinline__ float decode(uint32_t bits, int e) { return __builtin_ldexpf(__uint_as_float(bits), e + kScale); }
 };
 typedef Codes<16> CodesM;
 typedef Codes<32> CodesV;
 constexpr uint32_t kNotANumber = 255;   // of a block's exponent: a NaN or an infinity is in it
+
+// Byte k of x, its low 7 or 8 bits, from bit 20 on.
+template <int K, uint32_t MASK>
+__device__ __forceinline__ uint32_t from_byte(uint32_t x) {
+  return (K < 2 ? x << (20 - 8 * K) : K == 2 ? x << 4 : x >> 4) & MASK << 20;
+}
 
 struct Factors {
   float size;   // 1 / (1 - b1^t)
@@ -152,15 +152,24 @@ struct Moments<8> {
     e = *reinterpret_cast<const uint32_t*>(s + 2 * kMomentBlock);
   }
   __device__ __forceinline__ void open() {
-    const uint32_t bm = e & 255, bv = e >> 8 & 255;
-    const int em = int(bm) - 100, ev = int(bv) - 100;
+    const uint32_t both = __builtin_amdgcn_readfirstlane(e), bm = both & 255, bv = both >> 8 & 255;
+    open_one<0>(int(bm) - 100, int(bv) - 100);
+    open_one<1>(int(bm) - 100, int(bv) - 100);
+    open_one<2>(int(bm) - 100, int(bv) - 100);
+    open_one<3>(int(bm) - 100, int(bv) - 100);
+    if (bm == kNotANumber || bv == kNotANumber) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t c = cm >> 8 * k & 255;
-      const float x = CodesM::decode(c & 127, em);
-      m[k] = bm == kNotANumber ? NAN : c & 128 ? -x : x;
-      v[k] = bv == kNotANumber ? NAN : CodesV::decode(cv >> 8 * k & 255, ev);
+      for (int k = 0; k < 4; ++k) {
+        if (bm == kNotANumber) m[k] = NAN;
+        if (bv == kNotANumber) v[k] = NAN;
+      }
     }
+  }
+  template <int K>
+  __device__ __forceinline__ void open_one(int em, int ev) {
+    const float x = CodesM::decode(from_byte<K, 127>(cm), em);
+    m[K] = __uint_as_float(__float_as_uint(x) | (cm << (24 - 8 * K) & 0x80000000u));
+    v[K] = CodesV::decode(from_byte<K, 255>(cv), ev);
   }
   template <bool ONCE>
   __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t key, int64_t i) const {
@@ -174,17 +183,18 @@ struct Moments<8> {
     tv = lanes_reduce<64>(tv, Highest());
     const bool bm = !(tm < INFINITY), bv = !(tv < INFINITY);
     const int em = bm ? 0 : CodesM::exponent(tm), ev = bv ? 0 : CodesV::exponent(tv);
-    uint32_t pm = 0, pv = 0;
+    // 0x9E3779B9 times the upper half: the same for the block
+    const uint32_t base = key + uint32_t(i) + 0x9E3779B9u * uint32_t(uint64_t(i) >> 32);
+    uint32_t pm = 0, pv = 0, signs = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint64_t at = uint64_t(i + k);
-      const uint32_t r = mix(key + uint32_t(at) + 0x9E3779B9u * uint32_t(at >> 32));
-      const uint32_t a = CodesM::encode(fabsf(m[k]), em, r & 0xFFFF);
-      uint32_t b = CodesV::encode(v[k], ev, r >> 16);
-      b = v[k] > 0.f && b == 0 ? 1 : b;
-      pm |= (a | (m[k] < 0.f && a ? 128u : 0u)) << 8 * k;
-      pv |= b << 8 * k;
+      const uint32_t r = mix(base + k);
+      pm |= min(CodesM::encode(fabsf(m[k]), em, r & 0xFFFF), 127u) << 8 * k;
+      signs |= (__float_as_uint(m[k]) >> 24 & 128) << 8 * k;
+      // a v that is not 0 has a code that is not
+      pv |= min(max(CodesV::encode(v[k], ev, r >> 16), min(__float_as_uint(v[k]), 1u)), 255u) << 8 * k;
     }
+    pm |= signs & (pm + 0x7F7F7F7Fu);   // no sign without a code
     reinterpret_cast<uint32_t*>(s)[lane] = bm ? 0u : pm;
     reinterpret_cast<uint32_t*>(s + kMomentBlock)[lane] = bv ? 0u : pv;
     if (lane == 0)
@@ -217,7 +227,9 @@ __device__ __forceinline__ void chunk_step(const AdamwLaunch& a, const AdamwEntr
         float &m = mo[b].m[k], &v = mo[b].v[k];
         m = weighted(m, a.b1, xg[b][k], a.c1);
         v = weighted(v, a.b2, square(xg[b][k]), a.c2);
-        xp[b][k] = xp[b][k] * t.decay - size * m / (sqrtf(v) * f.root + a.eps);
+        // root and quotient of the hardware, one step off each; a v below the least normal float counts as that
+        const float d = __builtin_amdgcn_sqrtf(__builtin_elementwise_maximum(v, FLT_MIN)) * f.root + a.eps;
+        xp[b][k] = xp[b][k] * t.decay - size * m * __builtin_amdgcn_rcpf(d);
       }
       store4<P, FULL, ONCE>(p, i0 + b * kMomentBlock, t.n, xp[b]);
       mo[b].template store<ONCE>(s + b * Moments<BITS>::kBytes, lane, key, i0 + b * kMomentBlock);
