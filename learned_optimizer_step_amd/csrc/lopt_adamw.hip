@@ -11,8 +11,9 @@
 // fill the same grid.
 //
 // The step counter is on the device, so that a captured step counts as it is
-// replayed: every wave reads it first, and the last block of the last launch to
-// finish (a ticket) advances it.
+// replayed: every wave reads it first.  A short last launch advances it itself, by
+// its last block to finish (a ticket: some 40 ns a block, one after the other;
+// 2048 of them took 60 us of 547); behind a longer one a launch of one thread does.
 //
 // 8-bit moments: a block of 256 numbers shares an exponent e, which puts its
 // largest in the highest binade of the codes.  m has a sign, 4 bits of exponent
@@ -30,6 +31,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "lopt_ops.h"
 #include "lopt_ops_device.h"
@@ -37,8 +39,13 @@
 namespace lopt {
 namespace {
 
-constexpr int kPerLane = 4, kBlocks = 4;
-constexpr int kChunk = 64 * kPerLane * kBlocks;   // 4 of the moments' blocks
+// A wave's chunk is two of the moments' blocks, and a list gets a wave for every
+// chunk (ViT-B/16 fp32: 408 us, 439 with 2048 blocks of four-block chunks in a
+// loop; GPT-2 355M with 8-bit moments and their decoding 1447, 1540).
+constexpr int kPerLane = 4, kBlocks = 2;
+constexpr unsigned kMostTickets = 64;   // blocks
+constexpr unsigned kMostBlocks = 1u << 24;   // of 256 threads: a grid has room for 2^32 threads
+constexpr int kChunk = 64 * kPerLane * kBlocks;
 static_assert(kMomentBlock == 64 * kPerLane, "a wave holds a block of moments");
 static_assert(sizeof(AdamwLaunch) <= 4096, "kernel arguments");
 
@@ -272,16 +279,24 @@ __global__ __launch_bounds__(256) void k_adamw(AdamwLaunch a) {
   }
 }
 
-template <class T, int BITS>
+__global__ void k_adamw_advance(unsigned long long* step) { *step += 1; }
+
+template <class T, int BITS, bool ONCE>
 __global__ __launch_bounds__(256) void k_adamw_moments(const unsigned char* s, int64_t n, T* m, T* v) {
   const int lane = threadIdx.x & 63;
   const int64_t blocks = (n + kMomentBlock - 1) / kMomentBlock;
   for (int64_t b = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6); b < blocks; b += int64_t(gridDim.x) * 4) {
     Moments<BITS> mo;
-    mo.template load<false>(s + b * Moments<BITS>::kBytes, lane);
+    mo.template load<ONCE>(s + b * Moments<BITS>::kBytes, lane);
     mo.open();
-    if (m) store4<T, false, false>(m, b * kMomentBlock + lane * 4, n, mo.m);
-    if (v) store4<T, false, false>(v, b * kMomentBlock + lane * 4, n, mo.v);
+    const int64_t at = b * kMomentBlock + lane * 4;
+    if ((b + 1) * kMomentBlock <= n) {
+      if (m) store4<T, true, ONCE>(m, at, n, mo.m);
+      if (v) store4<T, true, ONCE>(v, at, n, mo.v);
+    } else {
+      if (m) store4<T, false, false>(m, at, n, mo.m);
+      if (v) store4<T, false, false>(v, at, n, mo.v);
+    }
   }
 }
 
@@ -296,11 +311,13 @@ hipError_t with_type(int32_t dtype, F&& f) {
 
 int64_t adamw_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 
-hipError_t launch_adamw(const AdamwLaunch& a, int32_t pdtype, int32_t gdtype, int32_t bits, bool once, hipStream_t s) {
-  // four blocks of a compute unit hide its memory's latency; a small list gets a wave for every chunk
+hipError_t launch_adamw(const AdamwLaunch& args, int32_t pdtype, int32_t gdtype, int32_t bits, bool once, hipStream_t s) {
+  AdamwLaunch a = args;
   const int64_t need = (int64_t(a.first[a.count]) + 3) / 4;
-  const dim3 grid(unsigned(std::max<int64_t>(1, std::min<int64_t>(need, 2048))));
-  return with_type(pdtype, [&](auto p) {
+  const dim3 grid(unsigned(std::max<int64_t>(1, std::min<int64_t>(need, kMostBlocks - 1))));
+  const bool behind = a.advance && grid.x > kMostTickets;
+  if (behind) a.advance = 0;
+  const hipError_t e = with_type(pdtype, [&](auto p) {
     return with_type(gdtype, [&](auto g) {
       using P = decltype(p);
       using G = decltype(g);
@@ -314,16 +331,24 @@ hipError_t launch_adamw(const AdamwLaunch& a, int32_t pdtype, int32_t gdtype, in
       return hipGetLastError();
     });
   });
+  if (e != hipSuccess || !behind) return e;
+  k_adamw_advance<<<dim3(1), dim3(1), 0, s>>>(a.step);
+  return hipGetLastError();
 }
 
 hipError_t launch_adamw_moments(const void* state, int64_t n, int32_t bits, int32_t dtype, void* m, void* v, hipStream_t s) {
   const int64_t blocks = (n + kMomentBlock - 1) / kMomentBlock;
-  const dim3 grid(unsigned(std::min<int64_t>((blocks + 3) / 4, 8192)));
+  const dim3 grid(unsigned(std::min<int64_t>((blocks + 3) / 4, kMostBlocks - 1)));
+  const bool once = n > 50'000'000;
   return with_type(dtype, [&](auto t) {
     using T = decltype(t);
     const unsigned char* p = static_cast<const unsigned char*>(state);
-    if (bits == 32) k_adamw_moments<T, 32><<<grid, dim3(256), 0, s>>>(p, n, static_cast<T*>(m), static_cast<T*>(v));
-    else k_adamw_moments<T, 8><<<grid, dim3(256), 0, s>>>(p, n, static_cast<T*>(m), static_cast<T*>(v));
+    const auto run = [&](auto bits) {
+      if (once) k_adamw_moments<T, bits(), true><<<grid, dim3(256), 0, s>>>(p, n, static_cast<T*>(m), static_cast<T*>(v));
+      else k_adamw_moments<T, bits(), false><<<grid, dim3(256), 0, s>>>(p, n, static_cast<T*>(m), static_cast<T*>(v));
+    };
+    if (bits == 32) run(std::integral_constant<int, 32>());
+    else run(std::integral_constant<int, 8>());
     return hipGetLastError();
   });
 }
