@@ -31,17 +31,21 @@ void with_residual_mode(int64_t n, F&& f) {
   f(std::integral_constant<int, kTail>());
 }
 
-// The thread's elements of a row, 0 where they are not its own.
+// The thread's vectors of a row as they are loaded, and their elements, 0 where they are not its own.
 template <class T, class At>
-__device__ __forceinline__ void load_row(const At& at, const T* row, float (&x)[At::NV * At::V]) {
+struct RowPacks {
   Pack<T, At::V> p[At::NV];
+  __device__ __forceinline__ void load(const At& at, const T* row) {
 #pragma unroll
-  for (int k = 0; k < At::NV; ++k) p[k] = at[k].load(row);
+    for (int k = 0; k < At::NV; ++k) p[k] = at[k].load(row);
+  }
+  __device__ __forceinline__ void open(const At& at, float (&x)[At::NV * At::V]) const {
 #pragma unroll
-  for (int k = 0; k < At::NV; ++k)
+    for (int k = 0; k < At::NV; ++k)
 #pragma unroll
-    for (int i = 0; i < At::V; ++i) x[k * At::V + i] = at[k].own(i) ? to_f32(p[k].v[i]) : 0.f;
-}
+      for (int i = 0; i < At::V; ++i) x[k * At::V + i] = at[k].own(i) ? to_f32(p[k].v[i]) : 0.f;
+  }
+};
 template <class T, class At>
 __device__ __forceinline__ void store_row(const At& at, T* row, const float (&x)[At::NV * At::V]) {
 #pragma unroll

@@ -6,8 +6,8 @@
 // and over the rows dw2 = sum dz hh, db2 = sum dz, dw1 = sum du yh, db1 = sum du
 // and a gate vector's sum of dgate.
 // Bound by HBM: dh, dz, y, h (and a gate matrix) are read once, dx and dy (and
-// the matrix's gradient) written once.  Each thread adds up its columns' sums over
-// the rows of its block in registers; the blocks' sums go to the workspace and a
+// the matrix's gradient) written once; a block's next row is loaded before the sums of this one.  Each thread adds up its columns'
+// sums over the rows of its block in registers; the blocks' sums go to the workspace and a
 // second kernel adds them in the order of the blocks: the same bits every time.
 #include <hip/hip_runtime.h>
 
@@ -40,19 +40,38 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_backward(ResidualBackward
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[k][e] = 0.f;
 
-  const int64_t stride = int64_t(gridDim.x) * L::ROWS;
-  for (int64_t r0 = int64_t(blockIdx.x) * L::ROWS; r0 < a.rows; r0 += stride) {
+  struct Row {
+    RowPacks<T, RowAt<T, L, MODE>> y, h, dh, dz, gate;
+    float mean1, rstd1, mean2, rstd2;
+  };
+  const auto load = [&](int64_t r0) {
+    const int64_t r = r0 + threadIdx.x / L::TPR, rr = r < a.rows ? r : 0;
+    Row p;
+    p.y.load(at, static_cast<const T*>(a.y) + rr * a.ldy);
+    if (PRE) p.h.load(at, static_cast<const T*>(a.h) + rr * a.ldh);
+    if (a.dh) p.dh.load(at, static_cast<const T*>(a.dh) + rr * a.lddh);
+    if (PRE && a.dz) p.dz.load(at, static_cast<const T*>(a.dz) + rr * a.lddz);
+    if (a.gate_kind == kGateMatrix) p.gate.load(at, static_cast<const T*>(a.gate) + rr * a.ldg);
+    p.mean1 = POST && !RMS ? a.stats[rr] : 0.f;
+    p.rstd1 = POST ? a.stats[a.rows + rr] : 0.f;
+    p.mean2 = PRE && !RMS ? a.stats[2 * a.rows + rr] : 0.f;
+    p.rstd2 = PRE ? a.stats[3 * a.rows + rr] : 0.f;
+    return p;
+  };
+  const int64_t stride = int64_t(gridDim.x) * L::ROWS, first = int64_t(blockIdx.x) * L::ROWS;
+  Row next = load(first);
+  for (int64_t r0 = first; r0 < a.rows; r0 += stride) {
     const int64_t r = r0 + threadIdx.x / L::TPR;
     const bool row = L::ROWS == 1 || r < a.rows;
-    const int64_t rr = row ? r : 0;
+    const Row now = next;
+    if (r0 + stride < a.rows) next = load(r0 + stride);
     float d[E], y[E], h[E], dz[E];
-    load_row(at, static_cast<const T*>(a.y) + rr * a.ldy, y);
-    if (PRE) load_row(at, static_cast<const T*>(a.h) + rr * a.ldh, h);
-    if (a.dh) load_row(at, static_cast<const T*>(a.dh) + rr * a.lddh, d);
-    if (PRE && a.dz) load_row(at, static_cast<const T*>(a.dz) + rr * a.lddz, dz);
-    if (a.gate_kind == kGateMatrix) load_row(at, static_cast<const T*>(a.gate) + rr * a.ldg, gate);
-    const float mean1 = POST && !RMS ? a.stats[rr] : 0.f, rstd1 = POST ? a.stats[a.rows + rr] : 0.f;
-    const float mean2 = PRE && !RMS ? a.stats[2 * a.rows + rr] : 0.f, rstd2 = PRE ? a.stats[3 * a.rows + rr] : 0.f;
+    now.y.open(at, y);
+    if (PRE) now.h.open(at, h);
+    if (a.dh) now.dh.open(at, d);
+    if (PRE && a.dz) now.dz.open(at, dz);
+    if (a.gate_kind == kGateMatrix) now.gate.open(at, gate);
+    const float mean1 = now.mean1, rstd1 = now.rstd1, mean2 = now.mean2, rstd2 = now.rstd2;
 #pragma unroll
     for (int e = 0; e < E; ++e)
       if (!a.dh || !row) d[e] = 0.f;

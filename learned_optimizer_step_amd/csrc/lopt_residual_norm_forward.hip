@@ -3,7 +3,7 @@
 // where h is rounded to its type first: z is the norm of what is kept.
 // Bound by HBM: x and y (and a gate matrix) are read once, h and z written
 // once; the row stays in registers through both norms, and so do the vectors of
-// parameters for all rows of a block.
+// parameters for all rows of a block.  A block's next row is loaded before the sums of this one.
 #include <hip/hip_runtime.h>
 
 #include "lopt_residual_norm.h"
@@ -57,16 +57,29 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_forward(ResidualForward a
     return m;
   };
 
-  const int64_t stride = int64_t(gridDim.x) * L::ROWS;
+  struct Row {
+    RowPacks<T, RowAt<T, L, MODE>> x, y, gate;
+  };
+  const auto load = [&](int64_t r0) {
+    const int64_t r = r0 + threadIdx.x / L::TPR, rr = r < a.rows ? r : 0;
+    Row p;
+    p.y.load(at, static_cast<const T*>(a.y) + rr * a.ldy);
+    p.x.load(at, static_cast<const T*>(a.x) + rr * a.ldx);
+    if (a.gate_kind == kGateMatrix) p.gate.load(at, static_cast<const T*>(a.gate) + rr * a.ldg);
+    return p;
+  };
+  const int64_t stride = int64_t(gridDim.x) * L::ROWS, first = int64_t(blockIdx.x) * L::ROWS;
+  Row next = load(first);
   // every thread of a block makes the same number of rounds (barriers inside)
-  for (int64_t r0 = int64_t(blockIdx.x) * L::ROWS; r0 < a.rows; r0 += stride) {
+  for (int64_t r0 = first; r0 < a.rows; r0 += stride) {
     const int64_t r = r0 + threadIdx.x / L::TPR;
     const bool row = L::ROWS == 1 || r < a.rows;
-    const int64_t rr = row ? r : 0;
+    const Row now = next;
+    if (r0 + stride < a.rows) next = load(r0 + stride);
     float x[E], u[E];
-    load_row(at, static_cast<const T*>(a.y) + rr * a.ldy, u);
-    load_row(at, static_cast<const T*>(a.x) + rr * a.ldx, x);
-    if (a.gate_kind == kGateMatrix) load_row(at, static_cast<const T*>(a.gate) + rr * a.ldg, gate);
+    now.y.open(at, u);
+    now.x.open(at, x);
+    if (a.gate_kind == kGateMatrix) now.gate.open(at, gate);
     if (a.post) {
       const Moments m = moments(u);
 #pragma unroll
@@ -81,7 +94,9 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_forward(ResidualForward a
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = k * V + i;
-        const float h = to_f32(from_f32<T>(fmaf(a.alpha, x[e], a.beta * (gate[e] * u[e]))));
+        float h = fmaf(a.alpha, x[e], a.beta * (gate[e] * u[e]));
+        if constexpr (std::is_same_v<T, f16>) asm("" : "+v"(h));   // an fp32 number first, whatever the instruction could round at once
+        h = to_f32(from_f32<T>(h));
         x[e] = at[k].own(i) ? h : 0.f;
       }
     if (row) store_row(at, static_cast<T*>(a.h) + r * a.ldh, x);
