@@ -11,17 +11,22 @@
 namespace lopt {
 namespace {
 
+// h as it is kept: an fp32 number first, also where one instruction could round the sum to fp16 at once.
+template <class T>
+__device__ __forceinline__ T kept(float h) {
+  if constexpr (std::is_same_v<T, f16>) asm("" : "+v"(h));
+  return from_f32<T>(h);
+}
+
 template <class T, class L, int MODE>
 __global__ __launch_bounds__(L::BLOCK) void k_residual_forward(ResidualForward a) {
   constexpr int V = kVec<T>, NV = L::E / V, E = L::E;
   constexpr int W = L::TPR > 64 ? L::TPR / 64 : 1;
-  __shared__ double red1[2][W][1];
-  __shared__ float red2[2][W][1];
-  RowSum<L::TPR, 1, double> row_sum1{red1};
-  RowSum<L::TPR, 1> row_sum2{red2};
+  __shared__ double red[2][W][1];
+  RowSum<L::TPR, 1, double> row_sum{red};
   const int lane = threadIdx.x % L::TPR;
   const int n = int(a.cols);
-  const float inv_n = 1.f / float(n);
+  const double inv_n = 1.0 / double(n);
 
   RowAt<T, L, MODE> at(lane, n);
   float w1[E], b1[E], gate[E], w2[E], b2[E];
@@ -40,20 +45,21 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_forward(ResidualForward a
 #pragma unroll
       for (int e = 0; e < E; ++e) part[e & 1] += Sum(v[e]);
       double sum[1] = {double(part[0]) + double(part[1])};
-      row_sum1(sum);
-      m = mean_of(sum[0], n);
+      row_sum(sum);
+      residual_mean(m, sum[0], inv_n);
     }
-    float s2[1] = {0.f};
+    float part[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float& d = v[k * V + i];
         d = at[k].own(i) ? d - m.mean : 0.f;
-        s2[0] = fmaf(d, d, s2[0]);
+        part[i & 1] = fmaf(d, d, part[i & 1]);
       }
-    row_sum2(s2);
-    spread(m, s2[0], float(n), inv_n, a.eps);
+    double s2[1] = {double(part[0]) + double(part[1])};
+    row_sum(s2);
+    residual_spread(m, s2[0], inv_n, a.eps);
     return m;
   };
 
@@ -94,9 +100,7 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_forward(ResidualForward a
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int e = k * V + i;
-        float h = fmaf(a.alpha, x[e], a.beta * (gate[e] * u[e]));
-        if constexpr (std::is_same_v<T, f16>) asm("" : "+v"(h));   // an fp32 number first, whatever the instruction could round at once
-        h = to_f32(from_f32<T>(h));
+        const float h = to_f32(kept<T>(fmaf(a.alpha, x[e], a.beta * (gate[e] * u[e]))));
         x[e] = at[k].own(i) ? h : 0.f;
       }
     if (row) store_row(at, static_cast<T*>(a.h) + r * a.ldh, x);
@@ -118,12 +122,10 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_forward(ResidualForward a
 template <class T>
 __global__ __launch_bounds__(1024) void k_residual_forward_long(ResidualForward a) {
   constexpr int V = kVec<T>;
-  __shared__ double red1[2][16][1];
-  __shared__ float red2[2][16][1];
-  RowSum<1024, 1, double> row_sum1{red1};
-  RowSum<1024, 1> row_sum2{red2};
+  __shared__ double red[2][16][1];
+  RowSum<1024, 1, double> row_sum{red};
   const int64_t n = a.cols;
-  const float inv_n = 1.f / float(n);
+  const double inv_n = 1.0 / double(n);
   const auto moments = [&](const T* row) {
     Moments m{};
     if (!a.rms) {
@@ -133,21 +135,22 @@ __global__ __launch_bounds__(1024) void k_residual_forward_long(ResidualForward 
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[0] += double(to_f32(p.v[i]));
       }
-      row_sum1(sum);
-      m = mean_of(sum[0], n);
+      row_sum(sum);
+      residual_mean(m, sum[0], inv_n);
     }
-    float s2[1] = {0.f};
+    float part = 0.f;
     for (int64_t c = threadIdx.x * V; c < n; c += 1024 * V) {
       const Pack<T, V> p = load_pack<T, V>(row, c, n);
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (c + i < n) {
           const float d = to_f32(p.v[i]) - m.mean;
-          s2[0] = fmaf(d, d, s2[0]);
+          part = fmaf(d, d, part);
         }
     }
-    row_sum2(s2);
-    spread(m, s2[0], float(n), inv_n, a.eps);
+    double s2[1] = {double(part)};
+    row_sum(s2);
+    residual_spread(m, s2[0], inv_n, a.eps);
     return m;
   };
   const auto param = [&](const void* p, int64_t c, float fill) { return p ? load_any(p, a.wdtype, c) : fill; };
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(1024) void k_residual_forward_long(ResidualForward 
         float u = to_f32(py.v[i]);
         if (a.post) u = fmaf((u - m1.mean - m1.rest) * m1.rstd, param(a.w1, c + i, 1.f), param(a.b1, c + i, 0.f));
         const float g = gr ? to_f32(gr[c + i]) : a.gate_kind == kGateVector ? load_any(a.gate, a.wdtype, c + i) : 1.f;
-        p.v[i] = from_f32<T>(fmaf(a.alpha, to_f32(px.v[i]), a.beta * (g * u)));
+        p.v[i] = kept<T>(fmaf(a.alpha, to_f32(px.v[i]), a.beta * (g * u)));
       }
       store_pack<T, V>(hr, c, n, p);
     }
