@@ -277,16 +277,20 @@ __device__ __forceinline__ float rows_reduce(float x, Op op) {
   return op(b.a, b.b);
 }
 
-// A block's tile.  Blocks go to the eight dies in turn, each with a cache of its
-// own: a die gets neighbours, 8 tiles of m by a run of n at a time.
+// A block's tile, and its part of a split sum.  Blocks go to the eight dies in turn, each with a cache
+// of its own: a die gets neighbours, 8 tiles of m by a run of n at a time, and few of the parts (4096 of
+// 50257 x 1024 bf16, backward 16 us less than with every part on every die).
 struct Place {
   int64_t m, n;
+  uint32_t split;
 };
-__device__ __forceinline__ Place place(uint32_t id, uint32_t mt, uint32_t nt) {
-  const uint32_t total = mt * nt, per = total / 8, rest = total % 8, die = id % 8;
-  id = die * per + min(die, rest) + id / 8;
+__device__ __forceinline__ Place place(uint32_t mt, uint32_t nt) {
+  const uint32_t per = gridDim.x / 8, rest = gridDim.x % 8, die = blockIdx.x % 8;
+  uint32_t id = die * per + min(die, rest) + blockIdx.x / 8;
+  const uint32_t split = id / (mt * nt);
+  id -= split * mt * nt;
   const uint32_t group = id / (8 * nt), first = group * 8, rows = min(8u, mt - first), in = id - group * 8 * nt;
-  return {first + in % rows, in / rows};
+  return {first + in % rows, in / rows, split};
 }
 
 // What the backward pass keeps on the device: tokens with a target (the others
@@ -324,7 +328,7 @@ struct Stats {
 template <class T, class C>
 __global__ __launch_bounds__(C::THREADS, 2) void k_ce_stats(Stats a) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
-  const Place t = place(blockIdx.x, a.mt, a.nt);
+  const Place t = place(a.mt, a.nt);
   const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
   Acc<C> acc;
   product<T, false, false, C>(acc, a.w, a.x, m0, n0, 0, a.steps, lds);
@@ -510,7 +514,7 @@ struct Grad {
 template <class T, class C>
 __global__ __launch_bounds__(C::THREADS, 2) void k_ce_grad(Grad a) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
-  const Place t = place(blockIdx.x, a.mt, a.nt);
+  const Place t = place(a.mt, a.nt);
   const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
   if (n0 >= a.head->n) return;
   Acc<C> acc;
@@ -561,8 +565,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_sums(Sums a) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
   constexpr int kStep = 128 / int(sizeof(T));
   const int64_t n = a.head->n;
-  const uint32_t tiles = a.mt * a.nt, z = blockIdx.x / tiles;
-  const Place t = place(blockIdx.x - z * tiles, a.mt, a.nt);
+  const Place t = place(a.mt, a.nt);
+  const int64_t z = t.split;
   const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
   if (!BC && n0 >= n) return;   // n: tokens
   int64_t first, count;
@@ -600,7 +604,7 @@ template <class T, class C>
 __global__ __launch_bounds__(C::THREADS, 2) void k_ce_weight(WeightGrad a) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * C::STAGE];
   constexpr int kStep = 128 / int(sizeof(T));
-  const Place t = place(blockIdx.x, a.mt, a.nt);
+  const Place t = place(a.mt, a.nt);
   const int64_t m0 = t.m * C::M, n0 = t.n * C::N;
   Acc<C> acc;
   product<T, true, true, C>(acc, a.a, a.b, m0, n0, 0, (int64_t(a.head->n) + kStep - 1) / kStep, lds);
@@ -620,7 +624,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_weight(WeightGrad a) {
       });
     } else {
       store_tile<W, C>(lds, value, [&](int n, int m, const Pack<W, kVec<W>>& p) {
-        if (n < rows && m < cols) store_pack<W, kVec<W>>(out + n * a.ldo, m, cols, p);
+        if (n >= rows || m >= cols) return;
+        // the gradient's reader comes later, G's next piece now: past the caches (34 of 1795 us)
+        if (m + kVec<W> <= cols) store_stream(reinterpret_cast<Pack<W, kVec<W>>*>(out + n * a.ldo + m), p);
+        else store_pack<W, kVec<W>>(out + n * a.ldo, m, cols, p);
       });
     }
   };
