@@ -435,19 +435,25 @@ __global__ __launch_bounds__(256) void k_ce_pack(const T* from, int64_t ld, int6
   }
 }
 
-// The tokens with a target, in their order: rows[k] of the k-th, pos[r] its k (-1: none); the scale of G.  One block.
+// The tokens with a target, in their order: rows[k] of the k-th, pos[r] its k (-1: none); the scale of G.  At most 64 blocks
+// with a run of tokens each, 1024 at a time; a block counts the targets before its run itself (65536 tokens bf16: 12 us, one block 48).
 __global__ __launch_bounds__(1024) void k_ce_rows(int64_t n, int64_t vocab, const void* targets, int32_t id_bytes, const float* g, int64_t g_stride,
                                                   const float* lse, int32_t scaled, Header* head, Row* rows, int32_t* pos) {
   __shared__ int32_t count[16];
   __shared__ float most[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t run = ((n + 1023) / 1024 + gridDim.x - 1) / gridDim.x * 1024, begin = blockIdx.x * run, end = min(begin + run, n);
+  if (begin >= n) return;
   float scale = 1.f;
   if (scaled) {   // |G| up to 2^11: fp16's smallest steps are then 2^-35 of the largest gradient
     float top = 0.f;
-    for (int64_t r = threadIdx.x; r < n; r += 1024) {
-      const int64_t t = load_id(targets, id_bytes, r);
-      const float x = fabsf(g[r * g_stride]);
-      if (t >= 0 && t < vocab && x < INFINITY) top = fmaxf(top, x);
+    for (int64_t r0 = threadIdx.x; r0 < n; r0 += 1024 * 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t r = min(r0 + 1024 * k, n - 1), t = load_id(targets, id_bytes, r);
+        const float x = fabsf(g[r * g_stride]);
+        top = t >= 0 && t < vocab && x < INFINITY ? fmaxf(top, x) : top;
+      }
     }
     top = lanes_reduce<64>(top, Max());
     if (lane == 0) most[wave] = top;
@@ -457,11 +463,36 @@ __global__ __launch_bounds__(1024) void k_ce_rows(int64_t n, int64_t vocab, cons
     const int k = 10 - e;
     if (top > 0.f) scale = __builtin_ldexpf(1.f, k < -126 ? -126 : k > 126 ? 126 : k);
   }
+  struct Token {
+    int64_t target;
+    float lse, g;
+  };
+  const auto load = [&](int64_t r) {
+    r = min(r, n - 1);
+    return Token{load_id(targets, id_bytes, r), lse[r], g[r * g_stride]};
+  };
+  Token next = load(begin + threadIdx.x);
   int32_t before = 0;
-  for (int64_t r0 = 0; r0 < n; r0 += 1024) {
+  for (int64_t r0 = threadIdx.x; r0 < begin; r0 += 1024 * 8) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t r = min(r0 + 1024 * k, begin - 1), t = load_id(targets, id_bytes, r);
+      before += r0 + 1024 * k < begin && t >= 0 && t < vocab ? 1 : 0;
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
+  if (lane == 0) count[wave] = before;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) before += count[k];
+  __syncthreads();   // count is written again
+  for (int64_t r0 = begin; r0 < end; r0 += 1024) {
     const int64_t r = r0 + threadIdx.x;
-    const int64_t t = r < n ? load_id(targets, id_bytes, r) : -1;
-    const bool there = t >= 0 && t < vocab;
+    const Token now = next;
+    next = load(r + 1024);
+    const bool there = r < n && now.target >= 0 && now.target < vocab;
     const uint64_t mask = __ballot(there);
     const int32_t mine = __popcll(mask & ((1ull << lane) - 1));
     if (lane == 0) count[wave] = __popcll(mask);
@@ -472,12 +503,12 @@ __global__ __launch_bounds__(1024) void k_ce_rows(int64_t n, int64_t vocab, cons
       if (k < wave) at += count[k];
       all += count[k];
     }
-    if (there) rows[at + mine] = {lse[r] * kLog2e, g[r * g_stride] * scale, int32_t(t), int32_t(r)};
+    if (there) rows[at + mine] = {now.lse * kLog2e, now.g * scale, int32_t(now.target), int32_t(r)};
     if (r < n) pos[r] = there ? at + mine : -1;
     before += all;
     __syncthreads();   // count is written again
   }
-  if (threadIdx.x == 0) *head = {before, scale, 1.f / scale};
+  if (end == n && threadIdx.x == 0) *head = {before, scale, 1.f / scale};
 }
 
 // The rows of x of those tokens, and zeros up to a whole tile.
@@ -523,7 +554,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_grad(Grad a) {
   Row rows[C::FN];
 #pragma unroll
   for (int k = 0; k < C::FN; ++k) rows[k] = a.rows[n0 + tile_n<C>(k)];
-  const bool last = v0 + C::M > a.vend;
+  const bool edge = v0 + C::M > a.vend || n0 + C::N > a.head->n;   // 0 behind the vocabulary and the tokens, whatever the logits are there
   T* out = static_cast<T*>(a.out) + n0 * a.width + m0;
   store_tile<T, C>(
       lds,
@@ -535,7 +566,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_grad(Grad a) {
         for (int e = 0; e < 4; ++e) {
           // a probability is at most 1, whatever half a step of a large lse is (NaN stays NaN)
           const float x = exp2_hw(__builtin_elementwise_minimum(fmaf(acc[i][k][e], kLog2e, -rows[k].lse), 0.f));
-          v[e] = last && v0 + m + e >= a.vend ? 0.f : rows[k].g * (x - (target == m + e ? 1.f : 0.f));
+          v[e] = edge && (v0 + m + e >= a.vend || rows[k].target < 0) ? 0.f : rows[k].g * (x - (target == m + e ? 1.f : 0.f));
         }
         return v;
       },
@@ -688,15 +719,19 @@ int64_t tiles_of(int64_t m, int64_t n, int tile) {
   const int64_t t = 256 >> tile;
   return ((m + t - 1) / t) * ((n + t - 1) / t);
 }
-// Whole sums: the largest tile that gives most compute units one (a bf16 1003 x 10007 x 333 product: TODO).
+// Whole sums: the largest tile that n fills by more than half and that gives most compute units one (bf16, forward: 2048 tokens
+// of 32000 x 1024 122 us with the large, 154 and 212 with the smaller ones; 100 of 50257 x 1024 40, 32 and 39; 4096 of 1000 x
+// 512 26, 19 and 18).
 int whole_tile(int64_t m, int64_t n) {
   for (int tile = kLarge; tile < kSmall; ++tile)
-    if (tiles_of(m, n, tile) >= kUnits * 3 / 4) return tile;
+    if (n > 128 >> tile && tiles_of(m, n, tile) >= kUnits * 3 / 4) return tile;
   return kSmall;
 }
-// Sums that may be split: the largest tile that does with parts of at least 16, 8 and 4 stages.
+// Sums that may be split: the largest tile that does with parts of at least 16, 8 and 4 stages (backward, with each for both
+// sums: 2048 tokens of 32000 x 1024 430, 633 and 892 us; 512 of 10000 x 512 82, 62 and 83; 3 of 1000 x 65 56, 37 and 28).
 Shape split_tile(int64_t m, int64_t n, int64_t steps) {
   for (int tile = kLarge; tile < kSmall; ++tile) {
+    if (n <= 128 >> tile) continue;
     const int64_t tiles = tiles_of(m, n, tile), most = std::max<int64_t>(1, steps / (16 >> tile));
     if (tiles * most >= kUnits * 3 / 4) return {tile, int32_t(std::max<int64_t>(1, std::min(most, kUnits / tiles)))};
   }
@@ -717,7 +752,6 @@ struct Plan {
   int64_t s, np, dp;             // element bytes; tokens and columns filled up
   int64_t width;                 // of a piece of the vocabulary
   Shape sx;                      // of dx: its splits are kept from piece to piece
-  int64_t parts;                 // tiles of the vocabulary
   int64_t bytes = 0;
   int64_t take(int64_t n) {
     const int64_t at = bytes;
@@ -749,8 +783,7 @@ Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) 
   p.x = p.take(p.np * p.dp * p.s);
   p.w = p.take(p.width * p.dp * p.s);
   if (!backward) {
-    p.parts = all / (256 >> kSmall);
-    p.part = p.take(p.parts * p.np * 8);
+    p.part = p.take(all / (256 >> whole_tile(std::min(vocab, p.width), n)) * p.np * 8);   // a weight that is not in pieces has no smaller tiles
     p.hit = p.take(n * 4);
     return p;
   }
@@ -832,7 +865,7 @@ hipError_t backward(const LinearCeBackward& a, hipStream_t s) {
   Row* rows = reinterpret_cast<Row*>(ws + p.rows);
   int32_t* pos = reinterpret_cast<int32_t*>(ws + p.pos);
   T* x = reinterpret_cast<T*>(ws + p.x);
-  k_ce_rows<<<dim3(1), dim3(1024), 0, s>>>(a.rows, a.vocab, a.targets, a.id_bytes, a.dloss, a.lddl, a.lse, a.dtype == kF16, head, rows, pos);
+  k_ce_rows<<<dim3(unsigned(std::min<int64_t>((a.rows + 1023) / 1024, 64))), dim3(1024), 0, s>>>(a.rows, a.vocab, a.targets, a.id_bytes, a.dloss, a.lddl, a.lse, a.dtype == kF16, head, rows, pos);
   const int64_t blocks = (p.np * (p.dp / kVec<T>) + 255) / 256;
   k_ce_gather<T><<<dim3(unsigned(std::min<int64_t>(blocks, 8192))), dim3(256), 0, s>>>(static_cast<const T*>(a.x), a.ldx, a.cols, head, rows, x, p.dp);
   const Operand xr{reinterpret_cast<const char*>(x), p.dp * p.s, p.np - 1, 0}, xc{xr.p, xr.ld, p.np - 1, p.dp * p.s - 16};

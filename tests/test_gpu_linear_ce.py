@@ -65,6 +65,21 @@ def test_vocabularies_in_several_pieces(t, n, vocab, dim):
     check(x, w, targets, g, f"{n} of {vocab} x {dim}", device="cuda")
 
 
+def test_entries_of_minus_infinity():
+    """A weight's row of -inf under positive tokens: its logits are -inf, its probabilities and its gradient 0."""
+    for t in TYPES:
+        x, w, targets, g = make(5, 300, 40, t, 12, pad=0.0)
+        x, targets = x.abs() + 0.25, targets.clamp(min=10)
+        w[7] = -6e4   # logits so low that nothing is left of them
+        want = layers.linear_ce_forward(x.cuda(), w.cuda(), targets.cuda())
+        dw = layers.linear_ce_backward(g.cuda(), x.cuda(), w.cuda(), targets.cuda(), want[1], need_x=False)[1]
+        w[7] = -math.inf
+        got = layers.linear_ce_forward(x.cuda(), w.cuda(), targets.cuda())
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        again = layers.linear_ce_backward(g.cuda(), x.cuda(), w.cuda(), targets.cuda(), got[1], need_x=False)[1]
+        assert torch.equal(again, dw) and not again[7].any()
+
+
 def test_rows_to_ignore_are_not_read():
     """NaN and infinities in rows without a target: loss 0, gradient 0, and nothing of them in dw."""
     for t in TYPES:
