@@ -38,9 +38,9 @@ def decode(state, bits):
     return np.where(cm & 128, -m, m), decode_codes(cv, ev, 31)
 
 
-def encode(x, top, u):
+def encode(x, top, u, exact=None):
     """Codes and exponent bytes of |x| (blocks, 256) in 64 bits; u: 16 random bits over 2^16.  A number is taken down to a
-    multiple of its step after adding u steps."""
+    multiple of its step after adding u steps; one that lies on it then, but above `exact`, to the multiple below."""
     most = np.max(np.where(np.isnan(x), np.inf, np.abs(x)), axis=1)
     bad = ~np.isfinite(most)
     most = np.where(bad, 1.0, most)
@@ -53,6 +53,8 @@ def encode(x, top, u):
     step = np.ldexp(1.0, np.maximum(f, 1) - top - 3)
     q = np.floor(y / step + u)                                 # 8 + k, or k for f = 0; 16 is the next binade's first
     code = np.where(f > 0, f * 8 + q - 8, q)
+    if exact is not None:
+        code = code - ((y / step + u == q) & (np.abs(exact) < np.abs(x)))
     return np.minimum(code, top * 8 + 7).astype(np.uint8), np.where(bad, 255, e + 100).astype(np.uint8)
 
 
@@ -65,6 +67,7 @@ def step_moments(g, state, bits, betas, seed, t, place, first=0):
     G = G.reshape(m.shape)
     b1, b2 = (np.float32(b) for b in betas)
     with np.errstate(over="ignore", invalid="ignore", under="ignore"):
+        v64 = v.astype(np.float64) * betas[1] + (1.0 - betas[1]) * G.astype(np.float64) ** 2
         m = m * b1 + G * np.float32(1.0 - betas[0])
         v = v * b2 + (G * G) * np.float32(1.0 - betas[1])
     if bits == 32:
@@ -72,7 +75,7 @@ def step_moments(g, state, bits, betas, seed, t, place, first=0):
     new = np.zeros((len(m), 2 * BLOCK + 16), np.uint8)
     r = random_bits(seed, t, place, first, m.size).reshape(m.shape)
     cm, em = encode(m.astype(np.float64), 15, (r & np.uint64(0xFFFF)).astype(np.float64) / 65536)
-    cv, ev = encode(v.astype(np.float64), 31, (r >> np.uint64(16)).astype(np.float64) / 65536)
+    cv, ev = encode(v.astype(np.float64), 31, (r >> np.uint64(16)).astype(np.float64) / 65536, v64)
     gone = em == 255
     cm = np.where(gone[:, None], 0, cm + 128 * ((m < 0) & (cm > 0)))
     cv = np.where((ev == 255)[:, None], 0, np.where((v > 0) & (cv == 0), 1, cv))

@@ -8,7 +8,7 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover - CPU container
     pytest.skip("no GPU", allow_module_level=True)
 
-from adamw_cases import BLOCK, as_numpy, decode, random_bits, step_moments, step_param  # noqa: E402
+from adamw_cases import BLOCK, as_numpy, decode, decode_codes, encode, random_bits, step_moments, step_param  # noqa: E402
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
 from ops_cases import TINY, TYPES, U, half  # noqa: E402
@@ -60,6 +60,26 @@ def test_against_the_definition(pt, gt, bits):
         step_and_check(ps, gs, states, step, bits, 1e-2, 0.1, 77, f"step {t}")
         gs = [g.flip(0) * 0.5 for g in gs]
     assert int(step[0]) == 3
+
+
+def test_codes_that_fp32_rounds_up_to():
+    """So many elements that some v in fp32 lie on a code's border while the definition's are below it."""
+    n = 1 << 23
+    ps, gs, states = make([n], torch.float32, torch.float32, 8, 21)
+    step = torch.zeros(2, dtype=torch.int64, device="cuda")
+    layers.adamw_step(ps, gs, states, step, lr=1e-3, betas=BETAS, eps=EPS, weight_decay=0.0, state_bits=8, seed=5)
+    gs = [g.flip(0) for g in gs]
+    v = decode(as_numpy(states[0]), 8)[1]
+    step_and_check(ps, gs, states, step, 8, 1e-3, 0.0, 5, "borders")
+    g = as_numpy(gs[0]).reshape(-1, BLOCK)
+    u = (random_bits(5, 2, 0, 0, n).reshape(-1, BLOCK) >> np.uint64(16)).astype(np.float64) / 65536
+    codes = []
+    for x in (BETAS[1] * v + (1 - BETAS[1]) * g.astype(np.float64) ** 2,
+              (v.astype(np.float32) * np.float32(BETAS[1]) + g * g * np.float32(1 - BETAS[1])).astype(np.float64)):
+        code, e = encode(x, 31, u)
+        codes.append(decode_codes(np.where((x > 0) & (code == 0), 1, code), e, 31))   # a v that is not 0 has a code that is not
+    got = decode(as_numpy(states[0]), 8)[1]
+    assert (got != codes[1]).any() and (got != codes[0]).sum() < (codes[1] != codes[0]).sum()
 
 
 @pytest.mark.parametrize("bits", [32, 8])
