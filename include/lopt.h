@@ -24,8 +24,9 @@
  *   (dir, mag) = W3 relu(W2 relu(W1 x + b1) + b2) + b3
  *   u = dir exp(mag exp_mult) step_mult;  p <- p - lr u - lr wd p
  *
- * The operators behind the step (norms, embedding, distillation loss) produce
- * the gradients it reads; they are declared at the end.
+ * The operators around the step (norms, residual update, embedding, distillation
+ * loss, linear cross entropy) produce the gradients it reads, and AdamW is a step
+ * of its own over the same lists; they are declared at the end.
  *
  * All arithmetic of a step on the device is fp32 (the operators take bf16 and
  * fp16 too, and their sums are fp32 or wider).  Every call returns an lopt_status;

@@ -6,7 +6,10 @@
 // part of the vocabulary.  Backward: the vocabulary in pieces; of each, the
 // product again, its tiles ending in G, which is kept for the piece alone, and
 // from it the piece's share of dx and its rows of dw.  Bound by the matrix
-// units: 2 N V D operations forward, 6 N V D backward.
+// units: 2 N V D operations forward, 6 N V D backward.  bf16: forward 8192 tokens of
+// 32000 x 2048 835 us (1286 TFLOP/s; the library's plain product of that size takes 901),
+// both passes 4096 of 50257 x 1024 1680 to 1745 us (1004 to 966 TFLOP/s; the library's
+// plain product of that size reaches 866).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

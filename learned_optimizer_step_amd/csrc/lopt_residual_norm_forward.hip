@@ -3,7 +3,8 @@
 // where h is rounded to its type first: z is the norm of what is kept.
 // Bound by HBM: x and y (and a gate matrix) are read once, h and z written
 // once; the row stays in registers through both norms, and so do the vectors of
-// parameters for all rows of a block.  A block's next row is loaded before the sums of this one.
+// parameters for all rows of a block.  A block's next row is loaded before the sums of this one
+// (65536 x 2048 bf16, RMS: 205 to 230 us, 4.7 to 5.2 TB/s; a copy reaches 5.1).
 #include <hip/hip_runtime.h>
 
 #include "lopt_residual_norm.h"
