@@ -14,7 +14,7 @@ BWD = dict(rows=5, cols=16, vocab=100, dtype=1, dloss=A[0], dloss_stride=1, x=A[
 
 BOTH = [(dict(rows=-1), BAD), (dict(cols=0), BAD), (dict(vocab=0), BAD), (dict(rows=(1 << 24) + 1), UNSUPPORTED),
         (dict(cols=(1 << 20) + 1), UNSUPPORTED), (dict(vocab=1 << 31), UNSUPPORTED), (dict(vocab=(1 << 31) - 300, rows=1 << 17), UNSUPPORTED),
-        (dict(vocab=1 << 15, rows=1 << 24), UNSUPPORTED), (dict(vocab=(1 << 31) - 300, rows=257), UNSUPPORTED),
+        (dict(vocab=1 << 15, rows=1 << 24), UNSUPPORTED), (dict(vocab=(1 << 31) - 300, rows=257), UNSUPPORTED), (dict(vocab=1 << 30, rows=1), UNSUPPORTED),
         (dict(dtype=3), BAD), (dict(x=None), BAD), (dict(w=None), BAD), (dict(targets=None), BAD), (dict(ldx=15), BAD), (dict(ldw=3), BAD),
         (dict(id_bytes=2), BAD), (dict(workspace=None), WORKSPACE), (dict(ws_bytes=100), WORKSPACE)]
 CASES = [
