@@ -647,8 +647,8 @@ lopt_status lopt_adamw_state_bytes(int64_t n, int32_t state_bits, size_t* bytes)
  *   p <- p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * with the m and v from before they are rounded to 8 bits (a v below the least normal float counts as that under the root).
  * 8-bit codes are rounded up or down with a probability that keeps their mean (for each number 32 bits, a hash of
- * seed, t, the tensor's place in ts and the element's number; 16 for each moment), as m and v are in fp32, and a v
- * down where fp32's own rounding alone takes it up to a code; a v that is not 0 stays so.  step: two 64-bit numbers in device memory, 8-byte aligned: the
+ * seed, t, the tensor's place in ts and the element's number; 16 for each moment) and follow from these and the m and v in
+ * fp32 alone; a v that is not 0 stays so.  step: two 64-bit numbers in device memory, 8-byte aligned: the
  * count of steps taken, which the call advances (also when every tensor is skipped, not for an empty list), and one that the
  * library keeps at 0.  So a captured step counts as it is replayed, but keeps lr and the addresses of its capture.
  * 0 <= beta1, beta2 < 1; eps finite and >= 0.  Params, states and step may not overlap each other or a gradient. */

@@ -24,9 +24,10 @@
 // at random, in proportion to what is left: v changes by a thousandth a step
 // with b2 = 0.999, which rounding to the nearest of 3 bits would lose every
 // time, and the codes could neither rise nor decay.  A number is rounded by
-// adding 16 random bits below the code's last bit.  The 32 random bits of an
-// element are a hash of the seed, t, the tensor's place in the list and the
-// element's number.  A v that is not 0 does not round to 0, as its root divides.
+// adding 16 random bits below the code's last bit: codes follow from the fp32
+// moment and these bits alone.  The 32 random bits of an element are a hash of
+// the seed, t, the tensor's place in the list and the element's number.  A v
+// that is not 0 does not round to 0, as its root divides.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -85,8 +86,8 @@ struct Codes {
     const int e = int((__float_as_uint(top) + 0x100000u) >> 23) - 127;
     return min(max(e, -100), 127);
   }
-  // The code of x >= 0, from bit 20 on, before it is held to those that there are; r: random bits, 16 of them under the code's last bit.
-  static __device__ __forceinline__ uint32_t encode(float x, int e, uint32_t r) { return __float_as_uint(__builtin_ldexpf(x, -e - kScale)) + (r << 4); }
+  // The code of x >= 0 before it is held to those that there are; r: random bits, 16 of them under the code's last bit.
+  static __device__ __forceinline__ uint32_t encode(float x, int e, uint32_t r) { return (__float_as_uint(__builtin_ldexpf(x, -e - kScale)) + (r << 4)) >> 20; }
   // bits: the code in its place, from bit 20 on
   static __device__ __forceinline__ float decode(uint32_t bits, int e) { return __builtin_ldexpf(__uint_as_float(bits), e + kScale); }
 };
@@ -142,7 +143,7 @@ struct Moments<32> {
   }
   __device__ __forceinline__ void open() {}
   template <bool ONCE>
-  __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t, int64_t, const AdamwLaunch&, const float (&)[4]) const {
+  __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t, int64_t) const {
     float* f = reinterpret_cast<float*>(s);
     store4<float, true, ONCE>(f, lane * 4, 0, m);
     store4<float, true, ONCE>(f + kMomentBlock, lane * 4, 0, v);
@@ -174,29 +175,14 @@ struct Moments<8> {
       }
     }
   }
-  // A v that reaches a code exactly, but only by fp32's rounding, has the code below (one in two million, each 8 to 15 hundredths
-  // above the definition's in 64 bits otherwise; 355M elements: 1343 us with this, 1339 without).
-  __device__ __forceinline__ void below(const AdamwLaunch& a, const float (&g)[4], uint32_t (&codes)[4]) const {
-    Moments<8> old;
-    old.cm = cm;
-    old.cv = cv;
-    old.e = e;
-    old.open();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const double exact = a.beta2 * old.v[k] + (1.0 - a.beta2) * g[k] * g[k];
-      if ((codes[k] & 0xFFFFF) == 0 && exact < double(v[k])) --codes[k];
-    }
-  }
   template <int K>
   __device__ __forceinline__ void open_one(int em, int ev) {
     const float x = CodesM::decode(from_byte<K, 127>(cm), em);
     m[K] = __uint_as_float(__float_as_uint(x) | (cm << (24 - 8 * K) & 0x80000000u));
     v[K] = CodesV::decode(from_byte<K, 255>(cv), ev);
   }
-  // g: the gradients that v is of
   template <bool ONCE>
-  __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t key, int64_t i, const AdamwLaunch& a, const float (&g)[4]) const {
+  __device__ __forceinline__ void store(unsigned char* s, int lane, uint32_t key, int64_t i) const {
     float tm = 0.f, tv = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -209,19 +195,15 @@ struct Moments<8> {
     const int em = bm ? 0 : CodesM::exponent(tm), ev = bv ? 0 : CodesV::exponent(tv);
     // 0x9E3779B9 times the upper half: the same for the block
     const uint32_t base = key + uint32_t(i) + 0x9E3779B9u * uint32_t(uint64_t(i) >> 32);
-    uint32_t pm = 0, pv = 0, signs = 0, codes[4], nearest = ~0u;
+    uint32_t pm = 0, pv = 0, signs = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t r = mix(base + k);
-      pm |= min(CodesM::encode(fabsf(m[k]), em, r & 0xFFFF) >> 20, 127u) << 8 * k;
+      pm |= min(CodesM::encode(fabsf(m[k]), em, r & 0xFFFF), 127u) << 8 * k;
       signs |= (__float_as_uint(m[k]) >> 24 & 128) << 8 * k;
-      codes[k] = CodesV::encode(v[k], ev, r >> 16);
-      nearest = min(nearest, codes[k] & 0xFFFFF);
+      // a v that is not 0 has a code that is not
+      pv |= min(max(CodesV::encode(v[k], ev, r >> 16), min(__float_as_uint(v[k]), 1u)), 255u) << 8 * k;
     }
-    if (nearest == 0) below(a, g, codes);   // one block in some thousand
-#pragma unroll
-    for (int k = 0; k < 4; ++k)   // a v that is not 0 has a code that is not
-      pv |= min(max(codes[k] >> 20, min(__float_as_uint(v[k]), 1u)), 255u) << 8 * k;
     pm |= signs & (pm + 0x7F7F7F7Fu);   // no sign without a code
     reinterpret_cast<uint32_t*>(s)[lane] = bm ? 0u : pm;
     reinterpret_cast<uint32_t*>(s + kMomentBlock)[lane] = bv ? 0u : pv;
@@ -260,7 +242,7 @@ __device__ __forceinline__ void chunk_step(const AdamwLaunch& a, const AdamwEntr
         xp[b][k] = xp[b][k] * t.decay - size * m * __builtin_amdgcn_rcpf(d);
       }
       store4<P, FULL, ONCE>(p, i0 + b * kMomentBlock, t.n, xp[b]);
-      mo[b].template store<ONCE>(s + b * Moments<BITS>::kBytes, lane, key, i0 + b * kMomentBlock, a, xg[b]);
+      mo[b].template store<ONCE>(s + b * Moments<BITS>::kBytes, lane, key, i0 + b * kMomentBlock);
     }
 }
 

@@ -189,7 +189,7 @@ struct AdamwLaunch {
   int32_t count, advance;          // advance: the step counter goes on when this launch ends
   float b1, c1, b2, c2, eps;       // c = 1 - b
   uint32_t seed;
-  double beta2, log_b1, log_b2;
+  double log_b1, log_b2;
   unsigned long long* step;        // t, and a ticket that is 0 between launches
 };
 

@@ -572,7 +572,7 @@ lopt_status lopt_adamw_step(const lopt_adamw_tensor* ts, int32_t n, int32_t stat
     }
     AdamwLaunch a{};
     a.b1 = float(beta1); a.c1 = float(1.0 - beta1); a.b2 = float(beta2); a.c2 = float(1.0 - beta2);
-    a.beta2 = beta2; a.log_b1 = std::log(beta1); a.log_b2 = std::log(beta2);   // -inf of 0: no correction
+    a.log_b1 = std::log(beta1); a.log_b2 = std::log(beta2);   // -inf of 0: no correction
     a.eps = float(eps); a.seed = seed; a.step = reinterpret_cast<unsigned long long*>(step);
     const bool once = bytes > 200'000'000;   // what the memory-side cache does not hold until the next step
     if (groups.empty()) groups.push_back({{LOPT_F32, LOPT_F32}, {}});   // only the count

@@ -391,3 +391,70 @@ def test_refusals():
     with pytest.raises(L.LoptError, match="overlap"):
         layers.adamw_step([p], [p], [s], step, lr=1.0)
     assert step.tolist() == [0, 0] and bool((p == 1).all())
+
+
+# ---- 8-bit codes follow from the fp32 moments and the random bits, and from nothing else
+
+def fp32_codes(g, state, seed, t, place):
+    """(m, v) in fp32 and the buffer of their codes, each rounded with its random bits alone."""
+    m, v, _ = step_moments(g, state, 8, BETAS, seed, t, place)
+    r = random_bits(seed, t, place, 0, m.size).reshape(m.shape)
+    cm, em = encode(m.astype(np.float64), 15, (r & np.uint64(0xFFFF)).astype(np.float64) / 65536)
+    cv, ev = encode(v.astype(np.float64), 31, (r >> np.uint64(16)).astype(np.float64) / 65536)
+    new = np.zeros((len(m), 2 * BLOCK + 16), np.uint8)
+    new[:, :BLOCK] = np.where((em == 255)[:, None], 0, cm + 128 * ((m < 0) & (cm > 0)))
+    new[:, BLOCK:2 * BLOCK] = np.where((ev == 255)[:, None], 0, np.where((v > 0) & (cv == 0), 1, cv))
+    new[:, 2 * BLOCK], new[:, 2 * BLOCK + 1] = em, ev
+    return m, v, new.reshape(-1)
+
+
+def step8_and_check(ps, gs, states, step, lr, wd, seed, what):
+    lrs, wds = (np.broadcast_to(np.asarray(v, np.float64), len(ps)) for v in (lr, wd))
+    before = [as_numpy(p).reshape(-1).copy() for p in ps], [as_numpy(s).copy() for s in states]
+    layers.adamw_step(ps, gs, states, step, lr=lr, betas=BETAS, eps=EPS, weight_decay=wd, state_bits=8, seed=seed)
+    t = int(step[0])
+    for k, (p, g) in enumerate(zip(ps, gs)):
+        if g is None:
+            assert np.array_equal(as_numpy(p).reshape(-1), before[0][k]) and np.array_equal(as_numpy(states[k]), before[1][k])
+            continue
+        m, v, new = fp32_codes(as_numpy(g).reshape(-1), before[1][k], seed, t, k)
+        off = np.count_nonzero(as_numpy(states[k]) != new)
+        assert off == 0, f"{what} tensor {k}: {off} codes differ"
+        n = p.numel()
+        want, update = step_param(before[0][k], m.reshape(-1)[:n], v.reshape(-1)[:n], BETAS, EPS, lrs[k], wds[k], t)
+        close_param(p.reshape(-1), want, update, before[0][k], p.dtype, f"{what} tensor {k}")
+
+
+@pytest.mark.parametrize("gt", TYPES, ids=str)
+@pytest.mark.parametrize("pt", TYPES, ids=str)
+def test_codes_of_the_fp32_moments(pt, gt):
+    ps, gs, states = make(SIZES, pt, gt, 8, 3)
+    step = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for t in range(3):
+        step8_and_check(ps, gs, states, step, 1e-2, 0.1, 77, f"step {t}")
+        gs = [g.flip(0) * 0.5 for g in gs]
+
+
+def test_codes_of_the_fp32_moments_over_a_long_list():
+    g = torch.Generator().manual_seed(9)
+    sizes = torch.randint(1, 3000, (391,), generator=g).tolist()
+    ps, gs, states = [], [], []
+    for k, n in enumerate(sizes):
+        p, d, s = make([n], TYPES[k % 3], TYPES[0 if k % 2 else k % 3], 8, k)
+        ps, gs, states = ps + p, gs + ([None] if k % 7 == 3 else d), states + s
+    lr, wd = (1e-2 * torch.rand(391, generator=g)).tolist(), (0.2 * torch.rand(391, generator=g)).tolist()
+    step = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for t in range(2):
+        step8_and_check(ps, gs, states, step, lr, wd, 5, f"step {t}")
+
+
+def test_codes_and_parameters_of_two_steps_of_many_elements():
+    """2^24 elements of one size, some of whose v lie on a code's border in fp32 alone: every code of two steps, and every
+    parameter, which the second step moves by what the first one kept."""
+    n = 1 << 24
+    g = torch.Generator().manual_seed(21)
+    ps, gs = [0.1 * torch.randn(n, generator=g).cuda()], [1e-3 * torch.randn(n, generator=g).cuda()]
+    states, step = [layers.adamw_state(ps[0], 8)], torch.zeros(2, dtype=torch.int64, device="cuda")
+    for t in range(2):
+        step8_and_check(ps, gs, states, step, 1e-3, 0.1, 5, f"step {t}")
+        gs = [g.flip(0) for g in gs]
