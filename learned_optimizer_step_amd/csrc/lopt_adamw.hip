@@ -86,13 +86,16 @@ struct Codes {
     const int e = int((__float_as_uint(top) + 0x100000u) >> 23) - 127;
     return min(max(e, -100), 127);
   }
-  // The code of x >= 0 before it is held to those that there are; r: random bits, 16 of them under the code's last bit.
-  static __device__ __forceinline__ uint32_t encode(float x, int e, uint32_t r) { return (__float_as_uint(__builtin_ldexpf(x, -e - kScale)) + (r << 4)) >> 20; }
+  // x >= 0 scaled: its code from bit 20 on, and what is left of it below.  Numbers below the least exponent come rounded to
+  // 2^-20 of a code's step; `down` makes that the one below, so that a sum with random bits goes as high as x's own does.
+  static __device__ __forceinline__ uint32_t scaled(float x, int e) { return __float_as_uint(__builtin_ldexpf(x, -e - kScale)); }
+  static __device__ __forceinline__ uint32_t down(uint32_t bits, float x, int e) { return bits - (__builtin_ldexpf(__uint_as_float(bits), e + kScale) > x); }
   // bits: the code in its place, from bit 20 on
   static __device__ __forceinline__ float decode(uint32_t bits, int e) { return __builtin_ldexpf(__uint_as_float(bits), e + kScale); }
 };
 typedef Codes<16> CodesM;
 typedef Codes<32> CodesV;
+constexpr uint32_t kLeastNormal = 0x800000;   // float's bits
 constexpr uint32_t kNotANumber = 255;   // of a block's exponent: a NaN or an infinity is in it
 
 // Byte k of x, its low 7 or 8 bits, from bit 20 on.
@@ -195,14 +198,28 @@ struct Moments<8> {
     const int em = bm ? 0 : CodesM::exponent(tm), ev = bv ? 0 : CodesV::exponent(tv);
     // 0x9E3779B9 times the upper half: the same for the block
     const uint32_t base = key + uint32_t(i) + 0x9E3779B9u * uint32_t(uint64_t(i) >> 32);
+    uint32_t bits_m[4], bits_v[4], least = ~0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      bits_m[k] = CodesM::scaled(fabsf(m[k]), em);
+      bits_v[k] = CodesV::scaled(v[k], ev);
+      least = min(least, min(bits_m[k], bits_v[k]));
+    }
+    if (least < kLeastNormal) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        bits_m[k] = CodesM::down(bits_m[k], fabsf(m[k]), em);
+        bits_v[k] = CodesV::down(bits_v[k], v[k], ev);
+      }
+    }
     uint32_t pm = 0, pv = 0, signs = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const uint32_t r = mix(base + k);
-      pm |= min(CodesM::encode(fabsf(m[k]), em, r & 0xFFFF), 127u) << 8 * k;
+      const uint32_t r = mix(base + k);   // 16 bits under a code's last one for each moment
+      pm |= min((bits_m[k] + ((r & 0xFFFF) << 4)) >> 20, 127u) << 8 * k;
       signs |= (__float_as_uint(m[k]) >> 24 & 128) << 8 * k;
       // a v that is not 0 has a code that is not
-      pv |= min(max(CodesV::encode(v[k], ev, r >> 16), min(__float_as_uint(v[k]), 1u)), 255u) << 8 * k;
+      pv |= min(max((bits_v[k] + (r >> 16 << 4)) >> 20, min(__float_as_uint(v[k]), 1u)), 255u) << 8 * k;
     }
     pm |= signs & (pm + 0x7F7F7F7Fu);   // no sign without a code
     reinterpret_cast<uint32_t*>(s)[lane] = bm ? 0u : pm;

@@ -458,3 +458,14 @@ def test_codes_and_parameters_of_two_steps_of_many_elements():
     for t in range(2):
         step8_and_check(ps, gs, states, step, 1e-3, 0.1, 5, f"step {t}")
         gs = [g.flip(0) for g in gs]
+
+
+def test_codes_below_the_least_exponent():
+    """2^24 elements over five decades, many of them below their block's least exponent, where a scaled number loses bits: the
+    random bits meet what is there of it and not what it was rounded up to."""
+    n = 1 << 24
+    ps, gs, states = make([n], torch.float32, torch.float32, 8, 21)
+    step = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for t in range(2):
+        step8_and_check(ps, gs, states, step, 1e-3, 0.1, 5, f"step {t}")
+        gs = [g.flip(0) for g in gs]
