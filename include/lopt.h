@@ -586,7 +586,7 @@ lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, con
  *   z = x w^T,  lse = log sum_v exp(z_v),  loss = lse - z_t;
  * a row whose target lies outside [0, vocab) (an id to ignore) has loss 0.  Products of 16-bit elements
  * are exact and added in fp32.  targets: rows signed integers of id_bytes (4 or 8) bytes.  loss, lse: rows floats,
- * NULL: not written.  At most 2^24 rows and 2^20 columns, vocab below 2^30, and
+ * NULL: not written.  At most 2^24 rows and 2^20 columns, vocab at most 2^30 - 64, and
  * vocab / 256 * rows / 256 (rounded up) below 2^23. */
 lopt_status lopt_linear_ce_forward(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, const void* x, int64_t ldx,
                                    const void* w, int64_t ldw, const void* targets, int32_t id_bytes, float* loss, float* lse,

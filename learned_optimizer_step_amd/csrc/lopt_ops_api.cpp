@@ -114,8 +114,8 @@ void check_linear_ce(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype) {
   if (rows < 0 || cols < 1 || vocab < 1) fail(LOPT_ERR_INVALID_ARGUMENT, "rows must be >= 0, cols and vocab >= 1");
   if (rows > (int64_t(1) << 24) || cols > (int64_t(1) << 20)) fail(LOPT_ERR_UNSUPPORTED, "more than 2^24 rows or 2^20 columns");
   const int64_t tiles = (vocab + 255) / 256;
-  // a grid has room for 2^32 threads: 512 a tile of 256 x 256, and with few rows 256 a tile of 64
-  if (vocab >= (int64_t(1) << 30)) fail(LOPT_ERR_UNSUPPORTED, "vocab must be below 2^30");
+  // a grid has room for fewer than 2^32 threads: 512 a tile of 256 x 256, and with few rows 256 a tile of 64
+  if (vocab > (int64_t(1) << 30) - 64) fail(LOPT_ERR_UNSUPPORTED, "vocab must be at most 2^30 - 64");
   if (tiles * ((rows + 255) / 256) >= (int64_t(1) << 23)) fail(LOPT_ERR_UNSUPPORTED, "vocab / 256 * rows / 256 must be below 2^23");
   check_dtype(dtype, "x");
 }

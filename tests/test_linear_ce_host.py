@@ -73,3 +73,17 @@ def test_no_cpu_path():
                  lambda: layers.linear_ce_backward(x[:, 0], x, x, t, x[:, 0])):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_the_largest_vocabulary():
+    """64 entries a block of 256 threads for few rows: 2^24 blocks would be 2^32 threads, one more than a grid has room for."""
+    most = (1 << 30) - 64
+    assert -(-most // 64) * 256 < 1 << 32 <= -(-(most + 1) // 64) * 256
+    for size, call, args in ((L.lopt_linear_ce_forward_workspace, L.lopt_linear_ce_forward, FWD),
+                             (L.lopt_linear_ce_backward_workspace, L.lopt_linear_ce_backward, BWD)):
+        assert size(1, 64, most, 1) > 0
+        for vocab in (most + 1, (1 << 30) - 1):
+            for refused in (lambda: size(1, 64, vocab, 1), lambda: call(*{**args, "rows": 1, "cols": 64, "ldx": 64, "ldw": 64, "vocab": vocab}.values())):
+                with pytest.raises(L.LoptError, match="2\\^30") as e:
+                    refused()
+                assert e.value.status == UNSUPPORTED
