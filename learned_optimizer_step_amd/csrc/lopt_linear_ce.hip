@@ -321,9 +321,9 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int32_t bytes, int64
 struct Stats {
   Operand w, x;
   const void* targets;
-  float2* part;    // [vocabulary tile][np]: largest logit, and the sum of exp of the rest
+  float2* part;    // [vocabulary tile][n]: largest logit, and the sum of exp of the rest
   float* hit;      // the target's logit
-  int64_t v0, vend, n, np, steps;
+  int64_t v0, vend, n, steps;
   uint32_t mt, nt;
   int32_t id_bytes;
 };
@@ -382,13 +382,13 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_stats(Stats a) {
     const float mc = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int q = 0; q < C::WM; ++q) s = fmaf(red[q][threadIdx.x].y, exp2_hw((red[q][threadIdx.x].x - mc) * kLog2e), s);
-    a.part[v0 / C::M * a.np + n0 + threadIdx.x] = make_float2(m, s);
+    a.part[v0 / C::M * a.n + n0 + threadIdx.x] = make_float2(m, s);
   }
 }
 
 // Per token, the tiles' maxima and sums in their order: 32 tokens a block, 32 threads a token with every 32nd tile each.
-__global__ __launch_bounds__(1024) void k_ce_loss(const float2* part, int64_t tiles, int64_t np, int64_t n, int64_t vocab, const void* targets,
-                                                  int32_t id_bytes, const float* hit, float* loss, float* lse) {
+__global__ __launch_bounds__(1024) void k_ce_loss(const float2* part, int64_t tiles, int64_t n, int64_t vocab, const void* targets, int32_t id_bytes,
+                                                  const float* hit, float* loss, float* lse) {
   __shared__ float2 red[32][33];
   const int i = threadIdx.x % 32, q = threadIdx.x / 32;
   const int64_t tok = int64_t(blockIdx.x) * 32 + i;
@@ -397,7 +397,7 @@ __global__ __launch_bounds__(1024) void k_ce_loss(const float2* part, int64_t ti
     for (int64_t t = q; t < tiles; t += 32 * 8) {
       float2 x[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = t + 32 * k < tiles ? part[(t + 32 * k) * np + tok] : make_float2(-INFINITY, 0.f);
+      for (int k = 0; k < 8; ++k) x[k] = t + 32 * k < tiles ? part[(t + 32 * k) * n + tok] : make_float2(-INFINITY, 0.f);
       const float old = m;
 #pragma unroll
       for (int k = 0; k < 8; ++k) m = fmaxf(m, x[k].x);
@@ -783,10 +783,10 @@ Plan plan(int64_t n, int64_t vocab, int64_t cols, int32_t dtype, bool backward) 
     for (int64_t nt = p.np / kTile; nt % 2 == 0 && whole > 1; nt /= 2) whole /= 2;
     if (tiles > whole) p.width = tiles / whole * whole * kTile;
   }
-  p.x = p.take(p.np * p.dp * p.s);
+  p.x = p.take((backward ? p.np : n) * p.dp * p.s);
   p.w = p.take(p.width * p.dp * p.s);
   if (!backward) {
-    p.part = p.take(all / (256 >> whole_tile(std::min(vocab, p.width), n)) * p.np * 8);   // a weight that is not in pieces has no smaller tiles
+    p.part = p.take(all / (256 >> whole_tile(std::min(vocab, p.width), n)) * n * 8);   // a weight that is not in pieces has no smaller tiles
     p.hit = p.take(n * 4);
     return p;
   }
@@ -823,7 +823,6 @@ hipError_t forward(const LinearCeForward& a, hipStream_t s) {
   Stats g{};
   g.steps = p.dp * p.s / 128;
   g.n = a.rows;
-  g.np = p.np;
   g.targets = a.targets;
   g.id_bytes = a.id_bytes;
   g.part = reinterpret_cast<float2*>(ws + p.part);
@@ -856,7 +855,7 @@ hipError_t forward(const LinearCeForward& a, hipStream_t s) {
     });
   }
   const int64_t parts = (a.vocab + (256 >> tile) - 1) / (256 >> tile);
-  k_ce_loss<<<dim3(unsigned((a.rows + 31) / 32)), dim3(1024), 0, s>>>(g.part, parts, p.np, a.rows, a.vocab, a.targets, a.id_bytes, g.hit, a.loss, a.lse);
+  k_ce_loss<<<dim3(unsigned((a.rows + 31) / 32)), dim3(1024), 0, s>>>(g.part, parts, a.rows, a.vocab, a.targets, a.id_bytes, g.hit, a.loss, a.lse);
   return hipGetLastError();
 }
 

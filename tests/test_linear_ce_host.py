@@ -87,3 +87,11 @@ def test_the_largest_vocabulary():
                 with pytest.raises(L.LoptError, match="2\\^30") as e:
                     refused()
                 assert e.value.status == UNSUPPORTED
+
+
+def test_the_forward_workspace_goes_by_the_tokens():
+    """A maximum and a sum for every token and tile of 64 entries or more, x laid out, and at most 128 MiB (or 1024 entries) of the weight."""
+    for n, d, v, t in ((1, 64, (1 << 30) - 64, 1), (1, 2048, 1 << 20, 1), (3, 768, 50257, 0), (300, 333, 10007, 2), (257, 100, 1 << 22, 1)):
+        dp, s = -(-d // 64) * 64, (4, 2, 2)[t]
+        piece = max(128 << 20, 1024 * dp * s)
+        assert L.lopt_linear_ce_forward_workspace(n, d, v, t) <= 8 * n * (-(-v // 256) * 4) + n * dp * s + piece + 4 * n + 4096, (n, d, v, t)
