@@ -601,6 +601,7 @@ lopt_status lopt_linear_ce_backward_workspace(int64_t rows, int64_t cols, int64_
  *   dx = G w,  dw = G^T x.
  * G is rounded to type dtype (for fp16 scaled by a power of two first, so that its smallest steps are 2^-35 of the largest
  * |dloss|); its sums are fp32.  A row to ignore is not read: whatever x holds there, its gradient is 0 and dw does not see it.
+ * exp(z - lse) is off by the rounding of lse to fp32, a relative 2^-24 |lse| that a row's entries share, and by that of small differences.
  * dloss: one float a row, dloss_stride apart (0: one value for all rows).  lse: as lopt_linear_ce_forward wrote it.  dx: rows x
  * cols of type dtype; dw: vocab x cols of type g_dtype, added to what is there if accumulate is not 0; NULL: not computed. */
 lopt_status lopt_linear_ce_backward(int64_t rows, int64_t cols, int64_t vocab, int32_t dtype, const float* dloss,

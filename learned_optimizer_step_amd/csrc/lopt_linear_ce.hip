@@ -305,7 +305,7 @@ struct Header {
 
 // A token of those with a target.
 struct Row {
-  float lse;      // of its logits, times log2(e)
+  float lse;      // of its logits
   float g;        // its gradient, scaled
   int32_t target;
   int32_t from;   // its row of x
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(1024) void k_ce_rows(int64_t n, int64_t vocab, cons
       if (k < wave) at += count[k];
       all += count[k];
     }
-    if (there) rows[at + mine] = {now.lse * kLog2e, now.g * scale, int32_t(now.target), int32_t(r)};
+    if (there) rows[at + mine] = {now.lse, now.g * scale, int32_t(now.target), int32_t(r)};
     if (r < n) pos[r] = there ? at + mine : -1;
     before += all;
     __syncthreads();   // count is written again
@@ -567,8 +567,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void k_ce_grad(Grad a) {
         f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // a probability is at most 1, whatever half a step of a large lse is (NaN stays NaN)
-          const float x = exp2_hw(__builtin_elementwise_minimum(fmaf(acc[i][k][e], kLog2e, -rows[k].lse), 0.f));
+          // the difference first: lse, which may be large, is not rounded again.  A probability is at most 1, whatever half a
+          // step of lse is (NaN stays NaN)
+          const float x = exp2_hw(__builtin_elementwise_minimum((acc[i][k][e] - rows[k].lse) * kLog2e, 0.f));
           v[e] = edge && (v0 + m + e >= a.vend || rows[k].target < 0) ? 0.f : rows[k].g * (x - (target == m + e ? 1.f : 0.f));
         }
         return v;

@@ -25,6 +25,7 @@ _NOT_THE_DEFINITION = {
       for g in ("float32", "float16")),
     "test_gpu_adamw.py::test_codes_that_fp32_rounds_up_to",
     "test_gpu_adamw.py::test_long_lists_of_several_types_and_skipped_tensors[8]",
+    "test_gpu_transformer_step.py::test_steps_of_adamw[8]",
 }
 
 

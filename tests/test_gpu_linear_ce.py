@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from linear_ce_cases import backward, forward  # noqa: E402
+from linear_ce_cases import backward, forward, product_depth  # noqa: E402
 from ops_cases import CODE, TYPES, U, close, rounding  # noqa: E402
 
 # (tokens, vocabulary, width): ones, tiles with their neighbours, widths that no stage divides, long vocabularies and many tokens
@@ -339,3 +339,25 @@ def test_refusals_of_the_tensors():
             call()
     with pytest.raises(L.LoptError, match="overlap"):
         bwd(loss, x, w, t, lse, grad_weight=w)
+
+
+def test_probabilities_under_a_large_common_offset():
+    """fp32 logits that are exact, 500 to 4000 above 0: with lse as it is kept, a probability is off by the roundings of a small
+    difference, however large lse is.  dx under a weight's column of ones is what a token's gradients add up to."""
+    n, vocab, dim = 200, 60, 48
+    g = torch.Generator().manual_seed(16)
+    x, w = torch.zeros(n, dim), torch.randint(-8, 9, (vocab, dim), generator=g) / 8.0
+    x[:, 1:9] = torch.randint(-8, 9, (n, 8), generator=g) / 8.0
+    x[:, 0], w[:, 0] = torch.randint(500 * 64, 4000 * 64, (n,), generator=g) / 64.0, 1.0
+    targets, gl = torch.randint(0, vocab, (n,), generator=g), torch.rand(n, generator=g)
+    z = x.double() @ w.double().t()
+    assert torch.equal(z, z.float().double())
+    lse = layers.linear_ce_forward(x.cuda(), w.cuda(), targets.cuda())[1]
+    dx, dw = layers.linear_ce_backward(gl.cuda(), x.cuda(), w.cuda(), targets.cuda(), lse)
+    d = z - lse.double().cpu()[:, None]
+    p, gd = torch.exp(d.clamp(max=0.0)), gl.double()[:, None]
+    G = gd * (p - torch.zeros_like(p).scatter_(1, targets[:, None], 1.0))
+    # the difference, its product with log2(e) and that constant: U each of an exponent of |d|; the exponential 2 U, then two of G's own
+    eG = gd * p * (3 * d.abs() + 4) * U + 2 * U * G.abs()
+    close(dx, G @ w.double(), eG @ w.double().abs() + product_depth(vocab, torch.float32) * U * (G.abs() @ w.double().abs()), "dx")
+    close(dw, G.t() @ x.double(), eG.t() @ x.double().abs() + product_depth(n, torch.float32) * U * (G.abs().t() @ x.double().abs()), "dw")
