@@ -426,7 +426,8 @@ class ResidualNorm : public Function<ResidualNorm> {
     ResidualOut out = residual_forward(x, y, gate, post_weight, post_bias, weight, bias, eps, o);
     const auto some = [](const Maybe& t) { return t ? *t : Tensor(); };
     ctx->set_materialize_grads(false);
-    ctx->save_for_backward({y, some(gate), some(post_weight), some(post_bias), some(weight), out.h, out.stats});
+    // h is read by its norm's gradient alone: without that norm a caller may change it in place
+    ctx->save_for_backward({y, some(gate), some(post_weight), some(post_bias), some(weight), pre ? out.h : Tensor(), out.stats});
     ctx->saved_data["flags"] = int64_t(rms) | int64_t(post) << 1 | int64_t(pre) << 2 | int64_t(bool(gate)) << 3 | int64_t(bool(post_weight)) << 4 |
                                int64_t(bool(post_bias)) << 5 | int64_t(bool(weight)) << 6 | int64_t(bool(bias)) << 7;
     ctx->saved_data["alpha"] = alpha;

@@ -330,3 +330,22 @@ def test_refusals_of_the_tensors():
     for kw in (dict(eps=-1.0), dict(alpha=float("nan")), dict(beta=float("inf"))):
         with pytest.raises(L.LoptError):
             fwd(x, x, **kw)
+
+
+@pytest.mark.parametrize("gate", GATES)
+def test_the_stream_may_change_in_place_where_its_norm_is_left_out(gate):
+    """Without pre nothing of h is needed for the gradients, so h += ... is allowed; with it, it is an error."""
+    args = gpu(*make(20, 130, torch.float32, torch.float32, 61, gate, pre=False)[:6])
+    dh = torch.randn(20, 130, device="cuda")
+    leaves = [None if v is None else v.requires_grad_(True) for v in args]
+    have = [v for v in leaves if v is not None]
+    want = torch.autograd.grad(layers.residual_norm(*leaves, pre=False)[0], have, 3 * dh)
+    h, z = layers.residual_norm(*leaves, pre=False)
+    assert z is None
+    h.mul_(3.0).add_(1.0)
+    got = torch.autograd.grad(h, have, dh)
+    assert all(bool(((a - b).abs() <= 200 * U * (b.abs() + b.abs().max())).all()) for a, b in zip(got, want))
+    h, z = layers.residual_norm(*leaves)
+    h.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        torch.autograd.grad(z, have, dh)
