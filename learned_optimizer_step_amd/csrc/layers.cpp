@@ -300,7 +300,8 @@ struct ResidualParams {
     if (!o.post && !o.pre) bad("neither norm: post and pre are False");
     if (o.rms && (b1.defined() || b2.defined())) bad("an RMS norm has no bias");
     if (gate && gate->defined()) {
-      if (gate->dim() == 1 && y.dim() != 1) {
+      // of one row alone, a gate of y's own type is like y, one of another type a vector
+      if (gate->dim() == 1 && (y.dim() != 1 || gate->scalar_type() != y.scalar_type())) {
         row_gate = vector(gate, cols, device, "gate");
       } else {
         on(device, *gate, "gate");

@@ -349,3 +349,18 @@ def test_the_stream_may_change_in_place_where_its_norm_is_left_out(gate):
     h.add_(1.0)
     with pytest.raises(RuntimeError, match="modified by an inplace"):
         torch.autograd.grad(z, have, dh)
+
+
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16], ids=str)
+def test_one_row_without_a_dimension_for_it(t):
+    """x and y of one dimension: the same as with a dimension of one row, a gate vector of the weights' type among them."""
+    x, y, gate, w1, b1, w2, b2, dh, dz = gpu(*make(1, 96, t, torch.float32, 71, "vector"))
+    for given in (gate, gate.to(t).view(1, 96), None):
+        args = [None if v is None else v.clone().requires_grad_(True) for v in (x, y, given, w1, b1, w2, b2)]
+        flat = [args[k][0] if args[k] is not None and args[k].dim() == 2 else args[k] for k in range(7)]
+        h, z = layers.residual_norm(*args)
+        hf, zf = layers.residual_norm(*flat)
+        assert hf.shape == zf.shape == (96,) and torch.equal(h[0], hf) and torch.equal(z[0], zf)
+        have = [v for v in args if v is not None]
+        for a, b in zip(torch.autograd.grad([h, z], have, [dh, dz]), torch.autograd.grad([hf, zf], have, [dh[0], dz[0]])):
+            assert a.dtype == b.dtype and torch.equal(a, b)
