@@ -34,7 +34,7 @@ void with_residual_mode(int64_t n, F&& f) {
 
 // Moments of a row of which z, the norm of a rounded number, is the reader: a
 // last bit of it decides where a rounding falls, so the row's sums are added up
-// in 64 bits (a thread's 8 numbers in fp32), and its reciprocal root is the nearest float.
+// in 64 bits (up to 16 numbers of a thread in fp32), and its reciprocal root is the nearest float.
 __device__ __forceinline__ void residual_mean(Moments& m, double sum, double inv_n) {
   const double mu = sum * inv_n;
   m.mean = float(mu);

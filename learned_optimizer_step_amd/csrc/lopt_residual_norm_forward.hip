@@ -139,17 +139,18 @@ __global__ __launch_bounds__(1024) void k_residual_forward_long(ResidualForward 
       row_sum(sum);
       residual_mean(m, sum[0], inv_n);
     }
-    float part = 0.f;
+    double s2[1] = {0.0};   // a vector's squares in fp32, the vectors' in 64 bits
     for (int64_t c = threadIdx.x * V; c < n; c += 1024 * V) {
       const Pack<T, V> p = load_pack<T, V>(row, c, n);
+      float part = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (c + i < n) {
           const float d = to_f32(p.v[i]) - m.mean;
           part = fmaf(d, d, part);
         }
+      s2[0] += double(part);
     }
-    double s2[1] = {double(part)};
     row_sum(s2);
     residual_spread(m, s2[0], inv_n, a.eps);
     return m;

@@ -364,3 +364,20 @@ def test_one_row_without_a_dimension_for_it(t):
         have = [v for v in args if v is not None]
         for a, b in zip(torch.autograd.grad([h, z], have, [dh, dz]), torch.autograd.grad([hf, zf], have, [dh[0], dz[0]])):
             assert a.dtype == b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("c", [0.3, 0.9])
+@pytest.mark.parametrize("cols", [9000, 1 << 18, 1 << 22])
+def test_spreads_of_very_long_rows(cols, c):
+    """Squares of one size, whose roundings in a running fp32 sum would all go one way: at most a vector's 8 are added in fp32,
+    so the spread is within 8 U, and half of that and two roundings are left in rstd."""
+    for t in TYPES:
+        y = torch.full((2, cols), c, dtype=t)
+        y[:, ::2] *= -1
+        want = 1.0 / y[0, 1].double().item()
+        for rms in (False, True):
+            h, z, stats = layers.residual_norm_forward(y.cuda(), torch.zeros_like(y).cuda(), eps=0.0, rms=rms, post=False)
+            assert torch.equal(h.cpu(), y)
+            assert bool(((stats[3].double().cpu() - want).abs() <= 6 * U * want).all()), (t, rms, (stats[3].double().cpu() / want - 1) / U)
+            h, z, stats = layers.residual_norm_forward(torch.zeros_like(y).cuda(), y.cuda(), eps=0.0, rms=rms, pre=False)
+            assert bool(((stats[1].double().cpu() - want).abs() <= 6 * U * want).all()), (t, rms)
