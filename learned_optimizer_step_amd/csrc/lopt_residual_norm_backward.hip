@@ -3,7 +3,10 @@
 //   D  = dh + rstd2 (a - hh mean(a hh) - mean(a)),  a = dz w2     (RMS: without mean(a))
 //   dx = alpha D,  E = beta D,  dgate = E u,  du = E gate
 //   dy = rstd1 (b - yh mean(b yh) - mean(b)),  b = du w1         (or du)
-// and over the rows dw2 = sum dz hh, db2 = sum dz, dw1 = sum du yh, db1 = sum du
+// The means that the forward pass kept are floats; what they leave of a row far
+// from zero, in units of its spread, is the mean that (h - mean2) rstd2 still
+// has, and is taken off hh and yh.
+// And over the rows dw2 = sum dz hh, db2 = sum dz, dw1 = sum du yh, db1 = sum du
 // and a gate vector's sum of dgate.
 // Bound by HBM: dh, dz, y, h (and a gate matrix) are read once, dx and dy (and
 // the matrix's gradient) written once; a block's next row is loaded before the sums of this one.  Each thread adds up its columns'
@@ -19,13 +22,18 @@
 namespace lopt {
 namespace {
 
+// Whether a row lies farther from zero than it is wide.  In others half a step of the mean is below the roundings of
+// (x - mean) rstd themselves, and nothing is taken off (65536 x 2048 bf16, layer norm of y alone: 194 us, 202 with the sums taken
+// of every row, 191 without any; norms on both sides 346, 336 without).
+__device__ __forceinline__ bool is_far(float mean, float rstd) { return fabsf(mean) * rstd > 1.f; }
+
 enum : int { kW1 = 0, kB1 = 1, kW2 = 2, kB2 = 3, kGate = 4, kSums = 5 };   // of ResidualBackward::sums
 
 template <class T, class L, int MODE, bool RMS, bool POST, bool PRE>
 __global__ __launch_bounds__(L::BLOCK) void k_residual_backward(ResidualBackward a) {
   constexpr int V = kVec<T>, NV = L::E / V, E = L::E;
-  __shared__ float red[2][L::TPR > 64 ? L::TPR / 64 : 1][2];
-  RowSum<L::TPR, 2> row_sum{red};
+  __shared__ float red[2][L::TPR > 64 ? L::TPR / 64 : 1][2], red_left[2][L::TPR > 64 ? L::TPR / 64 : 1][2];
+  RowSum<L::TPR, 2> row_sum{red}, left_sum{red_left};
   const int lane = threadIdx.x % L::TPR;
   const int n = int(a.cols);
   const float inv_n = 1.f / float(n);
@@ -76,21 +84,48 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_backward(ResidualBackward
 #pragma unroll
     for (int e = 0; e < E; ++e)
       if (!a.dh || !row) d[e] = 0.f;
-    if (PRE) {
-      float v[2] = {0.f, 0.f};
+    if (PRE)
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = k * V + i;
-          if (!a.dz || !row) dz[e] = 0.f;
-          h[e] = row && at[k].own(i) ? (h[e] - mean2) * rstd2 : 0.f;
-          sum[kW2][e] = fmaf(dz[e], h[e], sum[kW2][e]);
-          if (!RMS) sum[kB2][e] += dz[e];
-          dz[e] *= w2[e];
-          v[0] = fmaf(dz[e], h[e], v[0]);
-          v[1] += dz[e];
+        for (int i = 0; i < V; ++i) h[k * V + i] = row && at[k].own(i) ? (h[k * V + i] - mean2) * rstd2 : 0.f;
+    if (POST)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[k * V + i] = row && at[k].own(i) ? (y[k * V + i] - mean1) * rstd1 : 0.f;
+    if constexpr (!RMS) {
+      const bool far1 = POST && is_far(mean1, rstd1), far2 = PRE && is_far(mean2, rstd2);
+      if (far1 || far2) {   // the same for all threads of a row, and where a row's sum has a barrier a block has one row
+        float v[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (PRE) v[0] += h[e];
+          if (POST) v[1] += y[e];
         }
+        left_sum(v);
+        const float left2 = far2 ? v[0] * inv_n : 0.f, left1 = far1 ? v[1] * inv_n : 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (row && at[k].own(i)) {
+              if (PRE) h[k * V + i] -= left2;
+              if (POST) y[k * V + i] -= left1;
+            }
+      }
+    }
+    if (PRE) {
+      float v[2] = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (!a.dz || !row) dz[e] = 0.f;
+        sum[kW2][e] = fmaf(dz[e], h[e], sum[kW2][e]);
+        if (!RMS) sum[kB2][e] += dz[e];
+        dz[e] *= w2[e];
+        v[0] = fmaf(dz[e], h[e], v[0]);
+        v[1] += dz[e];
+      }
       row_sum(v);
       const float c1 = v[0] * inv_n, c2 = RMS ? 0.f : v[1] * inv_n;
 #pragma unroll
@@ -110,14 +145,6 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_backward(ResidualBackward
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) d[e] *= a.beta;
-    if (POST)
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = k * V + i;
-          y[e] = row && at[k].own(i) ? (y[e] - mean1) * rstd1 : 0.f;
-        }
     if (a.gate_kind != kNoGate) {
       float x[E];
 #pragma unroll
@@ -194,22 +221,23 @@ __global__ __launch_bounds__(L::BLOCK) void k_residual_backward(ResidualBackward
   }
 }
 
-// Rows longer than kLongestResidualRow: one block a row.  The row's two means of
-// the second norm's gradient stay in the workspace for the column sums.
+// Rows longer than kLongestResidualRow: one block a row.  Up to kLongBlocks rows, each leaves its columns' sums itself; of more,
+// the two means of the second norm's gradient and what the kept means leave stay in the workspace for the column sums.
+constexpr int64_t kLongBlocks = 64;
 struct LongRow {
-  float mean1, rstd1, mean2, rstd2, c1, c2;
+  float mean1, rstd1, mean2, rstd2, c1, c2, left1, left2;
 };
 template <class T>
 struct LongElement {   // column c of a row
   float hh, dz, d, u, yh, e, du;
   __device__ __forceinline__ LongElement(const ResidualBackward& a, const LongRow& m, int64_t r, int64_t c) {
     const auto param = [&](const void* p, float fill) { return p ? load_any(p, a.wdtype, c) : fill; };
-    hh = a.pre ? (to_f32(static_cast<const T*>(a.h)[r * a.ldh + c]) - m.mean2) * m.rstd2 : 0.f;
+    hh = a.pre ? (to_f32(static_cast<const T*>(a.h)[r * a.ldh + c]) - m.mean2) * m.rstd2 - m.left2 : 0.f;
     dz = a.pre && a.dz ? to_f32(static_cast<const T*>(a.dz)[r * a.lddz + c]) : 0.f;
     d = a.dh ? to_f32(static_cast<const T*>(a.dh)[r * a.lddh + c]) : 0.f;
     if (a.pre) d = fmaf(m.rstd2, dz * param(a.w2, 1.f) - fmaf(hh, m.c1, m.c2), d);
     const float y = to_f32(static_cast<const T*>(a.y)[r * a.ldy + c]);
-    yh = a.post ? (y - m.mean1) * m.rstd1 : 0.f;
+    yh = a.post ? (y - m.mean1) * m.rstd1 - m.left1 : 0.f;
     u = a.post ? fmaf(yh, param(a.w1, 1.f), param(a.b1, 0.f)) : y;
     e = a.beta * d;
     du = e * (a.gate_kind == kGateVector ? load_any(a.gate, a.wdtype, c)
@@ -225,6 +253,28 @@ __device__ __forceinline__ LongRow long_row(const ResidualBackward& a, int64_t r
   return m;
 }
 
+struct ColumnSums {   // of one column, over some rows
+  float sum[kSums] = {};
+  template <class T>
+  __device__ __forceinline__ void add(const LongElement<T>& x) {
+    sum[kW1] = fmaf(x.du, x.yh, sum[kW1]);
+    sum[kB1] += x.du;
+    sum[kW2] = fmaf(x.dz, x.hh, sum[kW2]);
+    sum[kB2] += x.dz;
+    sum[kGate] = fmaf(x.e, x.u, sum[kGate]);
+  }
+  // those that are wanted, one behind the other
+  __device__ __forceinline__ void store(const ResidualBackward& a, int64_t block, int64_t c) const {
+    float* out = a.part + size_t(block) * size_t(kSums) * size_t(a.cols) + c;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k)
+      if (a.sums[k]) {
+        *out = sum[k];
+        out += a.cols;
+      }
+  }
+};
+
 template <class T>
 __global__ __launch_bounds__(1024) void k_residual_backward_long(ResidualBackward a, float* means) {
   __shared__ float red[2][16][2];
@@ -233,6 +283,17 @@ __global__ __launch_bounds__(1024) void k_residual_backward_long(ResidualBackwar
   const float inv_n = 1.f / float(n);
   for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     LongRow m = long_row(a, r);
+    const bool far1 = !a.rms && a.post && is_far(m.mean1, m.rstd1), far2 = !a.rms && a.pre && is_far(m.mean2, m.rstd2);
+    if (far1 || far2) {
+      float v[2] = {0.f, 0.f};
+      for (int64_t c = threadIdx.x; c < n; c += 1024) {
+        if (far2) v[0] += to_f32(static_cast<const T*>(a.h)[r * a.ldh + c]) - m.mean2;
+        if (far1) v[1] += to_f32(static_cast<const T*>(a.y)[r * a.ldy + c]) - m.mean1;
+      }
+      row_sum(v);
+      if (far2) m.left2 = v[0] * inv_n * m.rstd2;
+      if (far1) m.left1 = v[1] * inv_n * m.rstd1;
+    }
     if (a.pre) {
       float v[2] = {0.f, 0.f};
       for (int64_t c = threadIdx.x; c < n; c += 1024) {
@@ -246,12 +307,19 @@ __global__ __launch_bounds__(1024) void k_residual_backward_long(ResidualBackwar
       m.c2 = a.rms ? 0.f : v[1] * inv_n;
     }
     if (means && threadIdx.x == 0) {
-      means[2 * r] = m.c1;
-      means[2 * r + 1] = m.c2;
+      means[4 * r] = m.c1;
+      means[4 * r + 1] = m.c2;
+      means[4 * r + 2] = m.left1;
+      means[4 * r + 3] = m.left2;
     }
     float v[2] = {0.f, 0.f};
     for (int64_t c = threadIdx.x; c < n; c += 1024) {
       const LongElement<T> x(a, m, r, c);
+      if (a.part && !means) {
+        ColumnSums s;
+        s.add(x);
+        s.store(a, r, c);
+      }
       if (a.dx) static_cast<T*>(a.dx)[r * a.lddx + c] = from_f32<T>(a.alpha * x.d);
       if (a.gate_kind == kGateMatrix && a.dgate) static_cast<T*>(a.dgate)[r * a.lddg + c] = from_f32<T>(x.e * x.u);
       if (a.post) {
@@ -273,30 +341,21 @@ __global__ __launch_bounds__(1024) void k_residual_backward_long(ResidualBackwar
   }
 }
 
-// Column sums over every gridDim.y-th row.
+// Column sums over every gridDim.y-th row; means: four floats a row.
 template <class T>
 __global__ __launch_bounds__(256) void k_residual_columns_long(ResidualBackward a, const float* means) {
   const int64_t n = a.cols, c = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (c >= n) return;
-  float sum[kSums] = {};
+  ColumnSums s;
   for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
     LongRow m = long_row(a, r);
-    m.c1 = means[2 * r];
-    m.c2 = means[2 * r + 1];
-    const LongElement<T> x(a, m, r, c);
-    sum[kW1] = fmaf(x.du, x.yh, sum[kW1]);
-    sum[kB1] += x.du;
-    sum[kW2] = fmaf(x.dz, x.hh, sum[kW2]);
-    sum[kB2] += x.dz;
-    sum[kGate] = fmaf(x.e, x.u, sum[kGate]);
+    m.c1 = means[4 * r];
+    m.c2 = means[4 * r + 1];
+    m.left1 = means[4 * r + 2];
+    m.left2 = means[4 * r + 3];
+    s.add(LongElement<T>(a, m, r, c));
   }
-  float* out = a.part + size_t(blockIdx.y) * size_t(kSums) * size_t(n) + c;
-#pragma unroll
-  for (int k = 0; k < kSums; ++k)
-    if (a.sums[k]) {
-      *out = sum[k];
-      out += n;
-    }
+  s.store(a, blockIdx.y, c);
 }
 
 // The parameters' gradients from the blocks' sums: 32 columns a block at a time, 32
@@ -339,7 +398,7 @@ __global__ __launch_bounds__(1024) void k_residual_join(ResidualBackward a, int6
 
 int64_t backward_blocks(int64_t rows, int64_t cols) {
   if (rows <= 0) return 0;
-  if (cols > kLongestResidualRow) return std::min<int64_t>(rows, 64);
+  if (cols > kLongestResidualRow) return std::min<int64_t>(rows, kLongBlocks);
   return with_residual_layout(cols, [&](auto l) {
     using L = decltype(l);
     // two rounds of rows a block (fewer sums to join) once every compute unit has a block, and no more blocks than are resident
@@ -352,8 +411,13 @@ int64_t backward_blocks(int64_t rows, int64_t cols) {
 }  // namespace
 
 size_t residual_backward_bytes(int64_t rows, int64_t cols) {
-  const size_t means = cols > kLongestResidualRow ? size_t(rows) * 2 * sizeof(float) : 0;
-  return size_t(backward_blocks(rows, cols)) * size_t(kSums) * size_t(cols) * sizeof(float) + means;
+  const size_t sums = size_t(kSums) * size_t(cols) * sizeof(float);   // of a block
+  size_t bytes = size_t(backward_blocks(rows, cols)) * sums;
+  if (cols > kLongestResidualRow) {   // four floats a row, two of them in the room of whole blocks' sums
+    const size_t half = size_t(rows) * 2 * sizeof(float);
+    bytes += half + (rows > kLongBlocks ? (half + sums - 1) / sums * sums : 0);
+  }
+  return bytes;
 }
 
 hipError_t launch_residual_backward(const ResidualBackward& args, hipStream_t s) {
@@ -366,9 +430,9 @@ hipError_t launch_residual_backward(const ResidualBackward& args, hipStream_t s)
     const hipError_t e = with_type(a.dtype, [&](auto t) {
       using T = decltype(t);
       if (a.cols > kLongestResidualRow) {
-        float* means = a.part ? a.part + size_t(blocks) * size_t(kSums) * size_t(a.cols) : nullptr;
+        float* means = a.part && a.rows > kLongBlocks ? a.part + size_t(blocks) * size_t(kSums) * size_t(a.cols) : nullptr;
         k_residual_backward_long<T><<<dim3(unsigned(std::min<int64_t>(a.rows, 4096))), dim3(1024), 0, s>>>(a, means);
-        if (a.part) k_residual_columns_long<T><<<dim3(unsigned((a.cols + 255) / 256), unsigned(blocks)), dim3(256), 0, s>>>(a, means);
+        if (means) k_residual_columns_long<T><<<dim3(unsigned((a.cols + 255) / 256), unsigned(blocks)), dim3(256), 0, s>>>(a, means);
         return hipGetLastError();
       }
       return with_residual_layout(a.cols, [&](auto l) {

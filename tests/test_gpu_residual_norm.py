@@ -11,8 +11,8 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import CODE, TYPES, U, close, norm_forward, norm_forward_tols  # noqa: E402
-from residual_cases import backward, bound, update  # noqa: E402
+from ops_cases import CODE, TYPES, U, close, depth, norm_forward, norm_forward_tols  # noqa: E402
+from residual_cases import backward, bound, sums_depth, update  # noqa: E402
 
 # one row to thousands; every row layout with its first and last width, widths that no vector divides, rows too long for registers
 SHAPES = [(1, 1), (3, 2), (1, 768), (5, 7), (1000, 8), (67, 64), (130, 65), (33, 197), (9, 512), (6, 513), (2049, 768), (70, 1000),
@@ -381,3 +381,76 @@ def test_spreads_of_very_long_rows(cols, c):
             assert bool(((stats[3].double().cpu() - want).abs() <= 6 * U * want).all()), (t, rms, (stats[3].double().cpu() / want - 1) / U)
             h, z, stats = layers.residual_norm_forward(torch.zeros_like(y).cuda(), y.cuda(), eps=0.0, rms=rms, pre=False)
             assert bool(((stats[1].double().cpu() - want).abs() <= 6 * U * want).all()), (t, rms)
+
+
+def gradients64(dh, dz, y, h, gate, w1, b1, w2, eps, post, pre):
+    """{name: (gradient, bound before the last rounding)} of layer norms with the statistics that the rows have in 64 bits.  A
+    normalised number is off by k, which is what a sum of its row's is off by (the mean's, taken out again in the backward pass, and
+    the spread's), and each row's two means with it."""
+    cols, k, ks = y.shape[1], (2 * depth(y.shape[1]) + 12) * U, sums_depth(y.shape[0]) * U
+    m = lambda v: v.mean(1, keepdim=True)  # noqa: E731
+
+    def norm(x, d, td, w):
+        """(normalised, gradient of x, its bound) under a gradient d that is off by td"""
+        x, w = x.double(), torch.ones(cols, dtype=torch.float64) if w is None else w.double()
+        c = x - m(x)
+        r = (m(c * c) + eps).rsqrt()
+        xh, a, ta = c * r, d * w, td * w.abs() + U * (d * w).abs()
+        own = a.abs() + xh.abs() * m((a * xh).abs()) + m(a.abs()) + m((a * xh).abs()) + xh.abs() * m(a.abs())
+        return xh, r * (a - xh * m(a * xh) - m(a)), r * (k * own + ta + xh.abs() * m(ta * xh.abs()) + m(ta))
+
+    out = {}
+    D, tD = dh.double(), U * dh.double().abs()
+    if pre:
+        z = dz.double()
+        hh, d, td = norm(h, z, 0.0 * z, w2)
+        out["weight"] = ((z * hh).sum(0), (ks * (z * hh).abs() + k * z.abs()).sum(0))
+        out["bias"] = (z.sum(0), ks * z.abs().sum(0))
+        D, tD = D + d, tD + td + U * d.abs()
+    out["x"] = (D, tD)
+    one = torch.ones(cols, dtype=torch.float64)
+    g = one if gate is None else gate.double()
+    du, tdu = D * g, tD * g.abs() + U * (D * g).abs()
+    u, tu = y.double(), torch.zeros_like(D)
+    if post:
+        W, B = (one if v is None else v.double() for v in (w1, b1))
+        yh, dy, tdy = norm(y, du, tdu, w1)
+        u, tu = yh * W + B, k * W.abs() + 4 * U * ((yh * W).abs() + B.abs())
+        out["post_weight"] = ((du * yh).sum(0), (tdu * yh.abs() + k * du.abs() + ks * (du * yh).abs()).sum(0))
+        out["post_bias"] = (du.sum(0), (tdu + ks * du.abs()).sum(0))
+        du, tdu = dy, tdy
+    out["y"] = (du, tdu)
+    if gate is not None:
+        dg, tg = D * u, tD * u.abs() + D.abs() * tu + U * (D * u).abs()
+        out["gate"] = (dg, tg) if gate.dim() == 2 else (dg.sum(0), (tg + ks * dg.abs()).sum(0))
+    return out
+
+
+@pytest.mark.parametrize("norms", range(3), ids=lambda k: "post" * NORMS[k][0] + "pre" * NORMS[k][1])
+@pytest.mark.parametrize("rows,cols", [(9, 7), (130, 24), (67, 64), (5, 300), (9, 768), (300, 1000), (5, 2048), (4, 4096), (6, 5000), (3, 8192), (2, 9000), (64, 8193), (65, 8200), (200, 9001)])
+def test_gradients_of_rows_far_from_zero(rows, cols, norms):
+    """Rows up to some 10^6 spreads from zero, whose mean a float does not hold: gradients of the update's definition, with the rows'
+    own statistics and not those that were kept."""
+    post, pre = NORMS[norms]
+    eps = 1e-12
+    for k, gate in enumerate(GATES):
+        g = torch.Generator().manual_seed(cols + rows + k)
+        x, y, gt, w1, b1, w2, b2, dh, dz = make(rows, cols, torch.float32, torch.float32, cols + k, gate, post, pre)
+        far = torch.tensor([0.0, 3.0, 41.7, 4097.3, 30011.9, -777.7])[torch.randint(0, 6, (rows, 1), generator=g)]
+        near = 0.05 * (0.5 + torch.rand(rows, 1, generator=g))
+        x, y = near * x + (far if pre else 0.0), near * y + far
+        t = torch.float16 if k == 2 and cols > 64 else torch.float32
+        if t == torch.float16:       # a few elements a step of fp16 away from the others
+            y = far.expand(rows, cols).clone() + 4 * (torch.rand(rows, cols, generator=g) < 0.02) + 0.01 * y
+            x, y, gt, dh, dz = (v.to(t) for v in (x, y, gt, dh, dz))
+        a = gpu(x, y, gt, w1, b1, w2, b2)
+        h, z, stats = layers.residual_norm_forward(*a, eps, post=post, pre=pre)
+        gdh, gdz = gpu(dh, dz)
+        got = dict(zip(NAMES, layers.residual_norm_backward(gdh, gdz if pre else None, a[1], h if pre else None, stats, a[2], a[3], a[4], a[5], post=post, pre=pre)))
+        for name, (want, tol) in gradients64(dh, dz, y, h.cpu(), gt, w1, b1, w2, eps, post, pre).items():
+            ty = t if got[name].dim() == 2 else torch.float32
+            tol = bound(want, tol, ty)
+            if ty == torch.float16:   # of 65520 and more nothing but infinity is kept (a row of equal numbers has a deviation of 10^-6); up to the bound, either
+                over = (want.abs() >= 65520 + tol) | (want.abs() >= 65520 - tol) & torch.isinf(got[name].cpu())
+                want = torch.where(over, want.sign() * math.inf, want)
+            close(got[name], want, tol, f"{rows}x{cols} {gate} grad of {name}")
