@@ -584,7 +584,8 @@ lopt_status lopt_distill_backward(int64_t rows, int64_t cols, int32_t dtype, con
 /* Cross entropy of a linear layer's logits, without the logits in memory.  For each
  * row of x (rows x cols), with the layer's weight w (vocab x cols), both of type dtype, and a target t:
  *   z = x w^T,  lse = log sum_v exp(z_v),  loss = lse - z_t;
- * a row whose target lies outside [0, vocab) (an id to ignore) has loss 0.  Products of 16-bit elements
+ * a row whose target lies outside [0, vocab) (an id to ignore) has loss 0.  A logit of +infinity, as one that is no number, makes
+ * its row's lse and loss NaN; one of -infinity counts as nothing.  Products of 16-bit elements
  * are exact and added in fp32.  targets: rows signed integers of id_bytes (4 or 8) bytes.  loss, lse: rows floats,
  * NULL: not written.  At most 2^24 rows and 2^20 columns, vocab at most 2^30 - 64, and
  * vocab / 256 * rows / 256 (rounded up) below 2^23. */
@@ -599,7 +600,7 @@ lopt_status lopt_linear_ce_backward_workspace(int64_t rows, int64_t cols, int64_
 
 /* Gradients of lopt_linear_ce_forward: with G = dloss (exp(z - lse) - onehot(t)), 0 for a row to ignore,
  *   dx = G w,  dw = G^T x.
- * G is rounded to type dtype (for fp16 scaled by a power of two first, so that its smallest steps are 2^-35 of the largest
+ * G is rounded to type dtype (for fp16 scaled by a power of two first, so that its smallest steps are at most 2^-34 of the largest
  * |dloss|); its sums are fp32.  A row to ignore is not read: whatever x holds there, its gradient is 0 and dw does not see it.
  * exp(z - lse) is off by the rounding of lse to fp32, a relative 2^-24 |lse| that a row's entries share, and by that of small differences.
  * dloss: one float a row, dloss_stride apart (0: one value for all rows).  lse: as lopt_linear_ce_forward wrote it.  dx: rows x

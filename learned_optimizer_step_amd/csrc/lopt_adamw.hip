@@ -3,8 +3,8 @@
 //   p <- p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
 // Bound by HBM: p, m and v are read and written once, g is read once (fp32: 28
 // bytes an element with 32-bit moments, 16.1 with 8-bit ones).  ViT-B/16 with 32-bit moments:
-// 408 us, 5.9 TB/s; GPT-2 355M with 8-bit ones 958, 6.0; 92.6M bf16 elements with 8-bit ones
-// 290, 3.2: the codes' arithmetic and the ends of 13 launches.
+// 408 us, 5.9 TB/s; GPT-2 355M with 8-bit ones 1028 (median of its kernels' trace; at best 958), 5.6; 92.6M bf16 elements
+// with 8-bit ones 294 (283), 3.2: the codes' arithmetic and the ends of 13 launches.
 //
 // The list travels as a kernel argument, kMaxAdamw tensors a launch: nothing is
 // uploaded, so gradients may lie elsewhere at every step, and a captured launch

@@ -7,8 +7,8 @@
 // product again, its tiles ending in G, which is kept for the piece alone, and
 // from it the piece's share of dx and its rows of dw.  Bound by the matrix
 // units: 2 N V D operations forward, 6 N V D backward.  bf16: forward 8192 tokens of
-// 32000 x 2048 835 us (1286 TFLOP/s; the library's plain product of that size takes 901),
-// both passes 4096 of 50257 x 1024 1680 to 1745 us (1004 to 966 TFLOP/s; the library's
+// 32000 x 2048 814 to 930 us (1320 to 1155 TFLOP/s, on several cards and in a trace; the library's plain product of that size takes 901),
+// both passes 4096 of 50257 x 1024 1680 to 1755 us (1004 to 961 TFLOP/s; the library's
 // plain product of that size reaches 866).
 #include <hip/hip_runtime.h>
 
@@ -448,7 +448,7 @@ __global__ __launch_bounds__(1024) void k_ce_rows(int64_t n, int64_t vocab, cons
   const int64_t run = ((n + 1023) / 1024 + gridDim.x - 1) / gridDim.x * 1024, begin = blockIdx.x * run, end = min(begin + run, n);
   if (begin >= n) return;
   float scale = 1.f;
-  if (scaled) {   // |G| up to 2^11: fp16's smallest steps are then 2^-35 of the largest gradient
+  if (scaled) {   // |G| up to 2^11: fp16's smallest steps are then 2^-35 to 2^-34 of the largest gradient
     float top = 0.f;
     for (int64_t r0 = threadIdx.x; r0 < n; r0 += 1024 * 8) {
 #pragma unroll

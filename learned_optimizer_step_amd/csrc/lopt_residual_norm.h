@@ -11,7 +11,8 @@ constexpr int64_t kLongestResidualRow = 8192;
 // Calls f(RowLayout) for the layout that holds rows of n columns: 8 elements a
 // thread, as up to eight vectors of parameters and sums stay in registers beside
 // a row's four and the next one's.  The widest rows take 16, as 1024 threads
-// would leave 128 registers each (4096 x 8192 bf16, layer norms, backward: 343 us, 230 so).
+// would leave 128 registers each.  Neither has room for all of it: with 16 the backward kernels of two norms keep up to 436
+// bytes of a thread in scratch memory (4096 x 8192 bf16, layer norms, backward: 203 us, 343 with 1024 threads; its bytes take 63).
 template <class F>
 auto with_residual_layout(int64_t n, F&& f) {
   if (n <= 64) return f(RowLayout<8, 8, 256>());     // eight rows in a wave

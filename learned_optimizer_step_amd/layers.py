@@ -179,7 +179,7 @@ def linear_ce_forward(x, weight, targets):
     that logarithm, for ``linear_ce_backward``.
 
     x: targets.shape + (D,); weight: (V, D), of x's type.  A target outside the vocabulary (say -1 or -100) is ignored:
-    its loss and gradient are 0."""
+    its loss and gradient are 0.  A logit of +infinity or NaN makes its row's loss and lse NaN."""
     return _C.linear_ce_forward(x, weight, targets)
 
 

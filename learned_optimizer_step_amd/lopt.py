@@ -697,7 +697,10 @@ class AdamW(_torch_optimizer_base()):
     """AdamW as a ``torch.optim.Optimizer`` over device parameters (fp32, bf16 or fp16), moments in 32 bits or in 8.
 
     Each ``step()`` is one ``lopt_adamw_step`` over every parameter, with the gradients in ``p.grad``; a parameter whose
-    ``grad`` is None is skipped, and the count of steps, which all parameters share, goes on.  ``lr`` and
+    ``grad`` is None is skipped, and the count of steps, which all parameters share, goes on: a gradient that comes first
+    after many steps is corrected by their number, and moves its parameter by up to (1 - beta1) / sqrt(1 - beta2) lr, 3.2 with
+    the defaults, where a first step moves it by lr.  With ``state_bits=8`` an infinite or NaN gradient, or a finite one whose square is
+    infinite, makes the moments of its block of 256 elements NaN for good.  A parameter needs at least one element.  ``lr`` and
     ``weight_decay`` are read from the parameter groups at every step, so ``torch.optim.lr_scheduler`` schedules drive
     them; ``betas`` and ``eps`` are the whole optimizer's.  With ``state_bits=8`` the moments take 2.06 bytes an element
     instead of 8; their codes are rounded at random, from ``seed``.  The count is on the device, so a step can be

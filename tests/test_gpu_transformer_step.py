@@ -14,6 +14,7 @@ from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
 from learned_optimizer_step_amd import workloads as W  # noqa: E402
 from ops_cases import U  # noqa: E402
+from test_gpu_adamw import fp32_codes  # noqa: E402
 
 VOCAB, DIM, TOKENS, BETA = 311, 96, 150, 0.7
 NAMES = ("wte", "norm0", "w1", "post1", "gate1", "norm1", "w2", "post2", "norm2", "head")
@@ -177,3 +178,20 @@ def test_gradients_into_the_same_buffers_of_two_batches():
         layers.linear_ce_backward(dl[part], z[part], head, targets[part], lse[part], grad_weight=buf, accumulate=True)
     # sums of the same terms in another order
     assert bool(((buf - want).abs() <= 400 * U * (want.abs() + want.abs().max())).all())
+
+
+def test_steps_of_adamw_with_8_bit_moments():
+    """Training steps through autograd: codes of the fp32 moments and their random bits, and the parameters they move."""
+    ps = [p.cuda().requires_grad_(True) for p in parameters()]
+    opt = L.AdamW(ps, lr=1e-2, weight_decay=0.1, state_bits=8, seed=2)
+    for t in (1, 2, 3):
+        ids, targets = (v.cuda() for v in data(t))
+        opt.zero_grad()
+        run(ps, ids, targets).backward()
+        before = [(as_numpy(p).reshape(-1).copy(), as_numpy(s).copy()) for p, s in zip(ps, opt.states)]
+        opt.step()
+        for k, (p, (old, state)) in enumerate(zip(ps, before)):
+            m, v, new = fp32_codes(as_numpy(p.grad).reshape(-1), state, 2, t, k)
+            assert (as_numpy(opt.states[k]) == new).all(), (t, NAMES[k])
+            want, update = step_param(old, m.reshape(-1)[:p.numel()], v.reshape(-1)[:p.numel()], opt.betas, opt.eps, 1e-2, 0.1, t)
+            assert (abs(as_numpy(p).reshape(-1) - want) <= U * (4 * abs(old) + 16 * update) + 1e-12).all(), (t, NAMES[k])

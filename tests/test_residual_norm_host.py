@@ -78,3 +78,11 @@ def test_no_cpu_path():
                  lambda: layers.residual_norm_backward(x, x, x, x, torch.ones(4, 3))):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_room_for_long_rows():
+    """Rows over 8192 columns: five floats a column for each of up to 64 blocks, and, of more rows, four floats a row."""
+    for rows, cols in ((1, 8193), (64, 9000), (65, 8200), (20481, 8193), (1_000_000, 10_000)):
+        b = L.lopt_residual_norm_backward_workspace(rows, cols)
+        need = 20 * cols * min(rows, 64) + (16 * rows if rows > 64 else 0)
+        assert need <= b < need + 20 * cols + 8 * rows + 1, (rows, cols, b, need)
