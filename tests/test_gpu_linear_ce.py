@@ -11,7 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from linear_ce_cases import backward, forward, product_depth  # noqa: E402
+from linear_ce_cases import backward, forward  # noqa: E402
 from ops_cases import CODE, TYPES, U, close, rounding  # noqa: E402
 
 # (tokens, vocabulary, width): ones, tiles with their neighbours, widths that no stage divides, long vocabularies and many tokens
@@ -344,6 +344,7 @@ def test_refusals_of_the_tensors():
 def test_probabilities_under_a_large_common_offset():
     """fp32 logits that are exact, 500 to 4000 above 0: with lse as it is kept, a probability is off by the roundings of a small
     difference, however large lse is.  dx under a weight's column of ones is what a token's gradients add up to."""
+    from linear_ce_cases import product_depth
     n, vocab, dim = 200, 60, 48
     g = torch.Generator().manual_seed(16)
     x, w = torch.zeros(n, dim), torch.randint(-8, 9, (vocab, dim), generator=g) / 8.0

@@ -11,8 +11,8 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
-from ops_cases import CODE, TYPES, U, close, depth, norm_forward, norm_forward_tols  # noqa: E402
-from residual_cases import backward, bound, sums_depth, update  # noqa: E402
+from ops_cases import CODE, TYPES, U, close, norm_forward, norm_forward_tols  # noqa: E402
+from residual_cases import backward, bound, update  # noqa: E402
 
 # one row to thousands; every row layout with its first and last width, widths that no vector divides, rows too long for registers
 SHAPES = [(1, 1), (3, 2), (1, 768), (5, 7), (1000, 8), (67, 64), (130, 65), (33, 197), (9, 512), (6, 513), (2049, 768), (70, 1000),
@@ -387,6 +387,7 @@ def gradients64(dh, dz, y, h, gate, w1, b1, w2, eps, post, pre):
     """{name: (gradient, bound before the last rounding)} of layer norms with the statistics that the rows have in 64 bits.  A
     normalised number is off by k, which is what a sum of its row's is off by (the mean's, taken out again in the backward pass, and
     the spread's), and each row's two means with it."""
+    from residual_cases import depth, sums_depth
     cols, k, ks = y.shape[1], (2 * depth(y.shape[1]) + 12) * U, sums_depth(y.shape[0]) * U
     m = lambda v: v.mean(1, keepdim=True)  # noqa: E731
 

@@ -14,7 +14,6 @@ from learned_optimizer_step_amd import layers  # noqa: E402
 from learned_optimizer_step_amd import lopt as L  # noqa: E402
 from learned_optimizer_step_amd import workloads as W  # noqa: E402
 from ops_cases import U  # noqa: E402
-from test_gpu_adamw import fp32_codes  # noqa: E402
 
 VOCAB, DIM, TOKENS, BETA = 311, 96, 150, 0.7
 NAMES = ("wte", "norm0", "w1", "post1", "gate1", "norm1", "w2", "post2", "norm2", "head")
@@ -182,6 +181,7 @@ def test_gradients_into_the_same_buffers_of_two_batches():
 
 def test_steps_of_adamw_with_8_bit_moments():
     """Training steps through autograd: codes of the fp32 moments and their random bits, and the parameters they move."""
+    from test_gpu_adamw import fp32_codes
     ps = [p.cuda().requires_grad_(True) for p in parameters()]
     opt = L.AdamW(ps, lr=1e-2, weight_decay=0.1, state_bits=8, seed=2)
     for t in (1, 2, 3):
